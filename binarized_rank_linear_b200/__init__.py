@@ -14,6 +14,7 @@ Build the library with ``python -m binarized_rank_linear_b200.build``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -68,7 +69,35 @@ class LbProjection(ctypes.Structure):
                 ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
 
 
+class LbAdapters(ctypes.Structure):
+    """``lb_adapters`` (include/lb.h): the adapter pool of one projection."""
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("ranks", ctypes.c_void_p),
+                ("count", ctypes.c_int64), ("rank", ctypes.c_int64)]
+
+
+class LbAdapterProjection(ctypes.Structure):
+    """``lb_adapter_projection`` (include/lb.h): one projection of an adapters call."""
+    _fields_ = [("n_out", ctypes.c_int64), ("adapters", ctypes.POINTER(LbAdapters)), ("base", ctypes.c_void_p),
+                ("ldbase", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
+
+
+class LbHeads(ctypes.Structure):
+    """``lb_heads`` (include/lb.h): one tensor of heads."""
+    _fields_ = [("heads", ctypes.c_int64), ("in_", ctypes.c_void_p), ("ld_in", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64)]
+
+
+class LbHeadsGrad(ctypes.Structure):
+    """``lb_heads_grad`` (include/lb.h): one tensor of heads and its gradients."""
+    _fields_ = [("heads", ctypes.c_int64), ("in_", ctypes.c_void_p), ("ld_in", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("dout", ctypes.c_void_p), ("ld_dout", ctypes.c_int64),
+                ("din", ctypes.c_void_p), ("ld_din", ctypes.c_int64), ("dweight", ctypes.c_void_p)]
+
+
 MAX_SIBLINGS = 4
+MAX_ADAPTERS = 1024
+MAX_ADAPTER_RANK = 128
+ROTATE_HALVES, ROTATE_PAIRS = 0, 1
 
 
 def lib() -> ctypes.CDLL:
@@ -117,6 +146,23 @@ def lib() -> ctypes.CDLL:
             L.lb_linear_backward.restype = i32
             L.lb_linear_backward.argtypes = [vp, vp, i64, i64, i64, i64, i64, ctypes.POINTER(LbPath),
                                              ctypes.POINTER(LbPath), vp, i64, vp, vp, vp, vp, sz, vp]
+            L.lb_adapters_workspace_bytes.restype = sz
+            L.lb_adapters_workspace_bytes.argtypes = [i64, i64, i32, ctypes.POINTER(LbAdapterProjection)]
+            L.lb_adapters_forward.restype = i32
+            L.lb_adapters_forward.argtypes = [vp, i64, i64, i64, vp, i32, ctypes.POINTER(LbAdapterProjection), vp, sz, vp]
+            L.lb_adapters_backward_workspace_bytes.restype = sz
+            L.lb_adapters_backward_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+            L.lb_adapters_backward.restype = i32
+            L.lb_adapters_backward.argtypes = [vp, vp, i64, i64, i64, i64, i64, vp, ctypes.POINTER(LbAdapters), vp, i64,
+                                               vp, i64, vp, vp, vp, sz, vp]
+            f32 = ctypes.c_float
+            L.lb_heads_norm_rotate.restype = i32
+            L.lb_heads_norm_rotate.argtypes = [i64, i64, i64, i32, vp, vp, f32, i32, ctypes.POINTER(LbHeads), vp]
+            L.lb_heads_backward_workspace_bytes.restype = sz
+            L.lb_heads_backward_workspace_bytes.argtypes = [i64]
+            L.lb_heads_norm_rotate_backward.restype = i32
+            L.lb_heads_norm_rotate_backward.argtypes = [i64, i64, i64, i32, vp, vp, f32, i32,
+                                                        ctypes.POINTER(LbHeadsGrad), vp, sz, vp]
             L.lb_device_status.restype = i32
             L.lb_device_status.argtypes = [vp, ctypes.POINTER(i32)]
             L.lb_debug_inject_stall.restype = i32
@@ -315,10 +361,18 @@ def siblings_workspace_bytes(tokens: int, n_in: int, layers) -> int:
     return int(lib().lb_siblings_workspace_bytes(tokens, n_in, len(layers), arr))
 
 
-def linear_forward_siblings(x, layers, ys=None, workspace=None, stream=None):
+def linear_forward_siblings(x, layers, ys=None, workspace=None, stream=None, adapters=None, ids=None, rotation=None,
+                            positions=None, rotate=None):
     """``lb_linear_forward_siblings``: several layers that read the same x,
     given as [(main, residual or None), ...]; returns their outputs (bf16
-    [tokens, n_out_j]), allocated with torch when not given."""
+    [tokens, n_out_j]), allocated with torch when not given.
+
+    With ``adapters`` (one :class:`AdapterPool` or None per layer) and ``ids``
+    each token's adapter is added to the outputs (:func:`adapters_forward`).
+    With ``rotation`` (a :class:`HeadRotation`) and ``positions`` the outputs
+    named by ``rotate``, a dict from the layer's index to its norm weight (or
+    None for no norm), then get their heads normed and rotated
+    (:func:`heads_norm_rotate`): an attention block's queries and keys."""
     torch = _torch()
     _require(x, "x", torch.bfloat16)
     tokens, n_in = x.shape
@@ -326,6 +380,10 @@ def linear_forward_siblings(x, layers, ys=None, workspace=None, stream=None):
         ys = [torch.empty((tokens, main.h.shape[0]), dtype=torch.bfloat16, device=x.device) for main, _ in layers]
     for j, y in enumerate(ys):
         _require(y, f"ys[{j}]", torch.bfloat16)
+    if adapters is not None and (len(adapters) != len(layers) or ids is None):
+        raise ValueError("adapters must name a pool or None for each layer, and ids each token's adapter")
+    if rotation is not None and (positions is None or not rotate or not all(0 <= j < len(layers) for j in rotate)):
+        raise ValueError("rotation needs positions and, in rotate, the layers whose outputs are rotated")
     arr, _keep = _projections(layers, ys)
     need = int(lib().lb_siblings_workspace_bytes(tokens, n_in, len(layers), arr))
     if workspace is None:
@@ -334,6 +392,14 @@ def linear_forward_siblings(x, layers, ys=None, workspace=None, stream=None):
     _check(lib().lb_linear_forward_siblings(
         x.data_ptr(), tokens, n_in, x.stride(0), len(layers), arr, workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream_handle(stream)), "lb_linear_forward_siblings")
+    if adapters is not None:
+        some = [j for j, pool in enumerate(adapters) if pool is not None]
+        if some:
+            adapters_forward(x, ids, [adapters[j] for j in some], ys=[ys[j] for j in some], stream=stream)
+    if rotation is not None:
+        which = sorted(rotate)
+        heads_norm_rotate([ys[j] for j in which], positions, rotation, weights=[rotate[j] for j in which],
+                          outs=[ys[j] for j in which], stream=stream)
     return ys
 
 
@@ -429,13 +495,16 @@ def backward_workspace_bytes(tokens: int, n_in: int, n_out: int, rank_main: int,
 
 
 def linear_backward(x, dy, main: PackedPath, residual: PackedPath | None = None, dx=None, want_dx: bool = True,
-                    workspace=None, stream=None) -> dict:
+                    workspace=None, stream=None, adapters: "AdapterPool | None" = None, ids=None) -> dict:
     """``lb_linear_backward``: the gradients of a loss with respect to the
     layer's input and scale vectors, given ``dy`` = dL/dy (bf16 [tokens,
     n_out]) and the forward input ``x`` (bf16 [tokens, n_in]).  Returns
     ``{"dx": bf16 [tokens, n_in] or None, "dh": fp32 [paths, n_out], "dg":
     fp32 [paths, n_in], "dl": fp32 [r_main + r_residual]}``; outputs and the
-    workspace are allocated with torch when not given."""
+    workspace are allocated with torch when not given.  With ``adapters`` and
+    ``ids`` (the layer ran with a pool beside it) dx includes the adapters'
+    part, and their gradients "da" and "db" are returned too
+    (:func:`adapters_backward`)."""
     torch = _torch()
     _require(x, "x", torch.bfloat16)
     _require(dy, "dy", torch.bfloat16)
@@ -464,7 +533,350 @@ def linear_backward(x, dy, main: PackedPath, residual: PackedPath | None = None,
         dx.stride(0) if dx is not None else n_in, dh.data_ptr(), dg.data_ptr(), dl.data_ptr(),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(stream)),
         "lb_linear_backward")
-    return {"dx": dx, "dh": dh, "dg": dg, "dl": dl}
+    out = {"dx": dx, "dh": dh, "dg": dg, "dl": dl}
+    if adapters is not None:
+        more = adapters_backward(x, dy, ids, adapters, dx=dx, want_dx=dx is not None, stream=stream)
+        out["da"], out["db"] = more["da"], more["db"]
+    return out
+
+
+# ------------------------------------------------------------------ adapters
+
+def _require_rows(t, name: str, rows: int, cols: int, dtype, device) -> int:
+    """Checks a [rows, cols] tensor of an adapters or heads call and that it
+    lives on `device`; returns its row stride in elements."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit inner stride, got strides {t.stride()}")
+    return ld if rows > 1 else cols
+
+
+def _require_vector(t, name: str, n: int, dtype, device) -> None:
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{n}] tensor, got shape {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _current(t, name: str):
+    """The device of `t`, which must be the current one: the library launches there."""
+    device = t.device
+    if device.type != "cuda":
+        raise ValueError(f"{name} must be in device memory")
+    if device.index != _torch().cuda.current_device():
+        raise ValueError(f"{name} is on {device}, which is not the current device")
+    return device
+
+
+def _held(t, stream):
+    """Keeps memory that torch gave on the current stream from being handed out
+    again before `stream` is done with it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+@dataclass(frozen=True)
+class AdapterPool:
+    """The adapters of one projection, on the device: ``a`` bf16 [count, rank,
+    n_in], ``b`` bf16 [count, n_out, rank], ``scale`` fp32 [count] or None for
+    1, ``ranks`` int32 [count] or None for ``rank`` each (``lb_adapters``)."""
+    a: object
+    b: object
+    scale: object = None
+    ranks: object = None
+
+    def as_c(self) -> LbAdapters:
+        """The lb_adapters struct of this pool, built once (the fields are
+        frozen and a tensor's storage does not move)."""
+        c = self.__dict__.get("_c")
+        if c is None:
+            torch = _torch()
+            for name in ("a", "b"):
+                t = getattr(self, name)
+                if t.dtype != torch.bfloat16:
+                    raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+                if t.dim() != 3 or not t.is_contiguous() or not t.is_cuda:
+                    raise ValueError(f"{name} must be a contiguous 3-D device tensor")
+            count, rank, n_in = self.a.shape
+            if self.b.shape[0] != count or self.b.shape[2] != rank:
+                raise ValueError(f"b must be [{count}, n_out, {rank}], got {tuple(self.b.shape)}")
+            if self.b.device != self.a.device:
+                raise ValueError("a and b must be on one device")
+            if self.scale is not None:
+                _require_vector(self.scale, "scale", count, torch.float32, self.a.device)
+            if self.ranks is not None:
+                _require_vector(self.ranks, "ranks", count, torch.int32, self.a.device)
+            c = LbAdapters(self.a.data_ptr(), self.b.data_ptr(),
+                           self.scale.data_ptr() if self.scale is not None else None,
+                           self.ranks.data_ptr() if self.ranks is not None else None, count, rank)
+            object.__setattr__(self, "_c", c)
+            object.__setattr__(self, "_p", ctypes.pointer(c))
+            object.__setattr__(self, "n_in", n_in)
+            object.__setattr__(self, "n_out", self.b.shape[1])
+            object.__setattr__(self, "device", self.a.device)
+        return c
+
+
+@functools.lru_cache(maxsize=4096)
+def adapters_workspace_bytes(tokens: int, n_in: int, count: int, ranks: tuple) -> int:
+    """``lb_adapters_workspace_bytes`` for pools of ``count`` adapters of the given stored ranks."""
+    arr = (LbAdapterProjection * max(1, len(ranks)))()
+    for j, r in enumerate(ranks):
+        arr[j].n_out = 32
+        arr[j].adapters = ctypes.pointer(LbAdapters(None, None, None, None, count, r))
+    return int(lib().lb_adapters_workspace_bytes(tokens, n_in, len(ranks), arr))
+
+
+def adapters_forward(x, ids, pools, bases=None, ys=None, workspace=None, stream=None):
+    """``lb_adapters_forward``: ``y_j = base_j + s_i B_ij (A_ij x)`` per token,
+    i = ids[token], for every pool j of ``pools`` (projections of one x).
+    ``ids`` int32 [tokens] on the device, negative for no adapter.  ``bases``
+    and ``ys`` are lists of bf16 [tokens, n_out_j]: without ``bases`` the
+    ``ys`` are updated in place, without ``ys`` they are allocated.  Returns
+    ``ys``."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    device = _current(x, "x")
+    _require(x, "x", bf16)
+    tokens, n_in = x.shape
+    _require_vector(ids, "ids", tokens, torch.int32, device)
+    n = len(pools)
+    if not 1 <= n <= MAX_SIBLINGS:
+        raise ValueError(f"1 to {MAX_SIBLINGS} pools, got {n}")
+    if bases is None and ys is None:
+        raise ValueError("give bases, or ys to update in place")
+    if (bases is not None and len(bases) != n) or (ys is not None and len(ys) != n):
+        raise ValueError(f"bases and ys must have one tensor for each of the {n} pools")
+    arr = (LbAdapterProjection * n)()
+    made = []
+    for j, pool in enumerate(pools):
+        pool.as_c()
+        if pool.n_in != n_in or pool.device != device:
+            raise ValueError(f"pools[{j}] has n_in = {pool.n_in} on {pool.device}, x {n_in} on {device}")
+        n_out, e = pool.n_out, arr[j]
+        e.n_out = n_out
+        e.adapters = pool._p
+        if ys is None:
+            y = _held(torch.empty((tokens, n_out), dtype=bf16, device=device), stream)
+            made.append(y)
+            e.ldy = n_out
+        else:
+            y = ys[j]
+            e.ldy = _require_rows(y, f"ys[{j}]", tokens, n_out, bf16, device)
+        e.y = y.data_ptr()
+        if bases is not None:
+            e.ldbase = _require_rows(bases[j], f"bases[{j}]", tokens, n_out, bf16, device)
+            e.base = bases[j].data_ptr()
+    if workspace is None:
+        need = adapters_workspace_bytes(tokens, n_in, pools[0]._c.count, tuple([p._c.rank for p in pools]))
+        workspace = _held(torch.empty(max(need, 16), dtype=torch.uint8, device=device), stream)
+    else:
+        _require_workspace(workspace)
+    _check(lib().lb_adapters_forward(
+        x.data_ptr(), tokens, n_in, x.stride(0) if tokens > 1 else n_in, ids.data_ptr(), n, arr, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream)), "lb_adapters_forward")
+    return made if ys is None else ys
+
+
+def adapters_backward_workspace_bytes(tokens: int, n_in: int, n_out: int, count: int, rank: int) -> int:
+    return int(lib().lb_adapters_backward_workspace_bytes(tokens, n_in, n_out, count, rank))
+
+
+def adapters_backward(x, dy, ids, pool: AdapterPool, dx_base=None, dx=None, want_dx: bool = True, da=None, db=None,
+                      workspace=None, stream=None) -> dict:
+    """``lb_adapters_backward``: the gradients of a loss with respect to a
+    pool's matrices and to x, given ``dy`` = dL/dy (bf16 [tokens, n_out]) and
+    the forward x and ids.  ``dx_base`` is the layer's own dx, to which the
+    adapters' part is added; without it ``dx`` is updated in place.  Returns
+    ``{"dx": bf16 [tokens, n_in] or None, "da": fp32 [count, rank, n_in],
+    "db": fp32 [count, n_out, rank]}``, allocated with torch when not given."""
+    torch = _torch()
+    bf16, f32 = torch.bfloat16, torch.float32
+    device = _current(x, "x")
+    _require(x, "x", bf16)
+    c = pool.as_c()
+    tokens, n_in = x.shape
+    n_out = pool.n_out
+    if pool.n_in != n_in or pool.device != device:
+        raise ValueError(f"pool has n_in = {pool.n_in} on {pool.device}, x {n_in} on {device}")
+    lddy = _require_rows(dy, "dy", tokens, n_out, bf16, device)
+    _require_vector(ids, "ids", tokens, torch.int32, device)
+    if want_dx and dx is None:
+        if dx_base is None:
+            raise ValueError("give dx_base, or dx to update in place, or want_dx=False")
+        dx = _held(torch.empty((tokens, n_in), dtype=bf16, device=device), stream)
+    if not want_dx:
+        dx = None
+    lddx = _require_rows(dx, "dx", tokens, n_in, bf16, device) if dx is not None else n_in
+    with_base = dx is not None and dx_base is not None
+    ldbase = _require_rows(dx_base, "dx_base", tokens, n_in, bf16, device) if with_base else n_in
+    for name, t, shape in (("da", da, (c.count, c.rank, n_in)), ("db", db, (c.count, n_out, c.rank))):
+        if t is not None and (t.dtype != f32 or t.shape != shape or not t.is_contiguous() or t.device != device):
+            raise ValueError(f"{name} must be a contiguous {shape} float32 tensor on {device}")
+    if da is None:
+        da = _held(torch.empty((c.count, c.rank, n_in), dtype=f32, device=device), stream)
+    if db is None:
+        db = _held(torch.empty((c.count, n_out, c.rank), dtype=f32, device=device), stream)
+    if workspace is None:
+        need = adapters_backward_workspace_bytes(tokens, n_in, n_out, c.count, c.rank)
+        workspace = _held(torch.empty(max(need, 16), dtype=torch.uint8, device=device), stream)
+    else:
+        _require_workspace(workspace)
+    _check(lib().lb_adapters_backward(
+        x.data_ptr(), dy.data_ptr(), tokens, n_in, n_out, x.stride(0) if tokens > 1 else n_in, lddy, ids.data_ptr(),
+        pool._p, dx_base.data_ptr() if with_base else None, ldbase, dx.data_ptr() if dx is not None else None, lddx,
+        da.data_ptr(), db.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream_handle(stream)), "lb_adapters_backward")
+    return {"dx": dx, "da": da, "db": db}
+
+
+# ------------------------------------------------------------------ heads
+
+@dataclass(frozen=True)
+class HeadRotation:
+    """What a model's blocks share of the per-head norm and rotation: the head
+    size, the rotation's frequencies ``inv_freq`` (fp32 [rotary_dim / 2] on the
+    device, or None for a norm alone), which elements form a pair
+    (``"halves"``: k and k + rotary_dim / 2, or ``"pairs"``: 2k and 2k + 1) and
+    the norm's eps."""
+    head_dim: int
+    inv_freq: object = None
+    rotation: str = "halves"
+    eps: float = 1e-6
+
+    def __post_init__(self):
+        torch = _torch()
+        if self.rotation not in ("halves", "pairs"):
+            raise ValueError(f"rotation must be 'halves' or 'pairs', got {self.rotation!r}")
+        f = self.inv_freq
+        if f is not None and (f.dtype != torch.float32 or f.dim() != 1 or not f.is_contiguous() or not f.is_cuda):
+            raise ValueError("inv_freq must be a contiguous 1-D float32 device tensor")
+        object.__setattr__(self, "rotary_dim", 2 * f.shape[0] if f is not None else 0)
+        object.__setattr__(self, "code", ROTATE_HALVES if self.rotation == "halves" else ROTATE_PAIRS)
+
+
+def _heads_call(tensors, positions, rotation: HeadRotation, weights, name: str):
+    """Checks what both heads calls share; returns (device, tokens, positions' address, frequencies' address)."""
+    torch = _torch()
+    n = len(tensors)
+    if not 1 <= n <= MAX_SIBLINGS:
+        raise ValueError(f"1 to {MAX_SIBLINGS} tensors, got {n}")
+    if weights is not None and len(weights) != n:
+        raise ValueError(f"weights must have one entry for each of the {n} tensors")
+    device = _current(tensors[0], f"{name}[0]")
+    tokens = tensors[0].shape[0]
+    if rotation.rotary_dim == 0:
+        return device, tokens, None, None
+    _require_vector(positions, "positions", tokens, torch.int32, device)
+    if rotation.inv_freq.device != device:
+        raise ValueError(f"inv_freq must be on {device}, got {rotation.inv_freq.device}")
+    return device, tokens, positions.data_ptr(), rotation.inv_freq.data_ptr()
+
+
+def _heads_of(t, name: str, head_dim: int) -> int:
+    if t.dim() != 2 or head_dim < 1 or t.shape[1] % head_dim:
+        raise ValueError(f"{name} must be [tokens, heads * {head_dim}], got {tuple(t.shape)}")
+    return t.shape[1] // head_dim
+
+
+def heads_norm_rotate(tensors, positions, rotation: HeadRotation, weights=None, outs=None, stream=None):
+    """``lb_heads_norm_rotate``: the RMS norm of each head (where ``weights``
+    has a bf16 [head_dim] weight for the tensor) and the rotation by
+    ``positions`` (int32 [tokens] on the device), for up to 4 tensors bf16
+    [tokens, heads * head_dim].  ``outs`` may be the tensors themselves; they
+    are allocated when not given.  Returns them."""
+    torch = _torch()
+    bf16, d = torch.bfloat16, rotation.head_dim
+    device, tokens, pos, freq = _heads_call(tensors, positions, rotation, weights, "tensors")
+    if outs is not None and len(outs) != len(tensors):
+        raise ValueError(f"outs must have one entry for each of the {len(tensors)} tensors")
+    arr = (LbHeads * len(tensors))()
+    made = []
+    for j, t in enumerate(tensors):
+        e = arr[j]
+        e.heads = _heads_of(t, f"tensors[{j}]", d)
+        cols = t.shape[1]
+        e.ld_in = _require_rows(t, f"tensors[{j}]", tokens, cols, bf16, device)
+        e.in_ = t.data_ptr()
+        if outs is None:
+            o = _held(torch.empty((tokens, cols), dtype=bf16, device=device), stream)
+            made.append(o)
+            e.ld_out = cols
+        else:
+            o = outs[j]
+            e.ld_out = _require_rows(o, f"outs[{j}]", tokens, cols, bf16, device)
+        e.out = o.data_ptr()
+        if weights is not None and weights[j] is not None:
+            _require_vector(weights[j], f"weights[{j}]", d, bf16, device)
+            e.weight = weights[j].data_ptr()
+    _check(lib().lb_heads_norm_rotate(tokens, d, rotation.rotary_dim, rotation.code, pos, freq, rotation.eps,
+                                      len(tensors), arr, _stream_handle(stream)), "lb_heads_norm_rotate")
+    return made if outs is None else outs
+
+
+def heads_backward_workspace_bytes(head_dim: int) -> int:
+    return int(lib().lb_heads_backward_workspace_bytes(head_dim))
+
+
+def heads_norm_rotate_backward(tensors, douts, positions, rotation: HeadRotation, weights=None, dins=None,
+                               want_dweight: bool = True, workspace=None, stream=None) -> list:
+    """``lb_heads_norm_rotate_backward``: the gradients of a loss given
+    ``douts`` = dL/dout and the forward call's inputs ``tensors``.  Returns a
+    dict for each tensor: ``{"din": bf16 [tokens, heads * head_dim]}``, and
+    where it has a norm weight (and ``want_dweight``) ``"dweight": fp32
+    [head_dim]``.  ``dins`` may be the douts or the tensors; outputs and the
+    workspace are allocated with torch when not given."""
+    torch = _torch()
+    bf16, d = torch.bfloat16, rotation.head_dim
+    device, tokens, pos, freq = _heads_call(tensors, positions, rotation, weights, "tensors")
+    n = len(tensors)
+    if len(douts) != n or (dins is not None and len(dins) != n):
+        raise ValueError(f"douts and dins must have one entry for each of the {n} tensors")
+    arr = (LbHeadsGrad * n)()
+    out = []
+    sums = False
+    for j, t in enumerate(tensors):
+        e = arr[j]
+        e.heads = _heads_of(t, f"tensors[{j}]", d)
+        cols = t.shape[1]
+        e.ld_in = _require_rows(t, f"tensors[{j}]", tokens, cols, bf16, device)
+        e.in_ = t.data_ptr()
+        e.ld_dout = _require_rows(douts[j], f"douts[{j}]", tokens, cols, bf16, device)
+        e.dout = douts[j].data_ptr()
+        if dins is None:
+            din = _held(torch.empty((tokens, cols), dtype=bf16, device=device), stream)
+            e.ld_din = cols
+        else:
+            din = dins[j]
+            e.ld_din = _require_rows(din, f"dins[{j}]", tokens, cols, bf16, device)
+        e.din = din.data_ptr()
+        out.append({"din": din})
+        if weights is not None and weights[j] is not None:
+            _require_vector(weights[j], f"weights[{j}]", d, bf16, device)
+            e.weight = weights[j].data_ptr()
+            if want_dweight:
+                dw = _held(torch.empty((d,), dtype=torch.float32, device=device), stream)
+                e.dweight = dw.data_ptr()
+                out[j]["dweight"] = dw
+                sums = True
+    if workspace is None:
+        workspace = _held(torch.empty(max(heads_backward_workspace_bytes(d), 16) if sums else 16, dtype=torch.uint8,
+                                      device=device), stream)
+    else:
+        _require_workspace(workspace)
+    _check(lib().lb_heads_norm_rotate_backward(tokens, d, rotation.rotary_dim, rotation.code, pos, freq, rotation.eps, n,
+                                               arr, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                               _stream_handle(stream)), "lb_heads_norm_rotate_backward")
+    return out
 
 
 def device_status(stream=None) -> int:
@@ -493,7 +905,9 @@ def set_prefill_pairs(enable: bool) -> None:
 class LittleBitLinear:
     """A deployed LittleBit layer: one or two packed paths on the device.
 
-    ``layer(x)`` runs ``lb_linear_forward`` on the current stream."""
+    ``layer(x)`` runs ``lb_linear_forward`` on the current stream;
+    ``layer(x, adapters=pool, ids=ids)`` adds each token's low-rank adapter
+    (:func:`adapters_forward`)."""
 
     def __init__(self, main: PackedPath, residual: PackedPath | None = None):
         self.main, self.residual = main, residual
@@ -519,6 +933,11 @@ class LittleBitLinear:
             self._ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
         return self._ws
 
-    def __call__(self, x, y=None, stream=None):
-        return linear_forward(x, self.main, self.residual, y=y,
-                              workspace=self.workspace(x.shape[0], x.device), stream=stream)
+    def __call__(self, x, y=None, stream=None, adapters: AdapterPool | None = None, ids=None):
+        if adapters is not None and ids is None:
+            raise ValueError("adapters need ids, each token's adapter")
+        y = linear_forward(x, self.main, self.residual, y=y,
+                           workspace=self.workspace(x.shape[0], x.device), stream=stream)
+        if adapters is not None:
+            adapters_forward(x, ids, [adapters], ys=[y], stream=stream)
+        return y

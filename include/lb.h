@@ -332,6 +332,153 @@ LB_API lb_status lb_linear_backward(const uint16_t *x, const uint16_t *dy, int64
                                     const lb_path *residual, uint16_t *dx, int64_t lddx, float *dh, float *dg,
                                     float *dl, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------- adapters
+ * Low-rank adapters of many requests beside a shared projection.  A batch's
+ * tokens share the projection's factors, and each token may have an adapter
+ * of its own (a pair of thin matrices A_i [r_i x n_in], B_i [n_out x r_i] with
+ * a scale s_i, trained beside the frozen layer) out of a pool that is resident
+ * on the device:
+ *     y[m] = base[m] + s_i B_i (A_i x[m]),   i = ids[m],
+ * base being the projection's output (lb_linear_forward and its relatives).
+ * The pages have no counterpart; this is a service of this library.
+ *
+ * lb_adapters: the pool of one projection.
+ *   a      : bf16 [count x rank x n_in], dense: adapter i's rows A_i first
+ *   b      : bf16 [count x n_out x rank], dense: row o holds B_i[o, 0 .. rank)
+ *   scale  : fp32 [count], or NULL for 1
+ *   ranks  : int32 [count], the rank r_i of each adapter (values outside 0 ..
+ *            rank count as the nearer end), or NULL for `rank` each.  A rank
+ *            of 0 is an adapter without effect.  What a and b store past r_i
+ *            does not change results, but must be finite.
+ *   count  : adapters, 1 .. LB_MAX_ADAPTERS
+ *   rank   : stored rank, a multiple of 8 up to LB_MAX_ADAPTER_RANK
+ * ids    : int32 [tokens] on the device, in any order.  A negative id is a
+ *          token without an adapter: its y is base to the bit.  An id of
+ *          `count` or more counts as none too, and LB_ERR_INVALID_ARGUMENT is
+ *          raised on the device status word.  ids is read on the device, so a
+ *          captured call may be replayed with new ids.
+ *
+ * lb_adapters_forward: up to LB_MAX_SIBLINGS projections of one x (a call for
+ *   one layer is a group of one), each with its own pool; their counts must
+ *   be equal.
+ *   base, ldbase : bf16 [tokens x n_out], or NULL: y itself is read and
+ *                  updated in place.  base may be y; it must not overlap it
+ *                  in another way.  The outputs must not overlap each other,
+ *                  x or the workspace.
+ * Numerics: products accumulate in fp32; A_i x is kept in fp32, or beyond
+ *   LB_ADAPTERS_SMALL_TOKENS tokens as the sum of two bf16 (16 bits and the
+ *   sign); base is added in fp32 and y rounded to bf16 once.  Every sum runs
+ *   in a fixed order: results are deterministic.  A token's result does not
+ *   depend on the other tokens' values (an infinity or NaN stays in its row).
+ * lb_adapters_backward: for one projection, given dy = dL/dy,
+ *     dA_i = s_i sum_m (B_i^T dy[m]) x[m]^T,   dB_i = s_i sum_m dy[m] (A_i x[m])^T,
+ *     dx[m] = dx_base[m] + s_i A_i^T (B_i^T dy[m]),
+ *   the sums over the tokens m with ids[m] = i.
+ *   da : fp32 [count x rank x n_in], db : fp32 [count x n_out x rank]; all of
+ *        both is written: zeros past an adapter's rank and for adapters that
+ *        no token uses.
+ *   dx_base, lddxbase : as base above (the layer's own dx; NULL: dx itself).
+ *   dx : bf16 [tokens x n_in], or NULL for none.
+ *   Numerics: B_i^T dy and A_i x travel as the sum of two bf16 each; fp32
+ *   accumulation in a fixed order.  tokens == 0 sets da and db to zero.
+ * Shapes, alignment and strides as lb_linear_forward, at most 2^20 tokens; a,
+ *   b, da and db 16-byte aligned, ids, scale and ranks 4-byte aligned.  No token is a no-op for
+ *   the forward call.  The workspace as there: its contents on entry do not
+ *   matter, and calls that share it must be ordered on one stream.
+ * Errors as lb_linear_forward. */
+#define LB_MAX_ADAPTERS 1024
+#define LB_MAX_ADAPTER_RANK 128
+#define LB_ADAPTERS_SMALL_TOKENS 128
+typedef struct {
+    const uint16_t *a;
+    const uint16_t *b;
+    const float *scale;
+    const int32_t *ranks;
+    int64_t count;
+    int64_t rank;
+} lb_adapters;
+typedef struct {
+    int64_t n_out;
+    const lb_adapters *adapters;
+    const uint16_t *base;
+    int64_t ldbase;
+    uint16_t *y;
+    int64_t ldy;
+} lb_adapter_projection;
+
+/* Workspace of lb_adapters_forward (the pools' count and rank and n_out are
+ * read, no pointer); 0 on a bad argument. */
+LB_API size_t lb_adapters_workspace_bytes(int64_t tokens, int64_t n_in, int nproj, const lb_adapter_projection *proj);
+LB_API lb_status lb_adapters_forward(const uint16_t *x, int64_t tokens, int64_t n_in, int64_t ldx, const int32_t *ids,
+                                     int nproj, const lb_adapter_projection *proj, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+LB_API size_t lb_adapters_backward_workspace_bytes(int64_t tokens, int64_t n_in, int64_t n_out, int64_t count,
+                                                   int64_t rank);
+LB_API lb_status lb_adapters_backward(const uint16_t *x, const uint16_t *dy, int64_t tokens, int64_t n_in,
+                                      int64_t n_out, int64_t ldx, int64_t lddy, const int32_t *ids,
+                                      const lb_adapters *adapters, const uint16_t *dx_base, int64_t lddxbase,
+                                      uint16_t *dx, int64_t lddx, float *da, float *db, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------- heads
+ * What a decoder block does with its projected queries and keys before
+ * attention: an RMS norm over each head (Qwen3's blocks; others have none) and
+ * the rotation by position, in one pass over up to LB_MAX_SIBLINGS tensors (a
+ * sibling group's outputs).  The pages have no counterpart; this is a service
+ * of this library.  For a head x [d] of a token at position p:
+ *     n = weight (.) x / sqrt(mean(x^2) + eps)   (n = x where weight is NULL)
+ *     out_a = n_a cos t - n_b sin t,  out_b = n_b cos t + n_a sin t,
+ *     t = p inv_freq[k],  k = 0 .. rotary_dim / 2 - 1,
+ *   over the pairs (a, b) = (k, k + rotary_dim / 2) with LB_ROTATE_HALVES, or
+ *   (2 k, 2 k + 1) with LB_ROTATE_PAIRS; elements from rotary_dim on are n.
+ * lb_heads: one tensor.
+ *   in, out : bf16 [tokens x heads * head_dim], row strides ld_in and ld_out;
+ *             out may be in, and must not overlap any input in another way
+ *   weight  : bf16 [head_dim], or NULL for no norm
+ * positions : int32 [tokens], any values; inv_freq : fp32 [rotary_dim / 2]
+ *             (both on the device; unused and possibly NULL when rotary_dim
+ *             is 0)
+ * Numerics: the angle's product and its reduction in 64 bits, everything else
+ *   in fp32; out is rounded to bf16 once.
+ * lb_heads_norm_rotate_backward: given dout = dL/dout and the forward input
+ *   `in` (not needed without a weight), din (may be dout or in) and, beside a
+ *   weight, dweight fp32 [head_dim] (or NULL for none) summed over tokens and
+ *   heads in a fixed order.  tokens == 0 sets dweight to zero.  The workspace
+ *   is needed where a dweight is asked for.
+ * Shapes: head_dim a multiple of 8 up to 256, rotary_dim a multiple of 8 from 0
+ *   to head_dim, heads >= 1 and at most 4096 in all, eps >= 0 and finite.  ld multiples of
+ *   8, bf16 tensors and the workspace 16-byte aligned, the rest 4-byte.
+ * Errors as lb_linear_forward. */
+typedef enum { LB_ROTATE_HALVES = 0, LB_ROTATE_PAIRS = 1 } lb_rotation;
+typedef struct {
+    int64_t heads;
+    const uint16_t *in;
+    int64_t ld_in;
+    const uint16_t *weight;
+    uint16_t *out;
+    int64_t ld_out;
+} lb_heads;
+typedef struct {
+    int64_t heads;
+    const uint16_t *in;
+    int64_t ld_in;
+    const uint16_t *weight;
+    const uint16_t *dout;
+    int64_t ld_dout;
+    uint16_t *din;
+    int64_t ld_din;
+    float *dweight;
+} lb_heads_grad;
+LB_API lb_status lb_heads_norm_rotate(int64_t tokens, int64_t head_dim, int64_t rotary_dim, lb_rotation rotation,
+                                      const int32_t *positions, const float *inv_freq, float eps, int ntensors,
+                                      const lb_heads *tensors, void *stream);
+/* 0 on a bad argument. */
+LB_API size_t lb_heads_backward_workspace_bytes(int64_t head_dim);
+LB_API lb_status lb_heads_norm_rotate_backward(int64_t tokens, int64_t head_dim, int64_t rotary_dim,
+                                               lb_rotation rotation, const int32_t *positions, const float *inv_freq,
+                                               float eps, int ntensors, const lb_heads_grad *tensors, void *workspace,
+                                               size_t workspace_bytes, void *stream);
+
 /* ---------------------------------------------------------- fixed scratch
  * lb_linear_forward_fixed_scratch: lb_linear_forward for 1..32 tokens with
  * no workspace argument.  The pages have no counterpart; this is a service of
