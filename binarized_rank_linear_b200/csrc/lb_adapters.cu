@@ -32,7 +32,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kGroup = 8;       // tokens of one adapter that a CTA takes together
 constexpr int kStep = 256;      // columns of A a warp reads at once (16 bytes a lane)
 constexpr int kMaxSteps = 4;    // steps of a shrink CTA's slice
-constexpr int kBatch = kThreads;  // tokens a launch pair serves: one thread each looks for its adapter
+static_assert(kAdapterSmallTokens <= kThreads, "one thread for each token looks for its adapter");
 
 struct SmallParams {
     const uint16_t *x;
@@ -279,12 +279,13 @@ cudaError_t launch_pdl(K kernel, dim3 grid, const SmallParams &p, cudaStream_t s
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-cudaError_t small_adapters(const AdaptersArgs &a, const DeviceInfo &dev, cudaStream_t stream, int m0, int M)
+cudaError_t small_adapters(const AdaptersArgs &a, const DeviceInfo &dev, cudaStream_t stream)
 {
+    const int M = a.tokens;
     SmallParams p{};
-    p.x = a.x + (int64_t)m0 * a.ldx;
+    p.x = a.x;
     p.ldx = a.ldx;
-    p.ids = a.ids + m0;
+    p.ids = a.ids;
     p.tokens = M;
     p.n_in = a.n_in;
     p.count = a.count;
@@ -295,8 +296,6 @@ cudaError_t small_adapters(const AdaptersArgs &a, const DeviceInfo &dev, cudaStr
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     for (int j = 0; j < a.nproj; ++j) {
         p.proj[j] = a.proj[j];
-        p.proj[j].base += (int64_t)m0 * a.proj[j].ldbase;
-        p.proj[j].y += (int64_t)m0 * a.proj[j].ldy;
         p.part[j] = reinterpret_cast<float *>(ws);
         ws += align256(sizeof(float) * (size_t)p.slices * (size_t)M * (size_t)a.proj[j].rank);
         p.chunk0[j + 1] = p.chunk0[j] + (a.proj[j].n_out + kThreads - 1) / kThreads;
@@ -314,126 +313,29 @@ size_t small_workspace(int M, int n_in, int nproj, const int *ranks)
     return b;
 }
 
-// ------------------------------------------------------------ backward, plain
-// grid (tokens): v = s A x and u = s B^T dy of one token, fp32 [tokens][rank] each.
-__global__ void __launch_bounds__(kThreads) plain_latent_kernel(const AdaptersBwdArgs b, float *v, float *u, int *status)
-{
-    __shared__ float red[kThreads];
-    pdl_wait();
-    const int m = blockIdx.x;
-    const int id = b.ids[m];
-    const bool use = id >= 0 && id < b.count;
-    if (id >= b.count && threadIdx.x == 0) set_status(status, LB_ERR_INVALID_ARGUMENT);
-    const int rank = !use ? 0 : b.ranks == nullptr ? b.rank : max(0, min(b.rank, b.ranks[id]));
-    const float s = use && b.scale != nullptr ? b.scale[id] : 1.0f;
-    for (int r = 0; r < b.rank; ++r) {
-        float sv = 0.0f, su = 0.0f;
-        if (r < rank) {
-            for (int i = threadIdx.x; i < b.n_in; i += kThreads)
-                sv += bf16_bits_to_float(b.a[((int64_t)id * b.rank + r) * b.n_in + i]) *
-                      bf16_bits_to_float(b.x[(int64_t)m * b.ldx + i]);
-            for (int o = threadIdx.x; o < b.n_out; o += kThreads)
-                su += bf16_bits_to_float(b.b[((int64_t)id * b.n_out + o) * b.rank + r]) *
-                      bf16_bits_to_float(b.dy[(int64_t)m * b.lddy + o]);
-        }
-        for (int which = 0; which < 2; ++which) {
-            __syncthreads();
-            red[threadIdx.x] = which ? su : sv;
-            __syncthreads();
-            for (int h = kThreads / 2; h > 0; h >>= 1) {
-                if ((int)threadIdx.x < h) red[threadIdx.x] += red[threadIdx.x + h];
-                __syncthreads();
-            }
-            if (threadIdx.x == 0) (which ? u : v)[(int64_t)m * b.rank + r] = s * red[0];
-        }
-    }
-}
-
-// grid (ceil(n_in / 256), tokens)
-__global__ void __launch_bounds__(kThreads) plain_dx_kernel(const AdaptersBwdArgs b, const float *u)
-{
-    pdl_wait();
-    const int m = blockIdx.y, i = blockIdx.x * kThreads + threadIdx.x;
-    if (i >= b.n_in) return;
-    const int id = b.ids[m];
-    const uint16_t base = b.dx_base[(int64_t)m * b.lddxbase + i];
-    const bool use = id >= 0 && id < b.count;
-    const int rank = !use ? 0 : b.ranks == nullptr ? b.rank : max(0, min(b.rank, b.ranks[id]));
-    float s = 0.0f;
-    for (int r = 0; r < rank; ++r)
-        s += u[(int64_t)m * b.rank + r] * bf16_bits_to_float(b.a[((int64_t)id * b.rank + r) * b.n_in + i]);
-    b.dx[(int64_t)m * b.lddx + i] = rank > 0 ? float_to_bf16_bits(bf16_bits_to_float(base) + s) : base;
-}
-
-// grid (ceil(max(n_in, n_out) / 256), rank, count): one thread per element of dA and one of dB
-__global__ void __launch_bounds__(kThreads) plain_grad_kernel(const AdaptersBwdArgs b, const float *v, const float *u)
-{
-    pdl_wait();
-    const int i = blockIdx.x * kThreads + threadIdx.x, r = blockIdx.y, id = blockIdx.z;
-    float ga = 0.0f, gb = 0.0f;
-    for (int m = 0; m < b.tokens; ++m) {
-        if (b.ids[m] != id) continue;
-        if (i < b.n_in) ga += u[(int64_t)m * b.rank + r] * bf16_bits_to_float(b.x[(int64_t)m * b.ldx + i]);
-        if (i < b.n_out) gb += v[(int64_t)m * b.rank + r] * bf16_bits_to_float(b.dy[(int64_t)m * b.lddy + i]);
-    }
-    const int rank = b.ranks == nullptr ? b.rank : max(0, min(b.rank, b.ranks[id]));
-    if (r >= rank) ga = gb = 0.0f;
-    if (i < b.n_in) b.da[((int64_t)id * b.rank + r) * b.n_in + i] = ga;
-    if (i < b.n_out) b.db[((int64_t)id * b.n_out + i) * b.rank + r] = gb;
-}
-
 }  // namespace
 
 size_t adapters_workspace_bytes(int tokens, int n_in, int count, int nproj, const int *ranks)
 {
-    (void)count;
-    size_t b = 0;  // the last batch may be smaller and take other slices
-    for (int m = std::min(tokens, kBatch); m > 0; m = tokens > kBatch && m == kBatch ? tokens % kBatch : 0)
-        b = std::max(b, small_workspace(m, n_in, nproj, ranks));
-    return b;
+    return tokens > kAdapterSmallTokens ? adapters_mma_workspace_bytes(tokens, count, nproj, ranks)
+                                        : small_workspace(tokens, n_in, nproj, ranks);
 }
 
-cudaError_t adapters_prepare_device(const DeviceInfo &dev)
-{
-    (void)dev;
-    return cudaSuccess;
-}
+cudaError_t adapters_prepare_device(const DeviceInfo &dev) { return adapters_mma_prepare_device(dev); }
 
 cudaError_t adapters_forward(const AdaptersArgs &a, const DeviceInfo &dev, cudaStream_t stream)
 {
-    for (int m0 = 0; m0 < a.tokens; m0 += kBatch) {
-        const cudaError_t e = small_adapters(a, dev, stream, m0, std::min(kBatch, a.tokens - m0));
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    return a.tokens > kAdapterSmallTokens ? adapters_mma_forward(a, dev, stream) : small_adapters(a, dev, stream);
 }
 
 size_t adapters_backward_workspace_bytes(int tokens, int n_in, int n_out, int count, int rank)
 {
-    (void)n_in, (void)n_out, (void)count;
-    return 2 * align256(sizeof(float) * (size_t)tokens * (size_t)rank);
+    return adapters_mma_backward_workspace_bytes(tokens, n_in, n_out, count, rank);
 }
 
 cudaError_t adapters_backward(const AdaptersBwdArgs &b, const DeviceInfo &dev, cudaStream_t stream)
 {
-    float *v = static_cast<float *>(b.workspace);
-    float *u = v + align256(sizeof(float) * (size_t)b.tokens * (size_t)b.rank) / sizeof(float);
-    plain_latent_kernel<<<(unsigned)b.tokens, kThreads, 0, stream>>>(b, v, u, dev.status);
-    if (b.dx != nullptr) {
-        for (int m0 = 0; m0 < b.tokens; m0 += 32768) {
-            AdaptersBwdArgs c = b;
-            c.ids += m0;
-            c.dx_base += (int64_t)m0 * b.lddxbase;
-            c.dx += (int64_t)m0 * b.lddx;
-            plain_dx_kernel<<<dim3((unsigned)((b.n_in + kThreads - 1) / kThreads),
-                                   (unsigned)std::min(32768, b.tokens - m0)),
-                              kThreads, 0, stream>>>(c, u + (int64_t)m0 * b.rank);
-        }
-    }
-    const int wide = std::max(b.n_in, b.n_out);
-    plain_grad_kernel<<<dim3((unsigned)((wide + kThreads - 1) / kThreads), (unsigned)b.rank, (unsigned)b.count), kThreads,
-                        0, stream>>>(b, v, u);
-    return cudaGetLastError();
+    return adapters_mma_backward(b, dev, stream);
 }
 
 }  // namespace lb
