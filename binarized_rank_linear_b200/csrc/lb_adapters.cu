@@ -328,9 +328,9 @@ cudaError_t adapters_forward(const AdaptersArgs &a, const DeviceInfo &dev, cudaS
     return a.tokens > kAdapterSmallTokens ? adapters_mma_forward(a, dev, stream) : small_adapters(a, dev, stream);
 }
 
-size_t adapters_backward_workspace_bytes(int tokens, int n_in, int n_out, int count, int rank)
+size_t adapters_backward_workspace_bytes(int tokens, int count, int rank)
 {
-    return adapters_mma_backward_workspace_bytes(tokens, n_in, n_out, count, rank);
+    return adapters_mma_backward_workspace_bytes(tokens, count, rank);
 }
 
 cudaError_t adapters_backward(const AdaptersBwdArgs &b, const DeviceInfo &dev, cudaStream_t stream)

@@ -14,15 +14,16 @@
 //           tiles of 128 slots, each of one adapter; a slot past an adapter's
 //           tokens holds the row number `tokens`, which no tensor has: TMA
 //           reads zeros there
-//   shrink  a tile's rows of x against A_i (or of dy against B_i): the rows come
-//           by TMA gather, K is split over a cluster of 1 to 8 CTAs, whose fp32
-//           sums meet through distributed shared memory in rank order; v is
+//   shrink  a tile's rows of x against A_i (or of dy against B_i), every CTA an
+//           equal share of all the tiles' K-blocks; the rows come by TMA; v is
 //           kept as a sum of bf16 (what a first one leaves goes to a second,
 //           and what that leaves to a third)
 //   expand  v against B_i (or A_i), 128 x 128 outputs at a time; base comes by
-//           TMA gather ahead of use, the sum goes back to its row
+//           TMA ahead of use, the sum goes back to its row
 //   wgrad   x^T u and dy^T v over an adapter's slots, both operands MN-major
-//           as they lie; long adapters in chunks whose parts are added in order
+//           as they lie, every CTA an equal share again
+//   finish  after shrink and wgrad: the products that fell to several CTAs,
+//           their fp32 sums added in the CTAs' order
 //
 // Two choices keep fp32 results fp32.  The tensor cores take bf16, so expand
 // multiplies the first two parts of v (2^-16 of v is lost, under a bf16 output
@@ -50,141 +51,180 @@ constexpr int kSegment = 4;           // K-blocks that are summed in tensor memo
 constexpr int kParts = 3;             // bf16 that v is the sum of
 
 // ------------------------------------------------------------ the plan
-struct Tile {
-    int adapter;  // -1: tokens without an adapter
-    int rows;     // slots in use, from 1 to TM
-};
-struct Chunk {  // a run of one adapter's tiles for wgrad
-    int adapter, tile0, slots;
-    int part;  // where its partial sums go, -1: straight to the gradient
-};
-struct Multi {  // an adapter of several chunks
-    int adapter, part0, parts;
+struct alignas(16) Tile {
+    int adapter;      // -1: tokens without an adapter
+    int rows;         // slots in use, from 1 to TM
+    int first;        // the first slot's token
+    int run;          // whether the others follow it one by one
 };
 struct Plan {
-    int *counts;  // tiles, chunks, adapters of several chunks
+    int *counts;   // tiles, those of adapters (the first ones), 64-slot blocks of adapters
     Tile *tiles;
-    int *perm;  // [tiles][TM]: the token of each slot, `tokens` for none
-    Chunk *chunks;
-    Multi *multi;
+    int *perm;     // [tiles][TM]: the token of each slot, `tokens` for none
+    int *block0;   // [count + 1]: blocks of the adapters before; each has ceil(its tokens / 64)
+    int *tile0;    // [count]: tiles of the adapters before
+    int *tokens;   // [count]: tokens of each adapter
 };
 
 struct PlanParams {
     const int32_t *ids;
     int tokens, count;
-    int chunk_tiles;  // tiles of a chunk; 0: no chunks wanted
     Plan plan;
     int *status;
 };
 
 constexpr int kPlanThreads = 1024, kPlanWarps = 32;
+constexpr int kHeld = 8192;  // tokens whose bins stay in shared memory between the two passes
+constexpr int kBlockTokens = 1 << 17, kLooseBits = 18;  // counts: whole blocks above 18 bits of other tokens
 
-// Exclusive sum over the block of one value per thread; `total` gets the sum.
-__device__ __forceinline__ int block_scan(int v, int *sums, int &total)
-{
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += n;
-    }
-    __syncthreads();
-    if (lane == 31) sums[w] = inc;
-    __syncthreads();
-    int before = 0;
-    total = 0;
-    for (int i = 0; i < kPlanWarps; ++i) {
-        const int s = sums[i];
-        if (i < w) before += s;
-        total += s;
-    }
-    return before + inc - v;
-}
-
-// Each warp takes a run of tokens in order, so that an adapter's tokens keep
-// their order and sums over them do not depend on timing.
+// Each warp takes a run of tokens in order, so that the slots of an adapter's
+// tokens, and with them its sums, do not depend on timing.  Of up to kBlockTokens tokens,
+// 32 neighbours (from a multiple of 32 on) of one adapter go to 32 slots
+// together, before the adapter's other tokens: prompts begin and end anywhere,
+// and a break inside a tile makes TMA gather its rows (one such tile held the
+// backward pass at 8192 tokens for 30 us).  One CTA runs this
+// once, so its instructions come from far away: the code is kept short (loops
+// stay rolled), which took 29 to 9 thousand cycles at 8192 tokens.  The ids
+// are read before the launch ahead is done; nothing is written before that.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
 {
     extern __shared__ int hist[];  // [warp][bin]; bin `count`: no adapter
-    __shared__ int sums[kPlanWarps], first_tile[LB_MAX_ADAPTERS + 1];
+    __shared__ unsigned long long sums[kPlanWarps];
+    __shared__ int first_tile[LB_MAX_ADAPTERS + 1], total[LB_MAX_ADAPTERS + 1], whole[LB_MAX_ADAPTERS + 1];
+    __shared__ int16_t held[kHeld];
     const int bins = p.count + 1, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    for (int i = tid; i < kPlanWarps * bins; i += kPlanThreads) hist[i] = 0;
-    pdl_wait();
-    pdl_launch_dependents();
-    __syncthreads();
-    const int run = (((p.tokens + kPlanWarps - 1) / kPlanWarps) + 31) & ~31;
-    const int t0 = w * run, t1 = min(p.tokens, t0 + run);
-    auto bin_of = [&](int t) {
-        if (t >= t1) return -1;
-        const int id = __ldg(p.ids + t);
+    const int rounds = (p.tokens + kPlanThreads - 1) / kPlanThreads;
+    const int t0 = w * rounds * 32 + lane, bits = 32 - __clz(p.count);
+    int *mine = hist + w * bins;
+    const bool hold = p.tokens <= kHeld, blocks = p.tokens <= kBlockTokens;
+    const int loose_mask = blocks ? (1 << kLooseBits) - 1 : -1;
+    auto bin_of = [&](int id) {
         if (id >= p.count) set_status(p.status, LB_ERR_INVALID_ARGUMENT);
         return id < 0 || id >= p.count ? p.count : id;
     };
-    int *mine = hist + w * bins;
-    for (int t = t0; t < t1; t += 32) {
-        const int b = bin_of(t + lane);
-        const uint32_t same = __match_any_sync(0xffffffffu, b);
-        if (b >= 0 && lane == __ffs(same) - 1) mine[b] += __popc(same);
-        __syncwarp();
+    if (hold) {
+        int ids[kHeld / kPlanThreads];
+#pragma unroll
+        for (int i = 0; i < kHeld / kPlanThreads; ++i) {
+            const int t = i * kPlanThreads + tid;
+            ids[i] = t < p.tokens ? __ldg(p.ids + t) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld / kPlanThreads; ++i) held[i * kPlanThreads + tid] = (int16_t)bin_of(ids[i]);
     }
+#pragma unroll 1
+    for (int i = tid; i < kPlanWarps * bins; i += kPlanThreads) hist[i] = 0;
     __syncthreads();
-    // per bin: its tokens, and where each warp's share of them begins
-    auto total_of = [&](int b) {
-        int n = 0;
-        for (int i = 0; i < kPlanWarps; ++i) {
-            const int k = hist[i * bins + b];
-            hist[i * bins + b] = n;
-            n += k;
+    // pass 0 counts each warp's tokens of each bin, pass 1 gives them their slots
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int i = 0; i < rounds; ++i) {
+            const int t = t0 + 32 * i;
+            int b = -1;
+            if (t < p.tokens) b = hold ? held[t] : bin_of(__ldg(p.ids + t));
+            // the lanes with the same bin, by a vote on each of its bits
+            uint32_t same = __ballot_sync(0xffffffffu, b >= 0);
+#pragma unroll 1
+            for (int k = 0; k < bits; ++k) {
+                const bool set = (b >> k) & 1;
+                const uint32_t vote = __ballot_sync(0xffffffffu, set);
+                same &= set ? vote : ~vote;
+            }
+            const bool block = blocks && same == 0xffffffffu;
+            const int had = b >= 0 ? mine[b] : 0;
+            __syncwarp();
+            if (b >= 0) {
+                if (pass == 1) {
+                    const int at = block ? 32 * (had >> kLooseBits) + lane
+                                         : 32 * whole[b] + (had & loose_mask) + __popc(same & ((1u << lane) - 1u));
+                    p.plan.perm[first_tile[b] * TM + at] = t;
+                }
+                if (lane == __ffs(same) - 1) mine[b] = had + (block ? 1 << kLooseBits : __popc(same));
+            }
+            __syncwarp();
         }
-        return n;
-    };
-    const int n = tid < p.count ? total_of(tid) : 0;
-    const int tiles = (n + TM - 1) / TM;
-    int all_tiles;
-    const int tile0 = block_scan(tiles, sums, all_tiles);
-    if (tid < p.count) first_tile[tid] = tile0;
-    int none = 0;
-    if (tid == 0) {
-        none = total_of(p.count);
-        first_tile[p.count] = all_tiles;
-        p.plan.counts[0] = all_tiles + (none + TM - 1) / TM;
-    }
-    auto list_tiles = [&](int adapter, int begin, int tokens) {
-        for (int i = 0; i * TM < tokens; ++i) p.plan.tiles[begin + i] = Tile{adapter, min(TM, tokens - i * TM)};
-        for (int s = tokens; s % TM != 0; ++s) p.plan.perm[begin * TM + s] = p.tokens;
-    };
-    list_tiles(tid, tile0, n);  // nothing for a thread without a bin
-    if (tid == 0) list_tiles(-1, all_tiles, none);
-    if (p.chunk_tiles > 0) {  // every adapter has a chunk, so that its gradient is written
-        const int parts = tid < p.count ? max(1, (tiles + p.chunk_tiles - 1) / p.chunk_tiles) : 0;
-        int all_chunks, all_parts, all_multi;
-        const int chunk0 = block_scan(parts, sums, all_chunks);
-        const int part0 = block_scan(parts > 1 ? parts : 0, sums, all_parts);
-        const int multi = block_scan(parts > 1 ? 1 : 0, sums, all_multi);
-        for (int i = 0; i < parts; ++i) {
-            const int a = i * p.chunk_tiles;
-            const int slots = min(n, (a + p.chunk_tiles) * TM) - a * TM;
-            p.plan.chunks[chunk0 + i] = Chunk{tid, tile0 + a, slots, parts > 1 ? part0 + i : -1};
+        if (pass == 1) break;
+        __syncthreads();
+        // per bin: its tokens, and where each warp's share of them begins
+#pragma unroll 1
+        for (int b = w; b < bins; b += kPlanWarps) {
+            const int k = hist[lane * bins + b];
+            int inc = k;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            hist[lane * bins + b] = inc - k;
+            if (lane == 31) {
+                whole[b] = blocks ? inc >> kLooseBits : 0;
+                total[b] = 32 * whole[b] + (inc & loose_mask);
+            }
         }
-        if (parts > 1) p.plan.multi[multi] = Multi{tid, part0, parts};
+        __syncthreads();
+        // one sum over the adapters of two 32-bit counts: tiles and blocks
+        const int n = tid < p.count ? total[tid] : 0;
+        const int tiles = (n + TM - 1) / TM;
+        const unsigned long long v = (unsigned long long)tiles | (unsigned long long)((n + 63) / 64) << 32;
+        unsigned long long inc = v;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+        }
+        if (lane == 31) sums[w] = inc;
+        __syncthreads();
+        unsigned long long all = sums[lane];
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long u = __shfl_up_sync(0xffffffffu, all, o);
+            if (lane >= o) all += u;
+        }
+        const unsigned long long below = __shfl_sync(0xffffffffu, all, max(w - 1, 0));
+        all = __shfl_sync(0xffffffffu, all, 31);
+        const unsigned long long before = inc - v + (w > 0 ? below : 0);
+        const int all_tiles = (int)all, tile0 = (int)before;
+        pdl_wait();
+        pdl_launch_dependents();
+        if (tid < p.count) {
+            first_tile[tid] = tile0;
+            p.plan.tile0[tid] = tile0;
+            p.plan.tokens[tid] = n;
+            p.plan.block0[tid] = (int)(before >> 32);
+        }
         if (tid == 0) {
-            p.plan.counts[1] = all_chunks;
-            p.plan.counts[2] = all_multi;
+            first_tile[p.count] = all_tiles;
+            p.plan.counts[0] = all_tiles + (total[p.count] + TM - 1) / TM;
+            p.plan.counts[1] = all_tiles;
+            p.plan.counts[2] = p.plan.block0[p.count] = (int)(all >> 32);
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int b = w; b < bins; b += kPlanWarps) {  // the bin's tiles, and its slots without a token
+            const int m = total[b], at = first_tile[b], end = (m + TM - 1) / TM * TM;
+#pragma unroll 1
+            for (int i = lane; i * TM < m; i += 32) {
+                p.plan.tiles[at + i].adapter = b < p.count ? b : -1;
+                p.plan.tiles[at + i].rows = min(TM, m - i * TM);
+            }
+#pragma unroll 1
+            for (int s = m + lane; s < end; s += 32) p.plan.perm[at * TM + s] = p.tokens;
         }
     }
     __syncthreads();
-    for (int t = t0; t < t1; t += 32) {
-        const int b = bin_of(t + lane);
-        const uint32_t same = __match_any_sync(0xffffffffu, b);
-        int at = 0;
-        if (b >= 0) at = mine[b] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (b >= 0) {
-            p.plan.perm[first_tile[b] * TM + at] = t + lane;
-            if (lane == __ffs(same) - 1) mine[b] += __popc(same);
+    const int ntiles = p.plan.counts[0];
+#pragma unroll 1
+    for (int i = w; i < ntiles; i += kPlanWarps) {
+        Tile *tile = p.plan.tiles + i;
+        const int4 r = *reinterpret_cast<const int4 *>(p.plan.perm + i * TM + 4 * lane);
+        const int first = __shfl_sync(0xffffffffu, r.x, 0), left = tile->rows - 4 * lane, f = first + 4 * lane;
+        const bool run = __all_sync(0xffffffffu, (left <= 0 || r.x == f) && (left <= 1 || r.y == f + 1) &&
+                                                     (left <= 2 || r.z == f + 2) && (left <= 3 || r.w == f + 3));
+        if (lane == 0) {
+            tile->first = first;
+            tile->run = run;
         }
-        __syncwarp();
     }
 }
 
@@ -206,6 +246,27 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm,
         "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+// True in one thread of a converged warp.  The loops that issue MMAs and copies
+// run under it rather than under `lane == 0`: what those instructions take must
+// be uniform, which the compiler then knows (an MMA of 128 x 64 x 16 issued
+// under a lane test took 110 cycles).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// An MMA by the low words of its operands' descriptors, which hold the address
+// in 16-byte units; the high words are the same for every K- or MN-major tile.
+constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void umma_lo(uint32_t tmem_d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh)
+        : "memory");
+}
 // MN-major operand with 128-byte swizzle: 64-wide MN chunks kBox bytes apart,
 // 8-row K groups 1024 bytes apart; 16 rows of K are 2048 bytes.
 __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr)
@@ -217,14 +278,81 @@ __device__ __forceinline__ uint32_t idesc_of(int n, bool a_mn, bool b_mn)
 {
     return instr_desc(1, TM, n) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
 }
-__device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr)
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4 &v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Two bf16 and two fp32 values added, back in bf16.
+__device__ __forceinline__ uint32_t add_bf162(uint32_t b, uint32_t lo, uint32_t hi)
+{
+    return pack_bf162(__uint_as_float(b << 16) + __uint_as_float(lo), __uint_as_float(b & 0xffff0000u) + __uint_as_float(hi));
+}
+
+// Where a wait gave up, copies may still be in flight to this CTA's shared
+// memory, and which ones is not kept; they land within microseconds.
+__device__ __forceinline__ void drain_copies()
+{
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < 200000ull) {
+    }
+}
+
+// How a tile's rows come.  A TMA gather moves four rows of 128 bytes in the
+// time of a far larger box (84 MB of x took 37 us as gathers, 25 us as boxes),
+// so consecutive rows, as a prompt's tokens are, come as boxes: the whole tile
+// in one where it is one run; else, with the rows of slots 4q .. 4q + 3 in lane
+// q, 32 slots (eight lanes) at a time, else four.
+struct RowMaps {
+    CUtensorMap all, box, quad, gather;  // a tile's rows (of a K-block for wgrad), 32, 4, any 4
+};
+struct RowLoad {
+    int4 rows;
+    int kind;        // 0 nothing, 1 a box of 32 from this lane's first row, 2 its four rows, 3 the same gathered
+    uint32_t bytes;  // all lanes', for 64 columns
+};
+// For LANES lanes that hold a box's rows.  Slots from `used` on need not be
+// read (`strict` false), or must come as zeros: their row numbers lie outside
+// the tensor.
+template <int LANES>
+__device__ __forceinline__ RowLoad row_load(int4 rows, int lane, int used, bool strict)
+{
+    RowLoad r;
+    r.rows = rows;
+    const int left = used - 4 * (lane % LANES);  // of this lane's slots
+    const bool mine = (left <= 1 || rows.y == rows.x + 1) && (left <= 2 || rows.z == rows.x + 2) &&
+                      (left <= 3 || rows.w == rows.x + 3) && !(strict && left < 4);
+    const int first = __shfl_sync(0xffffffffu, rows.x, lane & 24);
+    const uint32_t good = __ballot_sync(0xffffffffu, mine && (left <= 0 || rows.x == first + 4 * (lane & 7)));
+    if (((good >> (lane & 24)) & 0xffu) == 0xffu)
+        r.kind = (lane & 7) == 0 && left > 0 ? 1 : 0;
+    else
+        r.kind = !strict && left <= 0 ? 0 : mine ? 2 : 3;
+    r.bytes = 4096u * (uint32_t)__popc(__ballot_sync(0xffffffffu, r.kind == 1)) +
+              512u * (uint32_t)__popc(__ballot_sync(0xffffffffu, r.kind > 1));
+    return r;
+}
+// Rows that do not come as one box take up to 32 copies a K-block, which one
+// warp issues in twice the time the K-block has; kLoaders warps share them, a
+// group of eight lanes each.  Only the first waits for nobody: the others meet
+// it (loaders_meet) before they touch a stage, so that none runs ahead by
+// more than the ring of stages.
+constexpr int kLoaders = 4;
+__device__ __forceinline__ void loaders_meet() { asm volatile("bar.sync 2, %0;" ::"n"(32 * kLoaders) : "memory"); }
+
+// 64 columns from x on, each lane's to row 4 (lane % LANES) of the tile at dst.
+template <int LANES>
+__device__ __forceinline__ void load_rows(const RowLoad &r, uint32_t dst, int lane, const RowMaps *maps, int x, uint32_t bar)
+{
+    const uint32_t at = dst + (lane % LANES) * 512u;
+    if (r.kind == 1) tma_load_2d(at, &maps->box, x, r.rows.x, bar);
+    if (r.kind == 2) tma_load_2d(at, &maps->quad, x, r.rows.x, bar);
+    if (r.kind == 3) tma_gather4(at, &maps->gather, x, r.rows, bar);
 }
 
 __device__ __forceinline__ int used_rank(const int32_t *ranks, int rank, int adapter)
@@ -232,51 +360,100 @@ __device__ __forceinline__ int used_rank(const int32_t *ranks, int rank, int ada
     return ranks == nullptr ? rank : max(0, min(rank, __ldg(ranks + adapter)));
 }
 
+// `work` K-blocks in equal runs over up to `most` CTAs, at least kLeastBlocks to
+// each: CTA c has start(c) .. start(c + 1) - 1.
+constexpr int kLeastBlocks = 4;
+struct Shares {
+    int ctas, base, rem;
+    __device__ __forceinline__ Shares(int work, int most)
+    {
+        ctas = max(1, min(most, work / kLeastBlocks));
+        base = work / ctas;
+        rem = work - base * ctas;
+    }
+    __device__ __forceinline__ int start(int c) const { return c * base + min(c, rem); }
+    __device__ __forceinline__ int owner(int w) const
+    {
+        const int longer = rem * (base + 1);
+        return w < longer ? w / (base + 1) : rem + (w - longer) / base;
+    }
+    // A CTA's sums of a product that it shares: its first product's are slot 0
+    // of its two, its last one's slot 1.
+    __device__ __forceinline__ int slot(int c, int product_begin) const { return 2 * c + (start(c) < product_begin); }
+};
+
 // ------------------------------------------------------------ shrink
-// v = s_i W_i x of a tile's rows, W_i [rank x K] (K-major: A_i) or [K x rank]
-// (MN-major: B_i).  Grid (splits, tiles, jobs), clusters of `splits` CTAs.
+// v = s_i W_i x of every tile's rows, W_i [rank x K] (K-major: A_i) or [K x rank]
+// (MN-major: B_i).  Persistent CTAs with equal shares of all K-blocks of all
+// jobs and tiles, in order.  Splitting each product over a cluster of 2, 4 or 8
+// CTAs instead left a third of the SMs idle at the end of the backward pass
+// (104 us at 8192 tokens, 5120 and 17408 columns), and letting the last CTA of
+// a product add the others' sums held 13 thousand cycles behind the last MMA.
 struct ShrinkJob {
-    CUtensorMap x, w;
-    int k, rank, mn;
+    RowMaps x;
+    CUtensorMap w;
+    int nkb, rank, mn;  // K-blocks of 64 columns
     const int32_t *ranks;
     const float *scale;
     uint16_t *v[kParts];  // [slots][rank] each; the third may be null
 };
 struct ShrinkParams {
     ShrinkJob job[kMaxSiblings];
+    int njobs, per_tile;  // K-blocks of a tile in all jobs
     Plan plan;
+    float *part;  // [slot][TM][part_rank]: sums of products that several CTAs share
+    int part_rank, ctas;
     int *status;
 };
 
-constexpr int kShrinkThreads = 192;
+constexpr int kShrinkThreads = 32 * (2 + 4 + kLoaders - 1);
 constexpr uint32_t kXBytes = TM * 128;  // a K-block of a tile's rows: 64 columns
-// two CTAs on an SM: 100 KB each
-__host__ __device__ constexpr int shrink_stages(int rank) { return rank > 64 ? 3 : 4; }
-__host__ __device__ constexpr uint32_t shrink_w_bytes(int rank) { return rank > 64 ? 2 * kBox : kBox; }
-constexpr size_t kShrinkSmem = 1024 + 4 * (kXBytes + kBox) + 128;
 constexpr int kMaxRank = LB_MAX_ADAPTER_RANK;
-static_assert(4 * (kXBytes + kBox) == 3 * (kXBytes + 2 * kBox), "stages of both widths fill the same memory");
-static_assert(TM * (128 + 4) * 4 <= 4 * (kXBytes + kBox), "the sums fit where the stages were");
+template <int NK>
+struct Shrink {
+    static constexpr uint32_t kStage = kXBytes + NK * kBox;
+    static constexpr int kStages = NK == 1 ? 8 : 6;
+    static constexpr size_t kSmem = 1024 + kStages * kStage + 256;
+};
 
-__global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_constant__ ShrinkParams p)
+// Four elements of v from their sums: scaled, zero past the adapter's rank, and
+// split into bf16 parts, each what the ones before leave (exactly; an infinity
+// or NaN is all in the first).
+__device__ __forceinline__ void store_v(const ShrinkJob &J, int64_t at, int c, int rank, float scale, const float4 &s)
 {
+    float f[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = c + e < rank ? f[e] * scale : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+        if (J.v[k] == nullptr) break;
+        const uint2 o = make_uint2(pack_bf162(f[0], f[1]), pack_bf162(f[2], f[3]));
+        *reinterpret_cast<uint2 *>(J.v[k] + at) = o;
+        const float h[4] = {__uint_as_float(o.x << 16), __uint_as_float(o.x & 0xffff0000u), __uint_as_float(o.y << 16),
+                            __uint_as_float(o.y & 0xffff0000u)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = fabsf(h[e]) < __int_as_float(0x7f800000) ? f[e] - h[e] : 0.0f;
+    }
+}
+
+template <int NK>
+__global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_constant__ ShrinkParams p)
+{
+    using S = Shrink<NK>;
+    constexpr int kRank = 64 * NK;
     extern __shared__ uint8_t smem_raw[];
-    const ShrinkJob &J = p.job[blockIdx.z];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    const int stages = shrink_stages(J.rank);
-    const uint32_t w_bytes = shrink_w_bytes(J.rank), stage_bytes = kXBytes + w_bytes;
-    // full[4], empty[4], acc_full[2], acc_empty[2], drain, the tmem address
-    const uint32_t bars = base + 4 * (kXBytes + kBox);
-    const uint32_t full0 = bars, empty0 = bars + 32, accf0 = bars + 64, acce0 = bars + 80, drain = bars + 96;
+    const uint32_t bars = base + S::kStages * S::kStage;
+    const uint32_t full0 = bars, empty0 = full0 + 8 * S::kStages, accf0 = empty0 + 8 * S::kStages, acce0 = accf0 + 16;
+    const uint32_t drain = acce0 + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + (drain + 8 - raw));
     __shared__ int abort_shared;
     volatile int &abort_flag = abort_shared;
-    const int splits = gridDim.x, split = blockIdx.x, tile = blockIdx.y;
 
     if (warp == 1) {
         if (lane == 0) {
-            for (int s = 0; s < stages; ++s) {
+            for (int s = 0; s < S::kStages; ++s) {
                 mbar_init(full0 + 8 * s, 1);
                 mbar_init(empty0 + 8 * s, 1);
             }
@@ -298,145 +475,184 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
     pdl_wait();
     pdl_launch_dependents();
 
-    const bool in_plan = tile < p.plan.counts[0];
-    const Tile T = in_plan ? p.plan.tiles[tile] : Tile{-1, 0};
-    const int rank = T.adapter >= 0 ? used_rank(J.ranks, J.rank, T.adapter) : 0;
-    const bool live = rank > 0;  // uniform over the cluster
-    const int nr = (J.rank + 15) & ~15;
-    const int nkb = (J.k + 63) / 64, kb0 = (int)((int64_t)nkb * split / splits), kb1 = (int)((int64_t)nkb * (split + 1) / splits);
-    if (live && warp == 0) {
-        // TMA: lane q brings rows 4q .. 4q + 3 (rows past the tile's stay as
-        // they were: they end in rows of v that are written as zeros)
-        const int quads = (T.rows + 3) >> 2;
-        const int4 rows = *reinterpret_cast<const int4 *>(p.plan.perm + tile * TM + 4 * lane);
-        const int boxes = J.mn ? (J.rank + 63) / 64 : 1;
-        const uint32_t tx = (uint32_t)quads * 512u + (J.mn ? (uint32_t)boxes * kBox : (uint32_t)nr * 128u);
-        int g = 0;
-        for (int kb = kb0; kb < kb1; ++kb, ++g) {
-            const int s = g % stages;
-            const uint32_t ph = (uint32_t)(g / stages) & 1u;
-            const bool ok = mbar_wait(empty0 + 8 * s, ph ^ 1u) && !abort_flag;
-            if (!__all_sync(0xffffffffu, ok)) {
-                abort_flag = 1;
-                break;
-            }
-            const uint32_t sx = base + s * stage_bytes, sw = sx + kXBytes, bar = full0 + 8 * s;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, tx);
-                if (J.mn)
-                    for (int b = 0; b < boxes; ++b) tma_load_3d(sw + b * kBox, &J.w, 64 * b, 64 * kb, T.adapter, bar);
-                else
-                    tma_load_3d(sw, &J.w, 64 * kb, 0, T.adapter, bar);
-            }
-            __syncwarp();
-            if (lane < quads) tma_gather4(sx + lane * 512u, &J.x, 64 * kb, rows, bar);
+    const int live = p.plan.counts[1], cta = blockIdx.x;
+    const Shares shares(live * p.per_tile, p.ctas);
+    const int w0 = cta < shares.ctas ? shares.start(cta) : 0, w1 = cta < shares.ctas ? shares.start(cta + 1) : 0;
+    // the part of one product that begins at K-block w of this CTA's share
+    struct Piece {
+        int tile, job, kb, n;
+    };
+    auto piece_at = [&](int w) {
+        Piece q;
+        q.job = 0;
+        int nkb = p.job[0].nkb;
+        while (w >= nkb * live) {
+            w -= nkb * live;
+            nkb = p.job[++q.job].nkb;
         }
-        if (abort_flag && lane == 0)
-            for (int q = (g > stages ? g - stages : 0); q < g; ++q)
-                mbar_wait(full0 + 8 * (q % stages), (uint32_t)(q / stages) & 1u);
-    } else if (live && warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_of(nr, false, J.mn != 0);
-            int g = 0;
-            for (int kb = kb0; kb < kb1; ++kb, ++g) {
-                const int s = g % stages, seg = g / kSegment, b = seg & 1;
-                const bool first = g % kSegment == 0;
-                if ((first && !mbar_wait(acce0 + 8 * b, ((uint32_t)(seg >> 1) & 1u) ^ 1u)) ||
-                    !mbar_wait(full0 + 8 * s, (uint32_t)(g / stages) & 1u) || abort_flag) {
-                    abort_flag = 1;
-                    break;
+        q.tile = w / nkb;
+        q.kb = w - q.tile * nkb;
+        return q;
+    };
+    auto piece = [&](int w) {
+        Piece q = piece_at(w);
+        q.n = min(p.job[q.job].nkb - q.kb, w1 - w);
+        return q;
+    };
+    // (What the K-block loops below need is in registers before they start: a
+    // parameter read there costs as much as an MMA.)
+
+    const int loader = warp == 0 ? 0 : warp - 5;  // warps 0 and 6 ..
+    if (warp == 0 || warp > 5) {
+        int g = 0;  // K-blocks of the pieces so far
+        for (int w = w0; w < w1;) {  // to the end in every loader, whatever happens: they meet
+            const Piece q = piece(w);
+            const ShrinkJob &J = p.job[q.job];
+            const Tile T = p.plan.tiles[q.tile];
+            // rows past the tile's may be anything: they end in rows of v that are zeros
+            const bool run = T.run != 0;
+            RowLoad rows;
+            if (!run) {
+                rows = row_load<32>(*reinterpret_cast<const int4 *>(p.plan.perm + q.tile * TM + 4 * lane), lane, T.rows, false);
+                if ((lane >> 3) != loader) rows.kind = 0;
+                loaders_meet();
+            }
+            const bool mn = J.mn != 0, two = mn && J.rank > 64;
+            const uint32_t tx = (run ? kXBytes : rows.bytes) +
+                                (two ? 2 * kBox : mn ? kBox : (uint32_t)((J.rank + 15) & ~15) * 128u);
+            const RowMaps *mx = &J.x;
+            const CUtensorMap *mw = &J.w;
+            int s = g % S::kStages;
+            uint32_t ph = ((uint32_t)(g / S::kStages) & 1u) ^ 1u;
+            auto open_stage = [&](int kb) {  // by one thread: the weights, and room for all
+                const uint32_t sw = base + s * S::kStage + kXBytes, bar = full0 + 8 * s;
+                mbar_arrive_expect_tx(bar, tx);
+                tma_load_3d(sw, mw, mn ? 0 : 64 * kb, mn ? 64 * kb : 0, T.adapter, bar);
+                if (two) tma_load_3d(sw + kBox, mw, 64, 64 * kb, T.adapter, bar);
+            };
+            if (run && loader == 0) {
+                if (elect_one()) {
+                    for (int kb = q.kb; kb < q.kb + q.n; ++kb) {
+                        if (!mbar_wait(empty0 + 8 * s, ph) || abort_flag) {
+                            abort_flag = 1;
+                            break;
+                        }
+                        open_stage(kb);
+                        tma_load_2d(base + s * S::kStage, &mx->all, 64 * kb, T.first, full0 + 8 * s);
+                        if (++s == S::kStages) s = 0, ph ^= 1;
+                    }
                 }
-                tc_fence_after();
-                const uint32_t sx = base + s * stage_bytes, sw = sx + kXBytes;
+                __syncwarp();
+            } else if (!run) {
+                for (int kb = q.kb; kb < q.kb + q.n; ++kb) {
+                    const bool ok = mbar_wait(empty0 + 8 * s, ph) && !abort_flag;
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        abort_flag = 1;
+                        break;
+                    }
+                    if (loader == 0 && elect_one()) open_stage(kb);
+                    __syncwarp();
+                    load_rows<32>(rows, base + s * S::kStage, lane, mx, 64 * kb, full0 + 8 * s);
+                    if (++s == S::kStages) s = 0, ph ^= 1;
+                }
+            }
+            g += q.n;
+            w += q.n;
+        }
+        // after an abort: copies in flight land within microseconds
+        if (abort_flag) drain_copies();
+    } else if (warp == 1) {
+        if (elect_one()) {
+            int s = 0, na = 0;
+            uint32_t ph = 0;
+            for (int w = w0; w < w1 && !abort_flag;) {
+                const Piece q = piece(w);
+                const ShrinkJob &J = p.job[q.job];
+                const bool mn = J.mn != 0;
+                const uint32_t idesc = idesc_of((J.rank + 15) & ~15, false, mn);
+                const uint32_t a0 = (uint32_t)smem_desc(base);
+                const uint32_t b0 = mn ? (uint32_t)smem_desc_mn(base + kXBytes) : (uint32_t)smem_desc(base + kXBytes);
+                const uint32_t bstep = mn ? 2048u >> 4 : 32u >> 4;
+                for (int i = 0; i < q.n; ++i) {
+                    const int b = na & 1;
+                    const bool first = i % kSegment == 0;
+                    if ((first && !mbar_wait(acce0 + 8 * b, ((uint32_t)(na >> 1) & 1u) ^ 1u)) ||
+                        !mbar_wait(full0 + 8 * s, ph) || abort_flag) {
+                        abort_flag = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t at = (uint32_t)s * (S::kStage >> 4);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const uint64_t bd = J.mn ? smem_desc_mn(sw + 2048u * kk) : smem_desc(sw + 32u * kk);
-                    umma(tmem + 128 * b, smem_desc(sx + 32u * kk), bd, idesc, !first || kk != 0 ? 1u : 0u);
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_lo(tmem + 128 * b, a0 + at + 2 * kk, b0 + at + bstep * kk, idesc, !first || kk != 0 ? 1u : 0u);
+                    umma_commit(empty0 + 8 * s);
+                    if (i % kSegment == kSegment - 1 || i + 1 == q.n) {
+                        umma_commit(accf0 + 8 * b);
+                        ++na;
+                    }
+                    if (++s == S::kStages) s = 0, ph ^= 1;
                 }
-                umma_commit(empty0 + 8 * s);
-                if (g % kSegment == kSegment - 1 || kb + 1 == kb1) umma_commit(accf0 + 8 * b);
+                w += q.n;
             }
             umma_commit(drain);
             if (!mbar_wait(drain, 0)) abort_flag = 1;
         }
         __syncwarp();
-    } else if (live) {
-        // this CTA's sums, a row a lane: the segments in registers, then to
-        // shared memory where the stages were (the last segment's MMAs, and
-        // with them every copy, are done by then)
+    } else {
+        // a row a lane: the segments' sums in registers
         const int quad = warp & 3, row = 32 * quad + lane;
-        float sum[kMaxRank];
+        int na = 0;
+        for (int w = w0; w < w1;) {
+            const Piece q = piece(w);
+            const ShrinkJob &J = p.job[q.job];
+            const int nr = (J.rank + 15) & ~15;
+            float sum[kRank];
 #pragma unroll
-        for (int c = 0; c < kMaxRank; ++c) sum[c] = 0.0f;
-        const int segs = (kb1 - kb0 + kSegment - 1) / kSegment;
-        bool ok = true;
-        for (int seg = 0; seg < segs; ++seg) {
-            const int b = seg & 1;
-            ok = !abort_flag && mbar_wait(accf0 + 8 * b, (uint32_t)(seg >> 1) & 1u);
-            ok = __all_sync(0xffffffffu, ok);
+            for (int c = 0; c < kRank; ++c) sum[c] = 0.0f;
+            bool ok = true;
+            for (int i = 0; i < q.n; i += kSegment, ++na) {
+                const int b = na & 1;
+                ok = !abort_flag && mbar_wait(accf0 + 8 * b, (uint32_t)(na >> 1) & 1u);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kRank; c += 16) {
+                    if (c < nr) {
+                        uint32_t v[16];
+                        tmem_ld16(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(128 * b + c), v);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) sum[c + e] += __uint_as_float(v[e]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acce0 + 8 * b);
+            }
             if (!ok) {
                 abort_flag = 1;
                 break;
             }
-            tc_fence_after();
+            w += q.n;
+            const Tile T = p.plan.tiles[q.tile];
+            if (q.n < J.nkb) {  // the rest is with this CTA's neighbours: their sums meet in shrink_finish_kernel
+                float *mine = p.part + ((int64_t)shares.slot(cta, w - q.n - q.kb) * TM + row) * p.part_rank;
 #pragma unroll
-            for (int c = 0; c < kMaxRank; c += 16) {
-                if (c < nr) {
-                    uint32_t v[16];
-                    tmem_ld16(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(128 * b + c), v);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
-                }
+                for (int c = 0; c < kRank; c += 4)
+                    if (c < J.rank) *reinterpret_cast<float4 *>(mine + c) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
+                continue;
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acce0 + 8 * b);
-        }
-        if (ok) {
+            const int rank = row < T.rows ? used_rank(J.ranks, J.rank, T.adapter) : 0;
+            const float scale = J.scale != nullptr ? __ldg(J.scale + T.adapter) : 1.0f;
+            const int64_t at = ((int64_t)q.tile * TM + row) * J.rank;
 #pragma unroll
-            for (int c = 0; c < kMaxRank; c += 4)
-                if (c < nr)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + (uint32_t)(row * (nr + 4) + c) * 4u),
-                                 "r"(__float_as_uint(sum[c])), "r"(__float_as_uint(sum[c + 1])),
-                                 "r"(__float_as_uint(sum[c + 2])), "r"(__float_as_uint(sum[c + 3]))
-                                 : "memory");
-        }
-    }
-    __syncthreads();
-    if (splits > 1) cluster_sync();
-    if (live) {
-        // rows 128 split / splits .. of the tile: every CTA's sums in rank order
-        const int per = TM / splits, r0 = split * per, cols4 = J.rank / 4;
-        const float scale = J.scale != nullptr ? __ldg(J.scale + T.adapter) : 1.0f;
-        for (int i = threadIdx.x; i < per * cols4; i += kShrinkThreads) {
-            const int row = r0 + i / cols4, c = 4 * (i % cols4);
-            const uint32_t at = base + (uint32_t)(row * (nr + 4) + c) * 4u;
-            float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (row < T.rows) {
-                for (int q = 0; q < splits; ++q) {
-                    const float4 v = ld_shared_cluster_f4(splits > 1 ? map_shared_addr(at, (uint32_t)q) : at);
-                    f[0] += v.x, f[1] += v.y, f[2] += v.z, f[3] += v.w;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = row < T.rows && c + e < rank ? f[e] * scale : 0.0f;
-            const int64_t o = ((int64_t)tile * TM + row) * J.rank + c;
-#pragma unroll
-            for (int q = 0; q < kParts; ++q) {
-                if (J.v[q] == nullptr) break;
-                const uint2 part = make_uint2(pack_bf162(f[0], f[1]), pack_bf162(f[2], f[3]));
-                *reinterpret_cast<uint2 *>(J.v[q] + o) = part;
-                const float h[4] = {__uint_as_float(part.x << 16), __uint_as_float(part.x & 0xffff0000u),
-                                    __uint_as_float(part.y << 16), __uint_as_float(part.y & 0xffff0000u)};
-                // what is left (exact); an infinity or NaN is all in the first
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = fabsf(h[e]) < __int_as_float(0x7f800000) ? f[e] - h[e] : 0.0f;
-            }
+            for (int c = 0; c < kRank; c += 4)
+                if (c < J.rank) store_v(J, at + c, c, rank, scale, make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]));
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (splits > 1) cluster_sync();  // the others may still read this CTA's sums
     if (abort_flag && threadIdx.x == 0) set_status(p.status, LB_ERR_DEVICE_TIMEOUT);
     if (warp == 1) {
         __syncwarp();
@@ -445,35 +661,69 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
     }
 }
 
+// The products of shrink that several CTAs share, kFinishRows rows a unit.
+constexpr int kFinishThreads = 256, kFinishRows = 16;
+__global__ void __launch_bounds__(kFinishThreads) shrink_finish_kernel(const __grid_constant__ ShrinkParams p)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int live = p.plan.counts[1];
+    const Shares shares(live * p.per_tile, p.ctas);
+    for (int u = blockIdx.x; u < live * p.njobs * (TM / kFinishRows); u += gridDim.x) {
+        const int product = u / (TM / kFinishRows), tile = product % live, job = product / live;
+        const ShrinkJob &J = p.job[job];
+        int begin = tile * J.nkb;
+        for (int j = 0; j < job; ++j) begin += p.job[j].nkb * live;
+        const int first = shares.owner(begin), last = shares.owner(begin + J.nkb - 1);
+        if (first == last) continue;
+        const Tile T = p.plan.tiles[tile];
+        const int cols = J.rank / 4;
+        for (int i = threadIdx.x; i < kFinishRows * cols; i += kFinishThreads) {
+            const int row = u % (TM / kFinishRows) * kFinishRows + i / cols, c = 4 * (i % cols);
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+            for (int k = first; k <= last; ++k) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                    p.part + ((int64_t)shares.slot(k, begin) * TM + row) * p.part_rank + c));
+                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            }
+            const int used = row < T.rows ? used_rank(J.ranks, J.rank, T.adapter) : 0;
+            const float scale = J.scale != nullptr ? __ldg(J.scale + T.adapter) : 1.0f;
+            store_v(J, ((int64_t)tile * TM + row) * J.rank + c, c, used, scale, s);
+        }
+    }
+}
+
 // ------------------------------------------------------------ expand
 // y = base + W_i v of every tile, 128 columns a unit.  W_i [n x rank]
 // (K-major: B_i) or [rank x n] (MN-major: A_i).  Persistent CTAs, each with a
 // run of consecutive units (chunk fastest, so a tile's v stays).
 struct ExpandJob {
-    CUtensorMap base, w, hi, lo;
+    RowMaps base;
+    CUtensorMap w, hi, lo, y;  // y: 32 rows x 64 columns
     int n, rank, mn, chunks;
     const int32_t *ranks;
-    uint16_t *y;
+    uint16_t *y_rows;
     int64_t ldy;
     int in_place;
 };
 struct ExpandParams {
     ExpandJob job[kMaxSiblings];
-    int njobs, per_tile;  // chunks of all jobs
+    int njobs, per_tile;  // chunks of a tile in all jobs
     int tokens;
     Plan plan;
     int *status;
 };
 
 constexpr int kExpandWarps = 8;  // of the epilogue
-constexpr int kExpandThreads = 64 + 32 * kExpandWarps;
+constexpr int kExpandThreads = 64 + 32 * (kExpandWarps + kLoaders - 1);
 constexpr uint32_t kBaseBytes = TM * 256;  // 128 columns of a tile's rows: two halves of 64
 constexpr uint32_t kVBytes = TM * 128;     // 64 columns of hi or lo
 // NK: 64-wide blocks of the rank
 template <int NK>
 struct Expand {
-    static constexpr int kStages = NK == 1 ? 3 : 2;
-    static constexpr int kVBufs = NK == 1 ? 2 : 1;
+    static constexpr int kStages = NK == 1 ? 4 : 2;
+    static constexpr int kVBufs = 1;
     static constexpr uint32_t kW = NK * 2 * kBox;  // 128 columns x 64 NK
     static constexpr uint32_t kV = NK * 2 * kVBytes;
     static constexpr uint32_t kStage = kW + kBaseBytes;
@@ -520,141 +770,175 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
     pdl_wait();
     pdl_launch_dependents();
 
-    const int64_t units = (int64_t)p.plan.counts[0] * p.per_tile;
+    const int ntiles = p.plan.counts[0];
+    const int64_t units = (int64_t)ntiles * p.per_tile;
     const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-    // every role walks the same units; `kind`: 0 nothing to do, 1 copy base, 2 add
-    struct Unit {
-        int tile, job, chunk, kind;
+    // Every role walks the same units, job by job, tile by tile.  What a unit
+    // needs is in registers but where the tile changes (`fresh`): a parameter
+    // read per unit and role costs as much as the unit's products.
+    struct Walk {
+        int job, tile, chunk, chunks;
+        int kind;  // of the tile: 0 nothing to do, 1 copy base, 2 add
         Tile t;
-        bool fresh;  // first unit of its tile and job here: v is loaded
+        bool fresh;
     };
-    int last_tile = -1, last_job = -1, tile_kind = 0;
-    Tile tile_info{-1, 0};
-    auto next = [&](int64_t u) {
-        Unit q;
-        q.tile = (int)(u / p.per_tile);
-        int c = (int)(u - (int64_t)q.tile * p.per_tile);
-        q.job = 0;
-        while (c >= p.job[q.job].chunks) c -= p.job[q.job++].chunks;
-        q.chunk = c;
-        q.fresh = q.tile != last_tile || q.job != last_job;
-        if (q.fresh) {
-            last_tile = q.tile;
-            last_job = q.job;
-            tile_info = p.plan.tiles[q.tile];
-            const ExpandJob &J = p.job[q.job];
-            const int r = tile_info.adapter >= 0 ? used_rank(J.ranks, J.rank, tile_info.adapter) : 0;
-            tile_kind = r > 0 ? 2 : J.in_place ? 0 : 1;
+    auto enter = [&](Walk &q) {  // a new tile or job
+        const ExpandJob &J = p.job[q.job];
+        q.chunks = J.chunks;
+        q.t = p.plan.tiles[q.tile];
+        const int r = q.t.adapter >= 0 ? used_rank(J.ranks, J.rank, q.t.adapter) : 0;
+        q.kind = r > 0 ? 2 : J.in_place ? 0 : 1;
+        q.fresh = true;
+    };
+    auto start = [&]() {
+        Walk q{};
+        int64_t r = u0;
+        while (u0 < u1 && r >= (int64_t)p.job[q.job].chunks * ntiles) r -= (int64_t)p.job[q.job++].chunks * ntiles;
+        if (u0 < u1) {
+            q.tile = (int)(r / p.job[q.job].chunks);
+            q.chunk = (int)(r % p.job[q.job].chunks);
+            enter(q);
         }
-        q.kind = tile_kind;
-        q.t = tile_info;
-        q.fresh = q.fresh && tile_kind == 2;
         return q;
     };
+    auto advance = [&](Walk &q) {  // not past the last unit
+        q.fresh = false;
+        if (++q.chunk == q.chunks) {
+            q.chunk = 0;
+            if (++q.tile == ntiles) {
+                q.tile = 0;
+                ++q.job;
+            }
+            enter(q);
+        }
+    };
 
-    if (warp == 0) {
-        int g = 0, nv = 0;
-        int4 rows = make_int4(0, 0, 0, 0);
-        int rows_tile = -1;
-        for (int64_t u = u0; u < u1; ++u) {
-            const Unit q = next(u);
-            if (q.kind == 0) continue;
-            const ExpandJob &J = p.job[q.job];
-            if (rows_tile != q.tile) {
-                rows = *reinterpret_cast<const int4 *>(p.plan.perm + q.tile * TM + 4 * lane);
-                rows_tile = q.tile;
-            }
-            bool ok = true;
-            if (q.fresh) {
-                const int b = nv % S::kVBufs;
-                ok = mbar_wait(vempty0 + 8 * b, ((uint32_t)(nv / S::kVBufs) & 1u) ^ 1u) && !abort_flag;
-                if (ok && lane == 0) {
-                    const uint32_t bar = vfull0 + 8 * b, dst = sV + b * S::kV;
-                    mbar_arrive_expect_tx(bar, S::kV);
-                    for (int k = 0; k < NK; ++k) {
-                        tma_load_2d(dst + (2 * k) * kVBytes, &J.hi, 64 * k, q.tile * TM, bar);
-                        tma_load_2d(dst + (2 * k + 1) * kVBytes, &J.lo, 64 * k, q.tile * TM, bar);
-                    }
+    const int loader = warp == 0 ? 0 : warp - 1 - kExpandWarps;
+    if (warp == 0 || warp >= 2 + kExpandWarps) {
+        int s = 0, nv = 0;
+        uint32_t ph = 1, bytes = 0;
+        RowLoad rows{};
+        bool mn = false, run = false;
+        const RowMaps *mb = nullptr;
+        const CUtensorMap *mw = nullptr;
+        Walk q = start();
+        for (int64_t u = u0; u < u1; ++u) {  // to the end in every loader, whatever happens: they meet
+            if (q.fresh && q.kind != 0) {
+                const ExpandJob &J = p.job[q.job];
+                mn = J.mn != 0;
+                mb = &J.base;
+                mw = &J.w;
+                run = q.t.run != 0;
+                if (!run) {
+                    rows = row_load<32>(*reinterpret_cast<const int4 *>(p.plan.perm + q.tile * TM + 4 * lane), lane, q.t.rows,
+                                        false);
+                    if ((lane >> 3) != loader) rows.kind = 0;
+                    loaders_meet();
                 }
-                ++nv;
+                bytes = (run ? kBaseBytes : 2 * rows.bytes) + (q.kind == 2 ? S::kW : 0u);
+                if (q.kind == 2 && loader == 0) {
+                    const int b = nv % S::kVBufs;
+                    const bool ok = mbar_wait(vempty0 + 8 * b, ((uint32_t)(nv / S::kVBufs) & 1u) ^ 1u) && !abort_flag;
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        abort_flag = 1;
+                    } else if (elect_one()) {
+                        const uint32_t bar = vfull0 + 8 * b, dst = sV + b * S::kV;
+                        mbar_arrive_expect_tx(bar, S::kV);
+                        for (int k = 0; k < NK; ++k) {
+                            tma_load_2d(dst + (2 * k) * kVBytes, &J.hi, 64 * k, q.tile * TM, bar);
+                            tma_load_2d(dst + (2 * k + 1) * kVBytes, &J.lo, 64 * k, q.tile * TM, bar);
+                        }
+                    }
+                    __syncwarp();
+                    ++nv;
+                }
             }
-            const int s = g % S::kStages;
-            ok = ok && mbar_wait(empty0 + 8 * s, ((uint32_t)(g / S::kStages) & 1u) ^ 1u) && !abort_flag;
-            if (!__all_sync(0xffffffffu, ok)) {
-                abort_flag = 1;
-                break;
-            }
-            const int quads = (q.t.rows + 3) >> 2, c0 = 128 * q.chunk;
-            const uint32_t dst = sS + s * S::kStage, bar = full0 + 8 * s;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, (uint32_t)quads * 1024u + (q.kind == 2 ? S::kW : 0u));
-                if (q.kind == 2) {
-                    for (int k = 0; k < NK; ++k) {
-                        if (J.mn) {  // 64 rows of the rank x 128 columns
-                            tma_load_3d(dst + (2 * k) * kBox, &J.w, c0, 64 * k, q.t.adapter, bar);
-                            tma_load_3d(dst + (2 * k + 1) * kBox, &J.w, c0 + 64, 64 * k, q.t.adapter, bar);
-                        } else {  // 128 rows x 64 columns of the rank
-                            tma_load_3d(dst + k * 2 * kBox, &J.w, 64 * k, c0, q.t.adapter, bar);
+            if (q.kind != 0) {
+                if (loader == 0 || !run) {
+                    const bool ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        abort_flag = 1;
+                    } else {
+                        const int c0 = 128 * q.chunk;
+                        const uint32_t dst = sS + s * S::kStage, bar = full0 + 8 * s;
+                        if (loader == 0 && elect_one()) {
+                            mbar_arrive_expect_tx(bar, bytes);
+                            if (run) {
+                                tma_load_2d(dst + S::kW, &mb->all, c0, q.t.first, bar);
+                                tma_load_2d(dst + S::kW + kBaseBytes / 2, &mb->all, c0 + 64, q.t.first, bar);
+                            }
+                            if (q.kind == 2) {
+#pragma unroll
+                                for (int k = 0; k < NK; ++k) {
+                                    if (mn) {  // 64 rows of the rank x 128 columns
+                                        tma_load_3d(dst + (2 * k) * kBox, mw, c0, 64 * k, q.t.adapter, bar);
+                                        tma_load_3d(dst + (2 * k + 1) * kBox, mw, c0 + 64, 64 * k, q.t.adapter, bar);
+                                    } else {  // 128 rows x 64 columns of the rank
+                                        tma_load_3d(dst + k * 2 * kBox, mw, 64 * k, c0, q.t.adapter, bar);
+                                    }
+                                }
+                            }
+                        }
+                        __syncwarp();
+                        if (!run) {
+                            load_rows<32>(rows, dst + S::kW, lane, mb, c0, bar);
+                            load_rows<32>(rows, dst + S::kW + kBaseBytes / 2, lane, mb, c0 + 64, bar);
                         }
                     }
                 }
+                if (++s == S::kStages) s = 0, ph ^= 1;
             }
-            __syncwarp();
-            if (lane < quads) {
-                tma_gather4(dst + S::kW + lane * 512u, &J.base, c0, rows, bar);
-                tma_gather4(dst + S::kW + kBaseBytes / 2 + lane * 512u, &J.base, c0 + 64, rows, bar);
-            }
-            ++g;
+            if (u + 1 < u1) advance(q);
         }
-        if (abort_flag && lane == 0) {
-            for (int i = (g > S::kStages ? g - S::kStages : 0); i < g; ++i)
-                mbar_wait(full0 + 8 * (i % S::kStages), (uint32_t)(i / S::kStages) & 1u);
-            for (int i = (nv > S::kVBufs ? nv - S::kVBufs : 0); i < nv; ++i)
-                mbar_wait(vfull0 + 8 * (i % S::kVBufs), (uint32_t)(i / S::kVBufs) & 1u);
-        }
+        if (abort_flag) drain_copies();
     } else if (warp == 1) {
-        if (lane == 0) {
-            int g = 0, nv = 0, na = 0;
+        if (elect_one()) {
+            int s = 0, nv = 0, na = 0, steps = 0;
+            uint32_t ph = 0, idesc = 0, wstep = 0;
+            uint32_t v0 = 0, wd0 = 0;
+            Walk q = start();
             for (int64_t u = u0; u < u1 && !abort_flag; ++u) {
-                const Unit q = next(u);
-                if (q.kind == 0) continue;
-                const ExpandJob &J = p.job[q.job];
-                const int s = g % S::kStages, ab = na & 1;
-                if (q.kind == 1) {  // no product; but no phase of a stage is skipped
-                    if (!mbar_wait(full0 + 8 * s, (uint32_t)(g / S::kStages) & 1u)) {
-                        abort_flag = 1;
-                        break;
-                    }
-                    ++g;
-                    continue;
-                }
-                if (q.fresh) {
+                if (q.fresh && q.kind == 2) {
+                    const ExpandJob &J = p.job[q.job];
+                    const bool mn = J.mn != 0;
+                    steps = (J.rank + 15) / 16;
+                    idesc = idesc_of(128, false, mn);
+                    wd0 = mn ? (uint32_t)smem_desc_mn(sS) : (uint32_t)smem_desc(sS);
+                    wstep = mn ? 2048u >> 4 : 32u >> 4;
                     if (nv > 0) umma_commit(vempty0 + 8 * ((nv - 1) % S::kVBufs));  // the tile before is read
                     const int b = nv % S::kVBufs;
                     if (!mbar_wait(vfull0 + 8 * b, (uint32_t)(nv / S::kVBufs) & 1u)) {
                         abort_flag = 1;
                         break;
                     }
+                    v0 = (uint32_t)smem_desc(sV + b * S::kV);
                     ++nv;
                 }
-                if (!mbar_wait(acce0 + 8 * ab, ((uint32_t)(na >> 1) & 1u) ^ 1u) ||
-                    !mbar_wait(full0 + 8 * s, (uint32_t)(g / S::kStages) & 1u) || abort_flag) {
-                    abort_flag = 1;
-                    break;
+                if (q.kind != 0) {  // a stage's phases are all waited for, with a product or without
+                    const int ab = na & 1;
+                    if ((q.kind == 2 && !mbar_wait(acce0 + 8 * ab, ((uint32_t)(na >> 1) & 1u) ^ 1u)) ||
+                        !mbar_wait(full0 + 8 * s, ph) || abort_flag) {
+                        abort_flag = 1;
+                        break;
+                    }
+                    if (q.kind == 2) {
+                        tc_fence_after();
+                        const uint32_t acc = tmem + 128 * ab, at = (uint32_t)s * (S::kStage >> 4);
+#pragma unroll
+                        for (int i = 0; i < 4 * NK; ++i) {
+                            if (i < steps) {
+                                const uint32_t w = wd0 + at + (i >> 2) * (2 * kBox >> 4) + (i & 3) * wstep;
+                                const uint32_t v = v0 + (i >> 2) * (2 * kVBytes >> 4) + (i & 3) * 2;
+                                umma_lo(acc, v, w, idesc, i != 0 ? 1u : 0u);
+                                umma_lo(acc, v + (kVBytes >> 4), w, idesc, 1u);
+                            }
+                        }
+                        umma_commit(accf0 + 8 * ab);
+                        ++na;
+                    }
+                    if (++s == S::kStages) s = 0, ph ^= 1;
                 }
-                tc_fence_after();
-                const uint32_t v = sV + ((nv - 1) % S::kVBufs) * S::kV, w = sS + s * S::kStage, acc = tmem + 128 * ab;
-                const uint32_t idesc = idesc_of(128, false, J.mn != 0);
-                const int steps = (J.rank + 15) / 16;
-                for (int i = 0; i < steps; ++i) {
-                    const int k = i >> 2, kk = i & 3;
-                    const uint64_t bd = J.mn ? smem_desc_mn(w + k * 2 * kBox + 2048u * kk) : smem_desc(w + k * 2 * kBox + 32u * kk);
-                    umma(acc, smem_desc(v + (2 * k) * kVBytes + 32u * kk), bd, idesc, i != 0 ? 1u : 0u);
-                    umma(acc, smem_desc(v + (2 * k + 1) * kVBytes + 32u * kk), bd, idesc, 1u);
-                }
-                umma_commit(accf0 + 8 * ab);
-                ++g;
-                ++na;
+                if (u + 1 < u1) advance(q);
             }
             umma_commit(drain);
             if (!mbar_wait(drain, 0)) abort_flag = 1;
@@ -662,18 +946,35 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
         __syncwarp();
     } else {
         // epilogue: warp e takes rows 32 (warp % 4) .. and 64 of the unit's columns
-        const int quad = warp & 3, half = (warp - 2) >> 2, row = 32 * quad + lane;
-        int g = 0, na = 0, tok = 0, tok_tile = -1;
+        const int quad = warp & 3, half = (warp - 2) >> 2, row = 32 * quad + lane, tokens = p.tokens;
+        // 32 consecutive rows go back as one box, others a row of 128 bytes
+        // for each 8 lanes.  A box is read from the stage in the background, so
+        // the stage is given back a unit later.
+        int s = 0, na = 0, tok = 0, n = 0, held = -1;
+        uint32_t ph = 0;
+        uint16_t *y = nullptr;  // this lane's columns of the job
+        int64_t ldy = 0;
+        bool run = false;
+        int row0 = 0;
+        const CUtensorMap *my = nullptr;
+        Walk q = start();
         for (int64_t u = u0; u < u1; ++u) {
-            const Unit q = next(u);
-            if (q.kind == 0) continue;
-            const ExpandJob &J = p.job[q.job];
-            if (tok_tile != q.tile) {
+            if (q.fresh) {
+                const ExpandJob &J = p.job[q.job];
                 tok = p.plan.perm[q.tile * TM + row];
-                tok_tile = q.tile;
+                row0 = __shfl_sync(0xffffffffu, tok, 0);
+                run = __all_sync(0xffffffffu, tok < tokens && tok == row0 + lane);
+                my = &J.y;
+                n = J.n;
+                y = J.y_rows + 64 * half + 8 * (lane & 7);
+                ldy = J.ldy;
             }
-            const int s = g % S::kStages, ab = na & 1;
-            bool ok = !abort_flag && mbar_wait(full0 + 8 * s, (uint32_t)(g / S::kStages) & 1u);
+            if (q.kind == 0) {
+                if (u + 1 < u1) advance(q);
+                continue;
+            }
+            const int ab = na & 1;
+            bool ok = !abort_flag && mbar_wait(full0 + 8 * s, ph);
             if (ok && q.kind == 2) ok = mbar_wait(accf0 + 8 * ab, (uint32_t)(na >> 1) & 1u);
             if (!__all_sync(0xffffffffu, ok)) {
                 abort_flag = 1;
@@ -685,25 +986,18 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
                 const uint32_t at = tile + (uint32_t)row * 128u;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    uint4 b[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) b[c] = ld_shared_v4(at + (uint32_t)(((4 * h + c) ^ (row & 7)) << 4));
                     uint32_t v[32];
                     tmem_ld32(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(128 * ab + 64 * half + 32 * h), v);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const uint32_t a = at + (uint32_t)(((4 * h + c) ^ (row & 7)) << 4);
-                        uint32_t b[4];
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
-                                     : "r"(a)
-                                     : "memory");
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float f0 = __uint_as_float(b[e] << 16) + __uint_as_float(v[8 * c + 2 * e]);
-                            const float f1 = __uint_as_float(b[e] & 0xffff0000u) + __uint_as_float(v[8 * c + 2 * e + 1]);
-                            b[e] = pack_bf162(f0, f1);
-                        }
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(b[0]), "r"(b[1]), "r"(b[2]),
-                                     "r"(b[3])
-                                     : "memory");
+                        b[c].x = add_bf162(b[c].x, v[8 * c], v[8 * c + 1]);
+                        b[c].y = add_bf162(b[c].y, v[8 * c + 2], v[8 * c + 3]);
+                        b[c].z = add_bf162(b[c].z, v[8 * c + 4], v[8 * c + 5]);
+                        b[c].w = add_bf162(b[c].w, v[8 * c + 6], v[8 * c + 7]);
+                        st_shared_v4(at + (uint32_t)(((4 * h + c) ^ (row & 7)) << 4), b[c]);
                     }
                 }
                 tc_fence_before();
@@ -711,27 +1005,50 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
                 if (lane == 0) mbar_arrive(acce0 + 8 * ab);
                 ++na;
             }
-            // back to the rows of y: 8 lanes a row, 128 bytes
-            const int col = 128 * q.chunk + 64 * half + 8 * (lane & 7);
+            const int c0 = 128 * q.chunk;
+            fence_async_shared();  // for the box, and for the next copy into this stage
+            __syncwarp();
+            if (run) {
+                if (lane == 0) {
+                    if (c0 + 64 * half < n) tma_store_2d(my, c0 + 64 * half, row0, tile + (uint32_t)quad * 4096u);
+                    bulk_commit();
+                    if (S::kStages > 2) {
+                        bulk_wait_read<1>();
+                        if (held >= 0) mbar_arrive(empty0 + 8 * held);
+                        held = s;
+                    } else {  // none to spare
+                        bulk_wait_read<0>();
+                        mbar_arrive(empty0 + 8 * s);
+                    }
+                }
+            } else {
+                const bool in = c0 + 64 * half + 8 * (lane & 7) < n;
+                uint4 o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 4 * i + (lane >> 3);  // within this warp's 32 rows
-                const int t = __shfl_sync(0xffffffffu, tok, r);
-                if (t < p.tokens && col < J.n) {
-                    uint4 o;
-                    const int tr = 32 * quad + r;
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
-                                 : "r"(tile + (uint32_t)tr * 128u + (uint32_t)(((lane & 7) ^ (tr & 7)) << 4))
-                                 : "memory");
-                    *reinterpret_cast<uint4 *>(J.y + (int64_t)t * J.ldy + col) = o;
+                for (int i = 0; i < 8; ++i) {
+                    const int tr = 32 * quad + 4 * i + (lane >> 3);
+                    o[i] = ld_shared_v4(tile + (uint32_t)tr * 128u + (uint32_t)(((lane & 7) ^ (tr & 7)) << 4));
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    if (held >= 0) {
+                        bulk_wait_read<0>();
+                        mbar_arrive(empty0 + 8 * held);
+                        held = -1;
+                    }
+                    mbar_arrive(empty0 + 8 * s);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int t = __shfl_sync(0xffffffffu, tok, 4 * i + (lane >> 3));
+                    if (t < tokens && in) *reinterpret_cast<uint4 *>(y + (int64_t)t * ldy + c0) = o[i];
                 }
             }
-            fence_async_shared();  // the next copy into this stage comes after these accesses
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty0 + 8 * s);
-            ++g;
+            if (++s == S::kStages) s = 0, ph ^= 1;
+            if (u + 1 < u1) advance(q);
         }
+        if (lane == 0) bulk_wait_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -745,37 +1062,73 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
 
 // ------------------------------------------------------------ wgrad
 // dA_i[r][n] = sum over an adapter's slots of u[slot][r] x[slot][n], and dB_i
-// the same of v and dy with the result [n][r]: D[n][r], 128 columns n a unit,
-// the slots as K; both operands MN-major (slots outermost).
+// the same of v and dy with the result [n][r]: D[n][r] with the slots as K, both
+// operands MN-major (slots outermost), 64 slots a K-block.  A product is kCols
+// columns n of one adapter: with ranks up to 64 two MMA tiles, so that v, three
+// bf16 parts wide, comes from L2 half as often for the x it meets (a tile alone
+// moved 40 KB for 16 KB of x and took 108 us at 8192 tokens).  Shares as in
+// shrink, adapter by adapter.
 struct WgradJob {
-    CUtensorMap x, v[kParts];
-    int n, tiles;      // columns, 128-wide units of them
-    int transposed;    // the gradient is [r][n]
-    float *out;        // [adapter][...]
-    int64_t part_off;  // within a part
+    RowMaps x;
+    CUtensorMap v[kParts];
+    int n, products;  // columns; products of an adapter
+    int transposed;   // the gradient is [r][n]
+    float *out;       // [adapter][...]
 };
 struct AdapterWgradParams {
     WgradJob job[2];
-    int rank;
+    int rank, count, ctas;
     const int32_t *ranks;
     Plan plan;
-    float *part;         // [part][part_size]
-    int64_t part_size;
+    float *part;  // [slot][kCols * rank], the gradient's order
     int *status;
 };
 
-constexpr int kWgradThreads = 192;
+constexpr int kWgradWarps = 8;  // of the epilogue
+constexpr int kWgradThreads = 64 + 32 * (kWgradWarps + kLoaders - 1);
 template <int NK>
-struct WgradShape {
-    static constexpr int kStages = NK == 1 ? 5 : 3;
-    static constexpr uint32_t kStage = 2 * kBox + kParts * NK * kBox;
+struct Wgrad {
+    static constexpr int kTiles = NK == 1 ? 2 : 1;  // of 128 columns
+    static constexpr int kCols = 128 * kTiles;
+    static constexpr uint32_t kX = kTiles * 2 * kBox;
+    static constexpr uint32_t kStage = kX + kParts * NK * kBox;
+    static constexpr int kStages = NK == 1 ? 4 : 3;
     static constexpr size_t kSmem = 1024 + kStages * kStage + 256;
 };
+
+// The product at K-block w of all the work: adapter i has block0[i] .. blocks,
+// each of them `per` (products of both jobs) times.
+struct Product {
+    int adapter, job, n0, begin, nkb, kb;
+};
+template <int NK>
+__device__ __forceinline__ Product product_at(const AdapterWgradParams &p, int w)
+{
+    const int per = p.job[0].products + p.job[1].products;
+    int lo = 0, hi = p.count;  // the last adapter with block0 * per <= w (those without blocks come before it)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.plan.block0[mid] * per <= w)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    Product q;
+    q.adapter = lo;
+    const int b0 = p.plan.block0[lo] * per;
+    q.nkb = p.plan.block0[lo + 1] - p.plan.block0[lo];
+    const int m = (w - b0) / q.nkb;
+    q.begin = b0 + m * q.nkb;
+    q.kb = w - q.begin;
+    q.job = m >= p.job[0].products;
+    q.n0 = Wgrad<NK>::kCols * (q.job ? m - p.job[0].products : m);
+    return q;
+}
 
 template <int NK>
 __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const __grid_constant__ AdapterWgradParams p)
 {
-    using S = WgradShape<NK>;
+    using S = Wgrad<NK>;
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -794,7 +1147,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
             }
             for (int b = 0; b < 2; ++b) {
                 mbar_init(accf0 + 8 * b, 1);
-                mbar_init(acce0 + 8 * b, 4);
+                mbar_init(acce0 + 8 * b, kWgradWarps);
             }
             mbar_init(drain, 1);
             abort_flag = 0;
@@ -810,146 +1163,173 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
     pdl_wait();
     pdl_launch_dependents();
 
-    const int per = p.job[0].tiles + p.job[1].tiles;
-    const int64_t units = (int64_t)p.plan.counts[1] * per;
-    const int nr = (p.rank + 15) & ~15;
-    struct Unit {
-        Chunk c;
-        int job, n0, nkb;
-    };
-    auto unit_of = [&](int64_t u) {
-        Unit q;
-        q.c = p.plan.chunks[u / per];
-        const int m = (int)(u % per);
-        q.job = m >= p.job[0].tiles;
-        q.n0 = 128 * (q.job ? m - p.job[0].tiles : m);
-        q.nkb = (q.c.slots + 63) / 64;
-        if (used_rank(p.ranks, p.rank, q.c.adapter) == 0) q.nkb = 0;
-        return q;
-    };
+    const int cta = blockIdx.x;
+    const Shares shares(p.plan.counts[2] * (p.job[0].products + p.job[1].products), p.ctas);
+    const int w0 = cta < shares.ctas ? shares.start(cta) : 0, w1 = cta < shares.ctas ? shares.start(cta + 1) : 0;
 
-    if (warp == 0) {
-        // lanes 0 .. 15 bring the 64 slots' rows of columns n0 .., lanes 16 .. 31 of n0 + 64 ..
-        int g = 0;
-        bool stop = false;
-        for (int64_t u = blockIdx.x; u < units && !stop; u += gridDim.x) {
-            const Unit q = unit_of(u);
+    const int loader = warp == 0 ? 0 : warp - 1 - kWgradWarps;
+    if (warp == 0 || warp >= 2 + kWgradWarps) {
+        int s = 0;
+        uint32_t ph = 1;
+        for (int w = w0; w < w1;) {  // to the end in every loader, whatever happens: they meet
+            const Product q = product_at<NK>(p, w);
+            const int n = min(q.nkb - q.kb, w1 - w);
             const WgradJob &J = p.job[q.job];
-            const int *perm = p.plan.perm + q.c.tile0 * TM + 4 * (lane & 15);
-            int4 rows = make_int4(0, 0, 0, 0);
-            if (q.nkb > 0) rows = *reinterpret_cast<const int4 *>(perm);
-            for (int kb = 0; kb < q.nkb; ++kb, ++g) {
-                const int s = g % S::kStages;
-                const int4 now = rows;
-                if (kb + 1 < q.nkb) rows = *reinterpret_cast<const int4 *>(perm + 64 * (kb + 1));
-                const bool ok = mbar_wait(empty0 + 8 * s, ((uint32_t)(g / S::kStages) & 1u) ^ 1u) && !abort_flag;
-                if (!__all_sync(0xffffffffu, ok)) {
-                    abort_flag = 1;
-                    stop = true;
-                    break;
+            const RowMaps *mx = &J.x;
+            const CUtensorMap *mv = J.v;
+            const int tile0 = p.plan.tile0[q.adapter], end = q.kb + n;
+            Tile T = p.plan.tiles[tile0 + q.kb / 2], next = T;
+            for (int kb = q.kb; kb < end; ++kb) {
+                const int half = kb & 1;
+                if (half == 0) T = next;
+                if (half == 0 || kb == q.kb) {  // ahead of use
+                    if ((kb | 1) + 1 < end) next = p.plan.tiles[tile0 + kb / 2 + 1];
                 }
                 const uint32_t dst = base + s * S::kStage, bar = full0 + 8 * s;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, S::kStage);
-                    const int slot = q.c.tile0 * TM + 64 * kb;
-                    for (int i = 0; i < kParts; ++i)
-                        for (int k = 0; k < NK; ++k) tma_load_2d(dst + (2 + i * NK + k) * kBox, &J.v[i], 64 * k, slot, bar);
+                const int slot = tile0 * TM + 64 * kb;
+                const bool run = T.run != 0 && T.rows >= 64 * half + 64;
+                RowLoad rows{};
+                if (!run) {  // each loader 64 columns of the 64 slots, with zeros past the adapter's tokens
+                    rows = row_load<16>(*reinterpret_cast<const int4 *>(p.plan.perm + slot + 4 * (lane & 15)), lane,
+                                        T.rows - 64 * half, true);
+                    if (lane > 15 || loader >= 2 * S::kTiles) rows.kind = 0;
+                    loaders_meet();
+                    const bool ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
+                    if (!__all_sync(0xffffffffu, ok)) abort_flag = 1, rows.kind = 0;
                 }
-                __syncwarp();
-                tma_gather4(dst + (lane >> 4) * kBox + (lane & 15) * 512u, &J.x, q.n0 + 64 * (lane >> 4), now, bar);
+                if (loader == 0) {
+                    bool ok = true;
+                    if (elect_one()) {
+                        ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
+                        if (ok) {
+                            mbar_arrive_expect_tx(bar, S::kStage);
+                            if (run) {
+#pragma unroll
+                                for (int c = 0; c < 2 * S::kTiles; ++c)
+                                    tma_load_2d(dst + c * kBox, &mx->all, q.n0 + 64 * c, T.first + 64 * half, bar);
+                            }
+#pragma unroll
+                            for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                                for (int k = 0; k < NK; ++k)
+                                    tma_load_2d(dst + S::kX + (i * NK + k) * kBox, mv + i, 64 * k, slot, bar);
+                        } else {
+                            abort_flag = 1;
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!run) load_rows<16>(rows, dst + loader * kBox, lane, mx, q.n0 + 64 * loader, bar);
+                if (++s == S::kStages) s = 0, ph ^= 1;
             }
+            w += n;
         }
-        if (abort_flag && lane == 0)
-            for (int i = (g > S::kStages ? g - S::kStages : 0); i < g; ++i)
-                mbar_wait(full0 + 8 * (i % S::kStages), (uint32_t)(i / S::kStages) & 1u);
+        if (abort_flag) drain_copies();
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_of(nr, true, true);
-            int g = 0, na = 0;  // K-blocks and segments so far
-            for (int64_t u = blockIdx.x; u < units && !abort_flag; u += gridDim.x) {
-                const Unit q = unit_of(u);
-                for (int kb = 0; kb < q.nkb; ++kb, ++g) {
-                    const int s = g % S::kStages, ab = na & 1;
-                    const bool first = kb % kSegment == 0;
+        if (elect_one()) {
+            // v's parts side by side as N, so that x is read less often from
+            // shared memory: the first two, then the third onto the second's sums
+            constexpr int NH = 64 * NK;
+            const uint32_t idesc = idesc_of(2 * NH, true, true), idesc2 = idesc_of(NH, true, true);
+            const uint32_t a0 = (uint32_t)smem_desc_mn(base), b0 = (uint32_t)smem_desc_mn(base + S::kX);
+            int s = 0, na = 0;  // stage; segments so far
+            uint32_t ph = 0;
+            for (int w = w0; w < w1 && !abort_flag;) {
+                const Product q = product_at<NK>(p, w);
+                const int n = min(q.nkb - q.kb, w1 - w);
+                for (int i = 0; i < n; ++i) {
+                    const int ab = na & 1;
+                    const bool first = i % kSegment == 0;
                     if ((first && !mbar_wait(acce0 + 8 * ab, ((uint32_t)(na >> 1) & 1u) ^ 1u)) ||
-                        !mbar_wait(full0 + 8 * s, (uint32_t)(g / S::kStages) & 1u) || abort_flag) {
+                        !mbar_wait(full0 + 8 * s, ph) || abort_flag) {
                         abort_flag = 1;
                         break;
                     }
                     tc_fence_after();
-                    // the first part of v in one sum, the smaller ones in another
-                    const uint32_t a = base + s * S::kStage, b = a + 2 * kBox, acc = tmem + 256 * ab;
+                    const uint32_t at = (uint32_t)s * (S::kStage >> 4), acc = tmem + 256 * ab;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t ad = smem_desc_mn(a + 2048u * kk);
-                        const uint32_t more = !first || kk != 0 ? 1u : 0u;
-                        umma(acc, ad, smem_desc_mn(b + 2048u * kk), idesc, more);
+                        const uint32_t bd = b0 + at + kk * (2048u >> 4);
 #pragma unroll
-                        for (int i = 1; i < kParts; ++i)
-                            umma(acc + 128, ad, smem_desc_mn(b + i * NK * kBox + 2048u * kk), idesc, i > 1 ? 1u : more);
+                        for (int m = 0; m < S::kTiles; ++m) {
+                            const uint32_t ad = a0 + at + m * (2 * kBox >> 4) + kk * (2048u >> 4);
+                            umma_lo(acc + 128 * m, ad, bd, idesc, !first || kk != 0 ? 1u : 0u);
+                            umma_lo(acc + 128 * m + NH, ad, bd + (2 * NK * kBox >> 4), idesc2, 1u);
+                        }
                     }
                     umma_commit(empty0 + 8 * s);
-                    if (kb % kSegment == kSegment - 1 || kb + 1 == q.nkb) {
+                    if (i % kSegment == kSegment - 1 || i + 1 == n) {
                         umma_commit(accf0 + 8 * ab);
                         ++na;
                     }
+                    if (++s == S::kStages) s = 0, ph ^= 1;
                 }
+                w += n;
             }
             umma_commit(drain);
             if (!mbar_wait(drain, 0)) abort_flag = 1;
         }
         __syncwarp();
     } else {
-        const int quad = warp & 3;
+        // a column n a lane, 64 of the rank: warps 2 .. 5 and 6 .. 9 take the
+        // two tiles (NK = 1), or the two halves of the rank
+        const int quad = warp & 3, part = (warp - 2) >> 2;
+        const int n_local = 32 * quad + lane + (NK == 1 ? 128 * part : 0), c0 = NK == 1 ? 0 : 64 * part;
+        const uint32_t lane_at = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(NK == 1 ? 128 * part : 64 * part);
+        const int nr = min(64, ((p.rank + 15) & ~15) - c0);
         int na = 0;
-        for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-            const Unit q = unit_of(u);
-            const WgradJob &J = p.job[q.job];
-            const int used = used_rank(p.ranks, p.rank, q.c.adapter);
-            float sum[64 * NK];
+        for (int w = w0; w < w1;) {
+            const Product q = product_at<NK>(p, w);
+            const int n = min(q.nkb - q.kb, w1 - w);
+            float sum[64];
 #pragma unroll
-            for (int c = 0; c < 64 * NK; ++c) sum[c] = 0.0f;
-            bool ok = !abort_flag;
-            for (int kb = 0; kb < q.nkb; kb += kSegment, ++na) {
+            for (int c = 0; c < 64; ++c) sum[c] = 0.0f;
+            bool ok = true;
+            for (int i = 0; i < n; i += kSegment, ++na) {
                 const int ab = na & 1;
                 ok = !abort_flag && mbar_wait(accf0 + 8 * ab, (uint32_t)(na >> 1) & 1u);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < 64 * NK; c += 16) {
+                for (int c = 0; c < 64; c += 16) {
                     if (c < nr) {
-                        uint32_t v[16], w[16];
-                        const uint32_t at = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(256 * ab + c);
-                        tmem_ld16(at, v);
-                        tmem_ld16(at + 128, w);
+                        uint32_t v[16], r[16];
+                        tmem_ld16(lane_at + (uint32_t)(256 * ab + c), v);
+                        tmem_ld16(lane_at + (uint32_t)(256 * ab + 64 * NK + c), r);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]) + __uint_as_float(w[i]);
+                        for (int e = 0; e < 16; ++e) sum[c + e] += __uint_as_float(v[e]) + __uint_as_float(r[e]);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(acce0 + 8 * ab);
             }
-            if (!__all_sync(0xffffffffu, ok)) {
+            if (!ok) {
                 abort_flag = 1;
                 break;
             }
-            const int n = q.n0 + 32 * quad + lane;
-            float *out = q.c.part >= 0 ? p.part + q.c.part * p.part_size + J.part_off
-                                       : J.out + (int64_t)q.c.adapter * p.rank * J.n;
-            if (n >= J.n) continue;
-            if (J.transposed) {
+            w += n;
+            const WgradJob &J = p.job[q.job];
+            const bool whole = n == q.nkb;
+            const int used = whole ? used_rank(p.ranks, p.rank, q.adapter) : p.rank;
+            // its place in the gradient, or among the shared sums
+            float *out = whole ? J.out + (int64_t)q.adapter * p.rank * J.n
+                               : p.part + (int64_t)shares.slot(cta, q.begin) * S::kCols * p.rank;
+            const int col = (whole ? q.n0 : 0) + n_local, ld = whole ? J.n : S::kCols;
+            if (q.n0 + n_local < J.n) {  // uniform over the warp
+                if (J.transposed) {
 #pragma unroll
-                for (int c = 0; c < 64 * NK; ++c)
-                    if (c < p.rank) out[(int64_t)c * J.n + n] = c < used ? sum[c] : 0.0f;
-            } else {
+                    for (int c = 0; c < 64; ++c)
+                        if (c0 + c < p.rank) out[(int64_t)(c0 + c) * ld + col] = c0 + c < used ? sum[c] : 0.0f;
+                } else {
 #pragma unroll
-                for (int c = 0; c < 64 * NK; c += 4)
-                    if (c < p.rank)
-                        *reinterpret_cast<float4 *>(out + (int64_t)n * p.rank + c) =
-                            make_float4(c < used ? sum[c] : 0.0f, c + 1 < used ? sum[c + 1] : 0.0f,
-                                        c + 2 < used ? sum[c + 2] : 0.0f, c + 3 < used ? sum[c + 3] : 0.0f);
+                    for (int c = 0; c < 64; c += 4)
+                        if (c0 + c < p.rank)
+                            *reinterpret_cast<float4 *>(out + (int64_t)col * p.rank + c0 + c) =
+                                make_float4(c0 + c < used ? sum[c] : 0.0f, c0 + c + 1 < used ? sum[c + 1] : 0.0f,
+                                            c0 + c + 2 < used ? sum[c + 2] : 0.0f, c0 + c + 3 < used ? sum[c + 3] : 0.0f);
+                }
             }
         }
     }
@@ -963,30 +1343,52 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
     }
 }
 
-// The gradients of adapters of several chunks: their parts, added in order.
-struct SumParams {
-    Plan plan;
-    const float *part;
-    int64_t part_size, a_size, b_size;  // floats
-    float *da, *db;
-};
-__global__ void __launch_bounds__(256) sum_parts_kernel(const SumParams p)
+// The products of wgrad that several CTAs share, and zeros for adapters that no
+// token uses; 1024 quads of the gradient a unit.
+constexpr int kQuads = 1024;
+template <int NK>
+__global__ void __launch_bounds__(kFinishThreads) wgrad_finish_kernel(const __grid_constant__ AdapterWgradParams p)
 {
+    constexpr int kCols = Wgrad<NK>::kCols;
     pdl_wait();
     pdl_launch_dependents();
-    const int multi = p.plan.counts[2];
-    const int64_t quads = p.part_size / 4;
-    for (int m = 0; m < multi; ++m) {
-        const Multi e = p.plan.multi[m];
-        const float4 *src = reinterpret_cast<const float4 *>(p.part + e.part0 * p.part_size);
-        for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < quads; i += (int64_t)gridDim.x * blockDim.x) {
-            float4 s = src[i];
-            for (int q = 1; q < e.parts; ++q) {
-                const float4 v = src[q * quads + i];
+    const int per = p.job[0].products + p.job[1].products;
+    const Shares shares(p.plan.counts[2] * per, p.ctas);
+    const int quads = kCols * p.rank / 4, units = (quads + kQuads - 1) / kQuads;
+    for (int64_t u = blockIdx.x; u < (int64_t)p.count * per * units; u += gridDim.x) {
+        const int adapter = (int)(u / (per * units)), r = (int)(u - (int64_t)adapter * per * units);
+        const int m = r / units, i0 = (r - m * units) * kQuads;
+        const int b0 = p.plan.block0[adapter], nkb = p.plan.block0[adapter + 1] - b0;
+        const int begin = b0 * per + m * nkb;
+        int first = 0, last = -1;
+        if (nkb > 0) {
+            first = shares.owner(begin);
+            last = shares.owner(begin + nkb - 1);
+            if (first == last) continue;
+        }
+        const int job = m >= p.job[0].products;
+        const WgradJob &J = p.job[job];
+        const int n0 = kCols * (job ? m - p.job[0].products : m), used = used_rank(p.ranks, p.rank, adapter);
+        float *out = J.out + (int64_t)adapter * p.rank * J.n;
+#pragma unroll 4
+        for (int i = i0 + threadIdx.x; i < min(quads, i0 + kQuads); i += kFinishThreads) {
+            const int n = J.transposed ? 4 * (i % (kCols / 4)) : i / (p.rank / 4);
+            const int c = J.transposed ? i / (kCols / 4) : 4 * (i % (p.rank / 4));
+            if (n0 + n >= J.n) continue;
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int k = first; k <= last; ++k) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part) + (int64_t)shares.slot(k, begin) * quads + i);
                 s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
             }
-            float *dst = 4 * i < p.a_size ? p.da + e.adapter * p.a_size + 4 * i : p.db + e.adapter * p.b_size + (4 * i - p.a_size);
-            *reinterpret_cast<float4 *>(dst) = s;
+            if (J.transposed) {
+                if (c >= used) s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                *reinterpret_cast<float4 *>(out + (int64_t)c * J.n + n0 + n) = s;
+            } else {
+                s = make_float4(c < used ? s.x : 0.0f, c + 1 < used ? s.y : 0.0f, c + 2 < used ? s.z : 0.0f,
+                                c + 3 < used ? s.w : 0.0f);
+                *reinterpret_cast<float4 *>(out + (int64_t)(n0 + n) * p.rank + c) = s;
+            }
         }
     }
 }
@@ -994,14 +1396,17 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const SumParams p)
 // ------------------------------------------------------------ host side
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
+constexpr int kMostCtas = 148;  // of shrink and wgrad, whatever the device has: workspaces are sized by it
+
 // Tiles of a batch: at most one partial tile per adapter in use, and for the
 // tokens without one.
 int most_tiles(int tokens, int count) { return tokens / TM + std::min(count + 1, tokens); }
 
 struct Layout {
-    size_t counts, tiles, perm, chunks, multi, v[kMaxSiblings][kParts], part, total;
+    size_t counts, tiles, perm, block0, tile0, tokens, v[kMaxSiblings][kParts], sums, grads, total;
 };
-Layout layout_of(int tokens, int count, int nv, const int *ranks, int parts, int max_chunks, size_t part_floats)
+// nv: products v per tile, of `parts` bf16 each; grad_floats: of the shared sums of wgrad
+Layout layout_of(int tokens, int count, int nv, const int *ranks, int parts, size_t grad_floats)
 {
     Layout L{};
     size_t off = 0;
@@ -1014,11 +1419,15 @@ Layout layout_of(int tokens, int count, int nv, const int *ranks, int parts, int
     L.counts = take(4 * sizeof(int));
     L.tiles = take(tiles * sizeof(Tile));
     L.perm = take(tiles * TM * sizeof(int));
-    L.chunks = take((size_t)max_chunks * sizeof(Chunk));
-    L.multi = take((size_t)max_chunks * sizeof(Multi));
+    L.block0 = take((size_t)(count + 1) * sizeof(int));
+    L.tile0 = take((size_t)count * sizeof(int));
+    L.tokens = take((size_t)count * sizeof(int));
+    int widest = 0;
+    for (int j = 0; j < nv; ++j) widest = std::max(widest, ranks[j]);
+    L.sums = take((size_t)2 * kMostCtas * TM * (size_t)widest * sizeof(float));
     for (int j = 0; j < nv; ++j)
         for (int q = 0; q < parts; ++q) L.v[j][q] = take(tiles * TM * (size_t)ranks[j] * 2);
-    L.part = take(part_floats * sizeof(float));
+    L.grads = take(grad_floats * sizeof(float));
     L.total = off;
     return L;
 }
@@ -1029,15 +1438,20 @@ Plan plan_at(const Layout &L, uint8_t *ws)
     p.counts = reinterpret_cast<int *>(ws + L.counts);
     p.tiles = reinterpret_cast<Tile *>(ws + L.tiles);
     p.perm = reinterpret_cast<int *>(ws + L.perm);
-    p.chunks = reinterpret_cast<Chunk *>(ws + L.chunks);
-    p.multi = reinterpret_cast<Multi *>(ws + L.multi);
+    p.block0 = reinterpret_cast<int *>(ws + L.block0);
+    p.tile0 = reinterpret_cast<int *>(ws + L.tile0);
+    p.tokens = reinterpret_cast<int *>(ws + L.tokens);
     return p;
 }
 
-// Rows of a bf16 matrix, gathered four at a time, 64 columns wide.
-cudaError_t encode_gather(CUtensorMap *tm, const void *ptr, int rows, int cols, int64_t ld)
+// Rows of a bf16 matrix, 64 columns wide: `all` together, 32, 4, or any 4 gathered.
+cudaError_t encode_rows(RowMaps *m, const void *ptr, int rows, int cols, int64_t ld, int all)
 {
-    return encode_2d(tm, ptr, rows, cols, ld, true, 1);
+    cudaError_t e = encode_2d(&m->all, ptr, rows, cols, ld, true, all);
+    if (e == cudaSuccess) e = encode_2d(&m->box, ptr, rows, cols, ld, true, 32);
+    if (e == cudaSuccess) e = encode_2d(&m->quad, ptr, rows, cols, ld, true, 4);
+    if (e == cudaSuccess) e = encode_2d(&m->gather, ptr, rows, cols, ld, true, 1);
+    return e;
 }
 // A dense bf16 [n2][n1][n0] in boxes of box1 x 64.
 cudaError_t encode_3d(CUtensorMap *tm, const void *ptr, int n0, int n1, int n2, int box1)
@@ -1055,61 +1469,54 @@ cudaError_t encode_3d(CUtensorMap *tm, const void *ptr, int n0, int n1, int n2, 
 }
 
 template <typename K, typename P>
-cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, int cluster, const P &p, cudaStream_t stream)
+cudaError_t launch(K kernel, int grid, int threads, size_t smem, const P &p, cudaStream_t stream)
 {
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-cudaError_t launch_plan(const int32_t *ids, int tokens, int count, int chunk_tiles, const Plan &plan, const DeviceInfo &dev,
-                        cudaStream_t stream)
+cudaError_t launch_plan(const int32_t *ids, int tokens, int count, const Plan &plan, const DeviceInfo &dev, cudaStream_t stream)
 {
-    const PlanParams p{ids, tokens, count, chunk_tiles, plan, dev.status};
-    return launch(plan_kernel, dim3(1), kPlanThreads, sizeof(int) * kPlanWarps * (size_t)(count + 1), 1, p, stream);
+    const PlanParams p{ids, tokens, count, plan, dev.status};
+    return launch(plan_kernel, 1, kPlanThreads, sizeof(int) * kPlanWarps * (size_t)(count + 1), p, stream);
 }
 
-// CTAs a tile's K is split over: as few as give every SM its two CTAs, with at
-// least four K-blocks each.
-int shrink_splits(int tokens, int jobs, int k, int sms)
+cudaError_t launch_shrink(ShrinkParams &p, int tiles, const DeviceInfo &dev, cudaStream_t stream)
 {
-    const int tiles = (tokens + TM - 1) / TM * jobs, nkb = (k + 63) / 64;
-    int s = 1;
-    while (s < 8 && tiles * s * 2 <= 2 * sms && nkb >= 8 * s) s *= 2;
-    return s;
+    p.ctas = std::min(dev.sm_count, kMostCtas);
+    const cudaError_t e = p.part_rank <= 64 ? launch(shrink_kernel<1>, p.ctas, kShrinkThreads, Shrink<1>::kSmem, p, stream)
+                                            : launch(shrink_kernel<2>, p.ctas, kShrinkThreads, Shrink<2>::kSmem, p, stream);
+    return e != cudaSuccess ? e : launch(shrink_finish_kernel, std::min(tiles * p.njobs * (TM / kFinishRows), 16 * dev.sm_count), kFinishThreads,
+                                        0, p, stream);
+}
+
+template <int NK>
+cudaError_t launch_wgrad(AdapterWgradParams &p, const DeviceInfo &dev, cudaStream_t stream)
+{
+    for (WgradJob &J : p.job) J.products = (J.n + Wgrad<NK>::kCols - 1) / Wgrad<NK>::kCols;
+    p.ctas = std::min(dev.sm_count, kMostCtas);
+    const cudaError_t e = launch(adapter_wgrad_kernel<NK>, p.ctas, kWgradThreads, Wgrad<NK>::kSmem, p, stream);
+    return e != cudaSuccess ? e : launch(wgrad_finish_kernel<NK>, 8 * dev.sm_count, kFinishThreads, 0, p, stream);
+}
+size_t wgrad_shared_floats(int rank)
+{
+    return (size_t)2 * kMostCtas * (size_t)(rank <= 64 ? Wgrad<1>::kCols : Wgrad<2>::kCols) * (size_t)rank;
 }
 
 cudaError_t launch_expand(const ExpandParams &p, int rank, const DeviceInfo &dev, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)dev.sm_count);
-    return rank <= 64 ? launch(expand_kernel<1>, grid, kExpandThreads, Expand<1>::kSmem, 1, p, stream)
-                      : launch(expand_kernel<2>, grid, kExpandThreads, Expand<2>::kSmem, 1, p, stream);
+    return rank <= 64 ? launch(expand_kernel<1>, dev.sm_count, kExpandThreads, Expand<1>::kSmem, p, stream)
+                      : launch(expand_kernel<2>, dev.sm_count, kExpandThreads, Expand<2>::kSmem, p, stream);
 }
-
-// Tiles of a wgrad chunk, for about three units an SM when one adapter has all tokens.
-int wgrad_chunk_tiles(int tokens, int n_in, int n_out, int sms)
-{
-    const int tiles = (tokens + TM - 1) / TM, per = (n_in + 127) / 128 + (n_out + 127) / 128;
-    const int chunks = std::max(1, std::min(tiles, (3 * sms + per - 1) / per));
-    return (tiles + chunks - 1) / chunks;
-}
-// Parts: an adapter of several chunks has more than chunk_tiles tiles of
-// tokens, so all of them have fewer than 2 tokens / (128 chunk_tiles) chunks.
-int wgrad_parts(int tokens, int chunk_tiles) { return chunk_tiles * TM >= tokens ? 0 : 2 * tokens / (TM * chunk_tiles) + 1; }
-
-constexpr int kSmsForPlan = 148;  // plans are made for this many SMs, so that workspaces do not depend on the device
 
 }  // namespace
 
@@ -1121,17 +1528,18 @@ cudaError_t adapters_mma_prepare_device(const DeviceInfo &dev)
     auto allow = [&](auto kernel, size_t bytes) {
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     };
-    allow(shrink_kernel, kShrinkSmem);
+    allow(shrink_kernel<1>, Shrink<1>::kSmem);
+    allow(shrink_kernel<2>, Shrink<2>::kSmem);
     allow(expand_kernel<1>, Expand<1>::kSmem);
     allow(expand_kernel<2>, Expand<2>::kSmem);
-    allow(adapter_wgrad_kernel<1>, WgradShape<1>::kSmem);
-    allow(adapter_wgrad_kernel<2>, WgradShape<2>::kSmem);
+    allow(adapter_wgrad_kernel<1>, Wgrad<1>::kSmem);
+    allow(adapter_wgrad_kernel<2>, Wgrad<2>::kSmem);
     return e;
 }
 
 size_t adapters_mma_workspace_bytes(int tokens, int count, int nproj, const int *ranks)
 {
-    return layout_of(tokens, count, nproj, ranks, 2, 0, 0).total;
+    return layout_of(tokens, count, nproj, ranks, 2, 0).total;
 }
 
 cudaError_t adapters_mma_forward(const AdaptersArgs &a, const DeviceInfo &dev, cudaStream_t stream)
@@ -1143,7 +1551,7 @@ cudaError_t adapters_mma_forward(const AdaptersArgs &a, const DeviceInfo &dev, c
         ranks[j] = a.proj[j].rank;
         widest = std::max(widest, ranks[j]);
     }
-    const Layout L = layout_of(a.tokens, a.count, a.nproj, ranks, 2, 0, 0);
+    const Layout L = layout_of(a.tokens, a.count, a.nproj, ranks, 2, 0);
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     const Plan plan = plan_at(L, ws);
     const int tiles = most_tiles(a.tokens, a.count);
@@ -1153,13 +1561,14 @@ cudaError_t adapters_mma_forward(const AdaptersArgs &a, const DeviceInfo &dev, c
     sp.status = ep.status = dev.status;
     ep.njobs = a.nproj;
     ep.tokens = a.tokens;
-    CUtensorMap mx;
-    e = encode_gather(&mx, a.x, a.tokens, a.n_in, a.ldx);
+    RowMaps mx;
+    e = encode_rows(&mx, a.x, a.tokens, a.n_in, a.ldx, TM);
     for (int j = 0; j < a.nproj && e == cudaSuccess; ++j) {
         const AdapterProj &P = a.proj[j];
         ShrinkJob &s = sp.job[j];
         s.x = mx;
-        s.k = a.n_in;
+        s.nkb = (a.n_in + 63) / 64;
+        sp.per_tile += s.nkb;
         s.rank = P.rank;
         s.ranks = P.ranks;
         s.scale = P.scale;
@@ -1171,57 +1580,56 @@ cudaError_t adapters_mma_forward(const AdaptersArgs &a, const DeviceInfo &dev, c
         x.chunks = (P.n_out + 127) / 128;
         ep.per_tile += x.chunks;
         x.ranks = P.ranks;
-        x.y = P.y;
+        x.y_rows = P.y;
         x.ldy = P.ldy;
         x.in_place = P.base == P.y;
-        if (e == cudaSuccess) e = encode_gather(&x.base, P.base, a.tokens, P.n_out, P.ldbase);
+        if (e == cudaSuccess) e = encode_rows(&x.base, P.base, a.tokens, P.n_out, P.ldbase, TM);
+        if (e == cudaSuccess) e = encode_2d(&x.y, P.y, a.tokens, P.n_out, P.ldy, true, 32);
         if (e == cudaSuccess) e = encode_3d(&x.w, P.b, P.rank, P.n_out, a.count, 128);
         if (e == cudaSuccess) e = encode_2d(&x.hi, s.v[0], tiles * TM, P.rank, P.rank, true, TM);
         if (e == cudaSuccess) e = encode_2d(&x.lo, s.v[1], tiles * TM, P.rank, P.rank, true, TM);
     }
-    if (e == cudaSuccess) e = launch_plan(a.ids, a.tokens, a.count, 0, plan, dev, stream);
-    const int splits = shrink_splits(a.tokens, a.nproj, a.n_in, dev.sm_count);
-    if (e == cudaSuccess)
-        e = launch(shrink_kernel, dim3((unsigned)splits, (unsigned)tiles, (unsigned)a.nproj), kShrinkThreads, kShrinkSmem,
-                   splits, sp, stream);
+    sp.njobs = a.nproj;
+    sp.part = reinterpret_cast<float *>(ws + L.sums);
+    sp.part_rank = widest;
+    if (e == cudaSuccess) e = launch_plan(a.ids, a.tokens, a.count, plan, dev, stream);
+    if (e == cudaSuccess) e = launch_shrink(sp, tiles, dev, stream);
     if (e == cudaSuccess) e = launch_expand(ep, widest, dev, stream);
     return e;
 }
 
-size_t adapters_mma_backward_workspace_bytes(int tokens, int n_in, int n_out, int count, int rank)
+size_t adapters_mma_backward_workspace_bytes(int tokens, int count, int rank)
 {
-    const int ct = wgrad_chunk_tiles(tokens, n_in, n_out, kSmsForPlan), parts = wgrad_parts(tokens, ct);
     const int ranks[2] = {rank, rank};
-    return layout_of(tokens, count, 2, ranks, kParts, count + parts,
-                     (size_t)parts * (size_t)rank * ((size_t)n_in + (size_t)n_out)).total;
+    return layout_of(tokens, count, 2, ranks, kParts, wgrad_shared_floats(rank)).total;
 }
 
 cudaError_t adapters_mma_backward(const AdaptersBwdArgs &b, const DeviceInfo &dev, cudaStream_t stream)
 {
     cudaError_t e = get_encoder();
     if (e != cudaSuccess) return e;
-    const int ct = wgrad_chunk_tiles(b.tokens, b.n_in, b.n_out, kSmsForPlan), parts = wgrad_parts(b.tokens, ct);
     const int ranks[2] = {b.rank, b.rank};
-    const int64_t a_size = (int64_t)b.rank * b.n_in, b_size = (int64_t)b.rank * b.n_out;
-    const Layout L = layout_of(b.tokens, b.count, 2, ranks, kParts, b.count + parts, (size_t)parts * (size_t)(a_size + b_size));
+    const Layout L = layout_of(b.tokens, b.count, 2, ranks, kParts, wgrad_shared_floats(b.rank));
     uint8_t *ws = static_cast<uint8_t *>(b.workspace);
     const Plan plan = plan_at(L, ws);
     const int tiles = most_tiles(b.tokens, b.count);
     uint16_t *v[2][kParts];  // v, then u
-    CUtensorMap mx, mdy, mhi, mlo;
+    RowMaps mx, mdy;
+    CUtensorMap mhi, mlo;
     for (int q = 0; q < 2; ++q)
         for (int i = 0; i < kParts; ++i) v[q][i] = reinterpret_cast<uint16_t *>(ws + L.v[q][i]);
     e = encode_2d(&mhi, v[1][0], tiles * TM, b.rank, b.rank, true, TM);
     if (e == cudaSuccess) e = encode_2d(&mlo, v[1][1], tiles * TM, b.rank, b.rank, true, TM);
-    if (e == cudaSuccess) e = encode_gather(&mx, b.x, b.tokens, b.n_in, b.ldx);
-    if (e == cudaSuccess) e = encode_gather(&mdy, b.dy, b.tokens, b.n_out, b.lddy);
+    if (e == cudaSuccess) e = encode_rows(&mx, b.x, b.tokens, b.n_in, b.ldx, TM);
+    if (e == cudaSuccess) e = encode_rows(&mdy, b.dy, b.tokens, b.n_out, b.lddy, TM);
     ShrinkParams sp{};
     sp.plan = plan;
     sp.status = dev.status;
     for (int q = 0; q < 2; ++q) {
         ShrinkJob &s = sp.job[q];
         s.x = q ? mdy : mx;
-        s.k = q ? b.n_out : b.n_in;
+        s.nkb = ((q ? b.n_out : b.n_in) + 63) / 64;
+        sp.per_tile += s.nkb;
         s.rank = b.rank;
         s.mn = q;
         s.ranks = b.ranks;
@@ -1230,10 +1638,11 @@ cudaError_t adapters_mma_backward(const AdaptersBwdArgs &b, const DeviceInfo &de
     }
     if (e == cudaSuccess) e = encode_3d(&sp.job[0].w, b.a, b.n_in, b.rank, b.count, (b.rank + 15) & ~15);
     if (e == cudaSuccess) e = encode_3d(&sp.job[1].w, b.b, b.rank, b.n_out, b.count, 64);
-    if (e == cudaSuccess) e = launch_plan(b.ids, b.tokens, b.count, ct, plan, dev, stream);
-    const int splits = shrink_splits(b.tokens, 2, std::min(b.n_in, b.n_out), dev.sm_count);
-    if (e == cudaSuccess)
-        e = launch(shrink_kernel, dim3((unsigned)splits, (unsigned)tiles, 2), kShrinkThreads, kShrinkSmem, splits, sp, stream);
+    sp.njobs = 2;
+    sp.part = reinterpret_cast<float *>(ws + L.sums);
+    sp.part_rank = b.rank;
+    if (e == cudaSuccess) e = launch_plan(b.ids, b.tokens, b.count, plan, dev, stream);
+    if (e == cudaSuccess) e = launch_shrink(sp, tiles, dev, stream);
     if (b.dx != nullptr && e == cudaSuccess) {
         ExpandParams ep{};
         ep.plan = plan;
@@ -1246,41 +1655,37 @@ cudaError_t adapters_mma_backward(const AdaptersBwdArgs &b, const DeviceInfo &de
         x.mn = 1;
         x.chunks = ep.per_tile = (b.n_in + 127) / 128;
         x.ranks = b.ranks;
-        x.y = b.dx;
+        x.y_rows = b.dx;
         x.ldy = b.lddx;
         x.in_place = b.dx_base == b.dx;
         x.hi = mhi;
         x.lo = mlo;
-        e = encode_gather(&x.base, b.dx_base, b.tokens, b.n_in, b.lddxbase);
+        e = encode_rows(&x.base, b.dx_base, b.tokens, b.n_in, b.lddxbase, TM);
+        if (e == cudaSuccess) e = encode_2d(&x.y, b.dx, b.tokens, b.n_in, b.lddx, true, 32);
         if (e == cudaSuccess) e = encode_3d(&x.w, b.a, b.n_in, b.rank, b.count, 64);
         if (e == cudaSuccess) e = launch_expand(ep, b.rank, dev, stream);
     }
     if (e != cudaSuccess) return e;
     AdapterWgradParams wp{};
     wp.rank = b.rank;
+    wp.count = b.count;
     wp.ranks = b.ranks;
     wp.plan = plan;
-    wp.part = reinterpret_cast<float *>(ws + L.part);
-    wp.part_size = a_size + b_size;
+    wp.part = reinterpret_cast<float *>(ws + L.grads);
     wp.status = dev.status;
     for (int q = 0; q < 2; ++q) {  // dA from x and u, dB from dy and v
         WgradJob &w = wp.job[q];
         w.x = q ? mdy : mx;
+        if (e == cudaSuccess)
+            e = encode_2d(&w.x.all, q ? b.dy : b.x, b.tokens, q ? b.n_out : b.n_in, q ? b.lddy : b.ldx, true, 64);
         for (int i = 0; i < kParts && e == cudaSuccess; ++i)
             e = encode_2d(&w.v[i], v[1 - q][i], tiles * TM, b.rank, b.rank, true, 64);
         w.n = q ? b.n_out : b.n_in;
-        w.tiles = (w.n + 127) / 128;
         w.transposed = !q;
         w.out = q ? b.db : b.da;
-        w.part_off = q ? a_size : 0;
     }
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)dev.sm_count);
-    e = b.rank <= 64 ? launch(adapter_wgrad_kernel<1>, grid, kWgradThreads, WgradShape<1>::kSmem, 1, wp, stream)
-                     : launch(adapter_wgrad_kernel<2>, grid, kWgradThreads, WgradShape<2>::kSmem, 1, wp, stream);
-    if (e != cudaSuccess || parts == 0) return e;
-    const SumParams qp{plan, wp.part, wp.part_size, a_size, b_size, b.da, b.db};
-    return launch(sum_parts_kernel, dim3((unsigned)(2 * dev.sm_count)), 256, 0, 1, qp, stream);
+    return b.rank <= 64 ? launch_wgrad<1>(wp, dev, stream) : launch_wgrad<2>(wp, dev, stream);
 }
 
 }  // namespace lb

@@ -673,7 +673,7 @@ size_t lb_adapters_backward_workspace_bytes(int64_t tokens, int64_t n_in, int64_
     if (tokens <= 0 || n_in <= 0 || n_out <= 0 || !adapters_backward_sizes(tokens, n_in, n_out) ||
         check_pool(&pool, true) != LB_OK)
         return 0;
-    return lb::adapters_backward_workspace_bytes((int)tokens, (int)n_in, (int)n_out, (int)count, (int)rank);
+    return lb::adapters_backward_workspace_bytes((int)tokens, (int)count, (int)rank);
 }
 
 lb_status lb_adapters_backward(const uint16_t *x, const uint16_t *dy, int64_t tokens, int64_t n_in, int64_t n_out,
@@ -696,8 +696,7 @@ lb_status lb_adapters_backward(const uint16_t *x, const uint16_t *dy, int64_t to
     lb::AdaptersBwdArgs b{};
     b.count = (int)adapters->count;
     b.rank = (int)adapters->rank;
-    const size_t need = tokens > 0 ? lb::adapters_backward_workspace_bytes((int)tokens, (int)n_in, (int)n_out, b.count,
-                                                                           b.rank)
+    const size_t need = tokens > 0 ? lb::adapters_backward_workspace_bytes((int)tokens, b.count, b.rank)
                                    : 0;
     if (need > 0 && !workspace) return LB_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return LB_ERR_WORKSPACE_TOO_SMALL;

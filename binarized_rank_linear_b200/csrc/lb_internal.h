@@ -256,13 +256,13 @@ struct AdaptersBwdArgs {
 };
 size_t adapters_workspace_bytes(int tokens, int n_in, int count, int nproj, const int *ranks);
 cudaError_t adapters_forward(const AdaptersArgs &a, const DeviceInfo &dev, cudaStream_t stream);
-size_t adapters_backward_workspace_bytes(int tokens, int n_in, int n_out, int count, int rank);
+size_t adapters_backward_workspace_bytes(int tokens, int count, int rank);
 cudaError_t adapters_backward(const AdaptersBwdArgs &a, const DeviceInfo &dev, cudaStream_t stream);
 cudaError_t adapters_prepare_device(const DeviceInfo &dev);
 // More than kAdapterSmallTokens tokens, and the backward pass (lb_adapters_mma.cu).
 size_t adapters_mma_workspace_bytes(int tokens, int count, int nproj, const int *ranks);
 cudaError_t adapters_mma_forward(const AdaptersArgs &a, const DeviceInfo &dev, cudaStream_t stream);
-size_t adapters_mma_backward_workspace_bytes(int tokens, int n_in, int n_out, int count, int rank);
+size_t adapters_mma_backward_workspace_bytes(int tokens, int count, int rank);
 cudaError_t adapters_mma_backward(const AdaptersBwdArgs &a, const DeviceInfo &dev, cudaStream_t stream);
 cudaError_t adapters_mma_prepare_device(const DeviceInfo &dev);
 
