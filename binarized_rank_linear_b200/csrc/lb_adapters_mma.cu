@@ -54,8 +54,8 @@ constexpr int kParts = 3;             // bf16 that v is the sum of
 struct alignas(16) Tile {
     int adapter;      // -1: tokens without an adapter
     int rows;         // slots in use, from 1 to TM
-    int first;        // the first slot's token
-    int run;          // whether the others follow it one by one
+    int first, last;  // the first and last of its tokens, which are in order
+    __device__ __forceinline__ bool run() const { return last - first == rows - 1; }  // none missing between
 };
 struct Plan {
     int *counts;   // tiles, those of adapters (the first ones), 64-slot blocks of adapters
@@ -75,29 +75,23 @@ struct PlanParams {
 
 constexpr int kPlanThreads = 1024, kPlanWarps = 32;
 constexpr int kHeld = 8192;  // tokens whose bins stay in shared memory between the two passes
-constexpr int kBlockTokens = 1 << 17, kLooseBits = 18;  // counts: whole blocks above 18 bits of other tokens
 
-// Each warp takes a run of tokens in order, so that the slots of an adapter's
-// tokens, and with them its sums, do not depend on timing.  Of up to kBlockTokens tokens,
-// 32 neighbours (from a multiple of 32 on) of one adapter go to 32 slots
-// together, before the adapter's other tokens: prompts begin and end anywhere,
-// and a break inside a tile makes TMA gather its rows (one such tile held the
-// backward pass at 8192 tokens for 30 us).  One CTA runs this
+// Each warp takes a run of tokens in order, so that an adapter's tokens keep
+// their order and sums over them do not depend on timing.  One CTA runs this
 // once, so its instructions come from far away: the code is kept short (loops
-// stay rolled), which took 29 to 9 thousand cycles at 8192 tokens.  The ids
-// are read before the launch ahead is done; nothing is written before that.
+// stay rolled; unrolled it took twice as long).  The ids are read before the
+// launch ahead is done; nothing is written before that.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
 {
     extern __shared__ int hist[];  // [warp][bin]; bin `count`: no adapter
     __shared__ unsigned long long sums[kPlanWarps];
-    __shared__ int first_tile[LB_MAX_ADAPTERS + 1], total[LB_MAX_ADAPTERS + 1], whole[LB_MAX_ADAPTERS + 1];
+    __shared__ int first_tile[LB_MAX_ADAPTERS + 1], total[LB_MAX_ADAPTERS + 1];
     __shared__ int16_t held[kHeld];
     const int bins = p.count + 1, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int rounds = (p.tokens + kPlanThreads - 1) / kPlanThreads;
     const int t0 = w * rounds * 32 + lane, bits = 32 - __clz(p.count);
     int *mine = hist + w * bins;
-    const bool hold = p.tokens <= kHeld, blocks = p.tokens <= kBlockTokens;
-    const int loose_mask = blocks ? (1 << kLooseBits) - 1 : -1;
+    const bool hold = p.tokens <= kHeld;
     auto bin_of = [&](int id) {
         if (id >= p.count) set_status(p.status, LB_ERR_INVALID_ARGUMENT);
         return id < 0 || id >= p.count ? p.count : id;
@@ -131,16 +125,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
                 const uint32_t vote = __ballot_sync(0xffffffffu, set);
                 same &= set ? vote : ~vote;
             }
-            const bool block = blocks && same == 0xffffffffu;
             const int had = b >= 0 ? mine[b] : 0;
             __syncwarp();
             if (b >= 0) {
+                const int rank = __popc(same & ((1u << lane) - 1u));
                 if (pass == 1) {
-                    const int at = block ? 32 * (had >> kLooseBits) + lane
-                                         : 32 * whole[b] + (had & loose_mask) + __popc(same & ((1u << lane) - 1u));
+                    const int at = had + rank;
                     p.plan.perm[first_tile[b] * TM + at] = t;
+                    Tile &tile = p.plan.tiles[first_tile[b] + at / TM];
+                    if (at % TM == 0) tile.first = t;
+                    if (at % TM == TM - 1 || at == total[b] - 1) tile.last = t;
                 }
-                if (lane == __ffs(same) - 1) mine[b] = had + (block ? 1 << kLooseBits : __popc(same));
+                if (rank == 0) mine[b] = had + __popc(same);
             }
             __syncwarp();
         }
@@ -157,10 +153,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
                 if (lane >= o) inc += v;
             }
             hist[lane * bins + b] = inc - k;
-            if (lane == 31) {
-                whole[b] = blocks ? inc >> kLooseBits : 0;
-                total[b] = 32 * whole[b] + (inc & loose_mask);
-            }
+            if (lane == 31) total[b] = inc;
         }
         __syncthreads();
         // one sum over the adapters of two 32-bit counts: tiles and blocks
@@ -212,32 +205,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
             for (int s = m + lane; s < end; s += 32) p.plan.perm[at * TM + s] = p.tokens;
         }
     }
-    __syncthreads();
-    const int ntiles = p.plan.counts[0];
-#pragma unroll 1
-    for (int i = w; i < ntiles; i += kPlanWarps) {
-        Tile *tile = p.plan.tiles + i;
-        const int4 r = *reinterpret_cast<const int4 *>(p.plan.perm + i * TM + 4 * lane);
-        const int first = __shfl_sync(0xffffffffu, r.x, 0), left = tile->rows - 4 * lane, f = first + 4 * lane;
-        const bool run = __all_sync(0xffffffffu, (left <= 0 || r.x == f) && (left <= 1 || r.y == f + 1) &&
-                                                     (left <= 2 || r.z == f + 2) && (left <= 3 || r.w == f + 3));
-        if (lane == 0) {
-            tile->first = first;
-            tile->run = run;
-        }
-    }
 }
 
 // ------------------------------------------------------------ loads
-// Four rows y.x .. y.w of a matrix, 64 columns from x on, to 4 x 128 bytes.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *tm, int x, int4 y, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-        "%5, %6}], [%7];" ::"r"(dst),
-        "l"(tm), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(bar)
-        : "memory");
-}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm, int x, int y, int z, uint32_t bar)
 {
     asm volatile(
@@ -303,57 +273,67 @@ __device__ __forceinline__ void drain_copies()
     }
 }
 
-// How a tile's rows come.  A TMA gather moves four rows of 128 bytes in the
-// time of a far larger box (84 MB of x took 37 us as gathers, 25 us as boxes),
-// so consecutive rows, as a prompt's tokens are, come as boxes: the whole tile
-// in one where it is one run; else, with the rows of slots 4q .. 4q + 3 in lane
-// q, 32 slots (eight lanes) at a time, else four.
-struct RowMaps {
-    CUtensorMap all, box, quad, gather;  // a tile's rows (of a K-block for wgrad), 32, 4, any 4
+// How a tile's rows come.  Consecutive ones, as a prompt's tokens are, in one
+// TMA box.  TMA's gather of four rows takes the time of a far larger box (84 MB
+// of x took 37 us so, 25 us in boxes; a single tile with a break in it held the
+// backward pass at 8192 tokens for 30 us), so the rows of other tiles come as
+// 16-byte copies of the threads of kLoaders warps.  A stage's full barrier
+// counts kFull arrivals: of those threads as their copies land, and of the one
+// that announces the TMA bytes, which arrives for all where TMA brings the rows.
+// (A writer's own wait and proxy fence before its arrival made a K-block of such
+// a tile wait for every copy under way; the reader of the stage has the fence.)
+struct Rows {
+    CUtensorMap box;  // a tile's rows (of a K-block for wgrad) x 64 columns
+    const uint16_t *p;
+    int64_t ld;
+    int cols;
 };
-struct RowLoad {
-    int4 rows;
-    int kind;        // 0 nothing, 1 a box of 32 from this lane's first row, 2 its four rows, 3 the same gathered
-    uint32_t bytes;  // all lanes', for 64 columns
-};
-// For LANES lanes that hold a box's rows.  Slots from `used` on need not be
-// read (`strict` false), or must come as zeros: their row numbers lie outside
-// the tensor.
-template <int LANES>
-__device__ __forceinline__ RowLoad row_load(int4 rows, int lane, int used, bool strict)
-{
-    RowLoad r;
-    r.rows = rows;
-    const int left = used - 4 * (lane % LANES);  // of this lane's slots
-    const bool mine = (left <= 1 || rows.y == rows.x + 1) && (left <= 2 || rows.z == rows.x + 2) &&
-                      (left <= 3 || rows.w == rows.x + 3) && !(strict && left < 4);
-    const int first = __shfl_sync(0xffffffffu, rows.x, lane & 24);
-    const uint32_t good = __ballot_sync(0xffffffffu, mine && (left <= 0 || rows.x == first + 4 * (lane & 7)));
-    if (((good >> (lane & 24)) & 0xffu) == 0xffu)
-        r.kind = (lane & 7) == 0 && left > 0 ? 1 : 0;
-    else
-        r.kind = !strict && left <= 0 ? 0 : mine ? 2 : 3;
-    r.bytes = 4096u * (uint32_t)__popc(__ballot_sync(0xffffffffu, r.kind == 1)) +
-              512u * (uint32_t)__popc(__ballot_sync(0xffffffffu, r.kind > 1));
-    return r;
-}
-// Rows that do not come as one box take up to 32 copies a K-block, which one
-// warp issues in twice the time the K-block has; kLoaders warps share them, a
-// group of eight lanes each.  Only the first waits for nobody: the others meet
-// it (loaders_meet) before they touch a stage, so that none runs ahead by
-// more than the ring of stages.
 constexpr int kLoaders = 4;
-__device__ __forceinline__ void loaders_meet() { asm volatile("bar.sync 2, %0;" ::"n"(32 * kLoaders) : "memory"); }
-
-// 64 columns from x on, each lane's to row 4 (lane % LANES) of the tile at dst.
-template <int LANES>
-__device__ __forceinline__ void load_rows(const RowLoad &r, uint32_t dst, int lane, const RowMaps *maps, int x, uint32_t bar)
+constexpr int kLoadThreads = 32 * kLoaders;
+__device__ __forceinline__ void loaders_meet() { asm volatile("bar.sync 2, %0;" ::"n"(kLoadThreads) : "memory"); }
+constexpr int kFull = 1 + kLoadThreads;
+__device__ __forceinline__ void mbar_arrive_for_loaders(uint32_t bar)
 {
-    const uint32_t at = dst + (lane % LANES) * 512u;
-    if (r.kind == 1) tma_load_2d(at, &maps->box, x, r.rows.x, bar);
-    if (r.kind == 2) tma_load_2d(at, &maps->quad, x, r.rows.x, bar);
-    if (r.kind == 3) tma_gather4(at, &maps->gather, x, r.rows, bar);
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar), "n"(kLoadThreads)
+                 : "memory");
 }
+// Arrives when this thread's copies so far have landed.
+__device__ __forceinline__ void mbar_arrive_after_copies(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// 16 bytes to shared memory, zeros where `there` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint16_t *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+// This thread's part of ROWS rows x 64 columns: every 16th row from tid / 8 on,
+// 16 bytes at chunk tid % 8, in the layout of a TMA box.  `row` holds the rows
+// (negative: not read; `strict`: as zeros).
+template <int ROWS>
+struct Copier {
+    static constexpr int kN = ROWS / (kLoadThreads / 8);
+    int row[kN];
+    int r0, chunk;
+    __device__ __forceinline__ void rows(const int *perm, int used, int tid)
+    {
+        r0 = tid >> 3;
+        chunk = tid & 7;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) row[i] = r0 + 16 * i < used ? perm[r0 + 16 * i] : -1;
+    }
+    __device__ __forceinline__ void copy(uint32_t dst, const uint16_t *p, int64_t ld, int cols, int col, bool strict) const
+    {
+        const int c = col + 8 * chunk;
+        const uint32_t at = dst + r0 * 128u + (uint32_t)((chunk ^ (r0 & 7)) << 4);  // rows 16 apart: the same swizzle
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            if (row[i] >= 0)
+                copy16(at + 2048u * i, c < cols ? p + row[i] * ld + c : p, c < cols);
+            else if (strict)
+                copy16(at + 2048u * i, p, false);
+    }
+};
 
 __device__ __forceinline__ int used_rank(const int32_t *ranks, int rank, int adapter)
 {
@@ -390,7 +370,7 @@ struct Shares {
 // (104 us at 8192 tokens, 5120 and 17408 columns), and letting the last CTA of
 // a product add the others' sums held 13 thousand cycles behind the last MMA.
 struct ShrinkJob {
-    RowMaps x;
+    Rows x;
     CUtensorMap w;
     int nkb, rank, mn;  // K-blocks of 64 columns
     const int32_t *ranks;
@@ -454,7 +434,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
     if (warp == 1) {
         if (lane == 0) {
             for (int s = 0; s < S::kStages; ++s) {
-                mbar_init(full0 + 8 * s, 1);
+                mbar_init(full0 + 8 * s, kFull);
                 mbar_init(empty0 + 8 * s, 1);
             }
             for (int b = 0; b < 2; ++b) {
@@ -510,23 +490,13 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
             const ShrinkJob &J = p.job[q.job];
             const Tile T = p.plan.tiles[q.tile];
             // rows past the tile's may be anything: they end in rows of v that are zeros
-            const bool run = T.run != 0;
-            RowLoad rows;
-            if (!run) {
-                rows = row_load<32>(*reinterpret_cast<const int4 *>(p.plan.perm + q.tile * TM + 4 * lane), lane, T.rows, false);
-                if ((lane >> 3) != loader) rows.kind = 0;
-                loaders_meet();
-            }
-            const bool mn = J.mn != 0, two = mn && J.rank > 64;
-            const uint32_t tx = (run ? kXBytes : rows.bytes) +
-                                (two ? 2 * kBox : mn ? kBox : (uint32_t)((J.rank + 15) & ~15) * 128u);
-            const RowMaps *mx = &J.x;
-            const CUtensorMap *mw = &J.w;
+            const bool run = T.run(), mn = J.mn != 0, two = mn && J.rank > 64;
+            const uint32_t w_bytes = two ? 2 * kBox : mn ? kBox : (uint32_t)((J.rank + 15) & ~15) * 128u;
+            const CUtensorMap *mx = &J.x.box, *mw = &J.w;
             int s = g % S::kStages;
             uint32_t ph = ((uint32_t)(g / S::kStages) & 1u) ^ 1u;
-            auto open_stage = [&](int kb) {  // by one thread: the weights, and room for all
+            auto load_w = [&](int kb) {
                 const uint32_t sw = base + s * S::kStage + kXBytes, bar = full0 + 8 * s;
-                mbar_arrive_expect_tx(bar, tx);
                 tma_load_3d(sw, mw, mn ? 0 : 64 * kb, mn ? 64 * kb : 0, T.adapter, bar);
                 if (two) tma_load_3d(sw + kBox, mw, 64, 64 * kb, T.adapter, bar);
             };
@@ -537,22 +507,34 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
                             abort_flag = 1;
                             break;
                         }
-                        open_stage(kb);
-                        tma_load_2d(base + s * S::kStage, &mx->all, 64 * kb, T.first, full0 + 8 * s);
+                        mbar_arrive_expect_tx(full0 + 8 * s, kXBytes + w_bytes);
+                        mbar_arrive_for_loaders(full0 + 8 * s);
+                        load_w(kb);
+                        tma_load_2d(base + s * S::kStage, mx, 64 * kb, T.first, full0 + 8 * s);
                         if (++s == S::kStages) s = 0, ph ^= 1;
                     }
                 }
                 __syncwarp();
             } else if (!run) {
+                const uint16_t *x = J.x.p;
+                const int64_t ld = J.x.ld;
+                const int cols = J.x.cols;
+                Copier<TM> mine;
+                mine.rows(p.plan.perm + q.tile * TM, T.rows, 32 * loader + lane);
+                loaders_meet();  // the first is here, so nobody is ahead of the ring
                 for (int kb = q.kb; kb < q.kb + q.n; ++kb) {
-                    const bool ok = mbar_wait(empty0 + 8 * s, ph) && !abort_flag;
+                    const bool ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
                     if (!__all_sync(0xffffffffu, ok)) {
                         abort_flag = 1;
                         break;
                     }
-                    if (loader == 0 && elect_one()) open_stage(kb);
+                    if (loader == 0 && elect_one()) {
+                        mbar_arrive_expect_tx(full0 + 8 * s, w_bytes);
+                        load_w(kb);
+                    }
                     __syncwarp();
-                    load_rows<32>(rows, base + s * S::kStage, lane, mx, 64 * kb, full0 + 8 * s);
+                    mine.copy(base + s * S::kStage, x, ld, cols, 64 * kb, false);
+                    mbar_arrive_after_copies(full0 + 8 * s);
                     if (++s == S::kStages) s = 0, ph ^= 1;
                 }
             }
@@ -573,6 +555,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
                 const uint32_t a0 = (uint32_t)smem_desc(base);
                 const uint32_t b0 = mn ? (uint32_t)smem_desc_mn(base + kXBytes) : (uint32_t)smem_desc(base + kXBytes);
                 const uint32_t bstep = mn ? 2048u >> 4 : 32u >> 4;
+                const bool copied = !p.plan.tiles[q.tile].run();
                 for (int i = 0; i < q.n; ++i) {
                     const int b = na & 1;
                     const bool first = i % kSegment == 0;
@@ -581,6 +564,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
                         abort_flag = 1;
                         break;
                     }
+                    if (copied) fence_async_shared();  // the loaders' writes, before the MMA reads them
                     tc_fence_after();
                     const uint32_t at = (uint32_t)s * (S::kStage >> 4);
 #pragma unroll
@@ -699,7 +683,7 @@ __global__ void __launch_bounds__(kFinishThreads) shrink_finish_kernel(const __g
 // (K-major: B_i) or [rank x n] (MN-major: A_i).  Persistent CTAs, each with a
 // run of consecutive units (chunk fastest, so a tile's v stays).
 struct ExpandJob {
-    RowMaps base;
+    Rows base;
     CUtensorMap w, hi, lo, y;  // y: 32 rows x 64 columns
     int n, rank, mn, chunks;
     const int32_t *ranks;
@@ -747,7 +731,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
     if (warp == 1) {
         if (lane == 0) {
             for (int s = 0; s < S::kStages; ++s) {
-                mbar_init(full0 + 8 * s, 1);
+                mbar_init(full0 + 8 * s, kFull);
                 mbar_init(empty0 + 8 * s, kExpandWarps);
             }
             for (int b = 0; b < 2; ++b) {
@@ -816,29 +800,31 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
     const int loader = warp == 0 ? 0 : warp - 1 - kExpandWarps;
     if (warp == 0 || warp >= 2 + kExpandWarps) {
         int s = 0, nv = 0;
-        uint32_t ph = 1, bytes = 0;
-        RowLoad rows{};
+        uint32_t ph = 1;
         bool mn = false, run = false;
-        const RowMaps *mb = nullptr;
-        const CUtensorMap *mw = nullptr;
+        const CUtensorMap *mb = nullptr, *mw = nullptr;
+        const uint16_t *x = nullptr;
+        int64_t ld = 0;
+        int cols = 0;
+        Copier<TM> mine;
         Walk q = start();
         for (int64_t u = u0; u < u1; ++u) {  // to the end in every loader, whatever happens: they meet
             if (q.fresh && q.kind != 0) {
                 const ExpandJob &J = p.job[q.job];
                 mn = J.mn != 0;
-                mb = &J.base;
+                mb = &J.base.box;
                 mw = &J.w;
-                run = q.t.run != 0;
+                x = J.base.p;
+                ld = J.base.ld;
+                cols = J.base.cols;
+                run = q.t.run();
                 if (!run) {
-                    rows = row_load<32>(*reinterpret_cast<const int4 *>(p.plan.perm + q.tile * TM + 4 * lane), lane, q.t.rows,
-                                        false);
-                    if ((lane >> 3) != loader) rows.kind = 0;
-                    loaders_meet();
+                    mine.rows(p.plan.perm + q.tile * TM, q.t.rows, 32 * loader + lane);
+                    loaders_meet();  // the first is here, so nobody is ahead of the ring
                 }
-                bytes = (run ? kBaseBytes : 2 * rows.bytes) + (q.kind == 2 ? S::kW : 0u);
                 if (q.kind == 2 && loader == 0) {
                     const int b = nv % S::kVBufs;
-                    const bool ok = mbar_wait(vempty0 + 8 * b, ((uint32_t)(nv / S::kVBufs) & 1u) ^ 1u) && !abort_flag;
+                    const bool ok = !abort_flag && mbar_wait(vempty0 + 8 * b, ((uint32_t)(nv / S::kVBufs) & 1u) ^ 1u);
                     if (!__all_sync(0xffffffffu, ok)) {
                         abort_flag = 1;
                     } else if (elect_one()) {
@@ -854,37 +840,39 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
                 }
             }
             if (q.kind != 0) {
+                const uint32_t dst = sS + s * S::kStage, bar = full0 + 8 * s;
+                const int c0 = 128 * q.chunk;
+                bool ok = true;
                 if (loader == 0 || !run) {
-                    const bool ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        abort_flag = 1;
-                    } else {
-                        const int c0 = 128 * q.chunk;
-                        const uint32_t dst = sS + s * S::kStage, bar = full0 + 8 * s;
-                        if (loader == 0 && elect_one()) {
-                            mbar_arrive_expect_tx(bar, bytes);
-                            if (run) {
-                                tma_load_2d(dst + S::kW, &mb->all, c0, q.t.first, bar);
-                                tma_load_2d(dst + S::kW + kBaseBytes / 2, &mb->all, c0 + 64, q.t.first, bar);
-                            }
-                            if (q.kind == 2) {
+                    ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) abort_flag = 1;
+                }
+                if (ok && loader == 0 && elect_one()) {
+                    const uint32_t w_bytes = q.kind == 2 ? S::kW : 0u;
+                    mbar_arrive_expect_tx(bar, w_bytes + (run ? kBaseBytes : 0u));
+                    if (run) {
+                        mbar_arrive_for_loaders(bar);
+                        tma_load_2d(dst + S::kW, mb, c0, q.t.first, bar);
+                        tma_load_2d(dst + S::kW + kBaseBytes / 2, mb, c0 + 64, q.t.first, bar);
+                    }
+                    if (q.kind == 2) {
 #pragma unroll
-                                for (int k = 0; k < NK; ++k) {
-                                    if (mn) {  // 64 rows of the rank x 128 columns
-                                        tma_load_3d(dst + (2 * k) * kBox, mw, c0, 64 * k, q.t.adapter, bar);
-                                        tma_load_3d(dst + (2 * k + 1) * kBox, mw, c0 + 64, 64 * k, q.t.adapter, bar);
-                                    } else {  // 128 rows x 64 columns of the rank
-                                        tma_load_3d(dst + k * 2 * kBox, mw, 64 * k, c0, q.t.adapter, bar);
-                                    }
-                                }
+                        for (int k = 0; k < NK; ++k) {
+                            if (mn) {  // 64 rows of the rank x 128 columns
+                                tma_load_3d(dst + (2 * k) * kBox, mw, c0, 64 * k, q.t.adapter, bar);
+                                tma_load_3d(dst + (2 * k + 1) * kBox, mw, c0 + 64, 64 * k, q.t.adapter, bar);
+                            } else {  // 128 rows x 64 columns of the rank
+                                tma_load_3d(dst + k * 2 * kBox, mw, 64 * k, c0, q.t.adapter, bar);
                             }
-                        }
-                        __syncwarp();
-                        if (!run) {
-                            load_rows<32>(rows, dst + S::kW, lane, mb, c0, bar);
-                            load_rows<32>(rows, dst + S::kW + kBaseBytes / 2, lane, mb, c0 + 64, bar);
                         }
                     }
+                }
+                __syncwarp();
+                if (ok && !run) {
+                    mine.copy(dst + S::kW, x, ld, cols, c0, false);
+                    mine.copy(dst + S::kW + kBaseBytes / 2, x, ld, cols, c0 + 64, false);
+                    mbar_arrive_after_copies(bar);
                 }
                 if (++s == S::kStages) s = 0, ph ^= 1;
             }
@@ -1069,7 +1057,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
 // moved 40 KB for 16 KB of x and took 108 us at 8192 tokens).  Shares as in
 // shrink, adapter by adapter.
 struct WgradJob {
-    RowMaps x;
+    Rows x;
     CUtensorMap v[kParts];
     int n, products;  // columns; products of an adapter
     int transposed;   // the gradient is [r][n]
@@ -1142,7 +1130,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
     if (warp == 1) {
         if (lane == 0) {
             for (int s = 0; s < S::kStages; ++s) {
-                mbar_init(full0 + 8 * s, 1);
+                mbar_init(full0 + 8 * s, kFull);
                 mbar_init(empty0 + 8 * s, 1);
             }
             for (int b = 0; b < 2; ++b) {
@@ -1175,8 +1163,9 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
             const Product q = product_at<NK>(p, w);
             const int n = min(q.nkb - q.kb, w1 - w);
             const WgradJob &J = p.job[q.job];
-            const RowMaps *mx = &J.x;
-            const CUtensorMap *mv = J.v;
+            const CUtensorMap *mx = &J.x.box, *mv = J.v;
+            const uint16_t *x = J.x.p;
+            const int64_t ld = J.x.ld;
             const int tile0 = p.plan.tile0[q.adapter], end = q.kb + n;
             Tile T = p.plan.tiles[tile0 + q.kb / 2], next = T;
             for (int kb = q.kb; kb < end; ++kb) {
@@ -1187,39 +1176,36 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
                 }
                 const uint32_t dst = base + s * S::kStage, bar = full0 + 8 * s;
                 const int slot = tile0 * TM + 64 * kb;
-                const bool run = T.run != 0 && T.rows >= 64 * half + 64;
-                RowLoad rows{};
-                if (!run) {  // each loader 64 columns of the 64 slots, with zeros past the adapter's tokens
-                    rows = row_load<16>(*reinterpret_cast<const int4 *>(p.plan.perm + slot + 4 * (lane & 15)), lane,
-                                        T.rows - 64 * half, true);
-                    if (lane > 15 || loader >= 2 * S::kTiles) rows.kind = 0;
-                    loaders_meet();
-                    const bool ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
-                    if (!__all_sync(0xffffffffu, ok)) abort_flag = 1, rows.kind = 0;
+                const bool run = T.run() && T.rows >= 64 * half + 64;
+                if (!run) loaders_meet();  // the first is here, so nobody is ahead of the ring
+                bool ok = true;
+                if (loader == 0 || !run) {
+                    ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) abort_flag = 1;
                 }
-                if (loader == 0) {
-                    bool ok = true;
-                    if (elect_one()) {
-                        ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
-                        if (ok) {
-                            mbar_arrive_expect_tx(bar, S::kStage);
-                            if (run) {
+                if (ok && loader == 0 && elect_one()) {
+                    mbar_arrive_expect_tx(bar, S::kStage - (run ? 0u : S::kX));
+                    if (run) {
+                        mbar_arrive_for_loaders(bar);
 #pragma unroll
-                                for (int c = 0; c < 2 * S::kTiles; ++c)
-                                    tma_load_2d(dst + c * kBox, &mx->all, q.n0 + 64 * c, T.first + 64 * half, bar);
-                            }
-#pragma unroll
-                            for (int i = 0; i < kParts; ++i)
-#pragma unroll
-                                for (int k = 0; k < NK; ++k)
-                                    tma_load_2d(dst + S::kX + (i * NK + k) * kBox, mv + i, 64 * k, slot, bar);
-                        } else {
-                            abort_flag = 1;
-                        }
+                        for (int c = 0; c < 2 * S::kTiles; ++c)
+                            tma_load_2d(dst + c * kBox, mx, q.n0 + 64 * c, T.first + 64 * half, bar);
                     }
-                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                        for (int k = 0; k < NK; ++k)
+                            tma_load_2d(dst + S::kX + (i * NK + k) * kBox, mv + i, 64 * k, slot, bar);
                 }
-                if (!run) load_rows<16>(rows, dst + loader * kBox, lane, mx, q.n0 + 64 * loader, bar);
+                __syncwarp();
+                if (ok && !run) {  // zeros past the adapter's tokens: the slots are what is summed over
+                    Copier<64> mine;
+                    mine.rows(p.plan.perm + slot, T.rows - 64 * half, 32 * loader + lane);
+#pragma unroll
+                    for (int c = 0; c < 2 * S::kTiles; ++c) mine.copy(dst + c * kBox, x, ld, J.x.cols, q.n0 + 64 * c, true);
+                    mbar_arrive_after_copies(bar);
+                }
                 if (++s == S::kStages) s = 0, ph ^= 1;
             }
             w += n;
@@ -1245,6 +1231,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
                         abort_flag = 1;
                         break;
                     }
+                    fence_async_shared();  // the loaders' writes, before the MMA reads them
                     tc_fence_after();
                     const uint32_t at = (uint32_t)s * (S::kStage >> 4), acc = tmem + 256 * ab;
 #pragma unroll
@@ -1444,14 +1431,12 @@ Plan plan_at(const Layout &L, uint8_t *ws)
     return p;
 }
 
-// Rows of a bf16 matrix, 64 columns wide: `all` together, 32, 4, or any 4 gathered.
-cudaError_t encode_rows(RowMaps *m, const void *ptr, int rows, int cols, int64_t ld, int all)
+cudaError_t encode_rows(Rows *m, const uint16_t *ptr, int rows, int cols, int64_t ld, int box)
 {
-    cudaError_t e = encode_2d(&m->all, ptr, rows, cols, ld, true, all);
-    if (e == cudaSuccess) e = encode_2d(&m->box, ptr, rows, cols, ld, true, 32);
-    if (e == cudaSuccess) e = encode_2d(&m->quad, ptr, rows, cols, ld, true, 4);
-    if (e == cudaSuccess) e = encode_2d(&m->gather, ptr, rows, cols, ld, true, 1);
-    return e;
+    m->p = ptr;
+    m->ld = ld;
+    m->cols = cols;
+    return encode_2d(&m->box, ptr, rows, cols, ld, true, box);
 }
 // A dense bf16 [n2][n1][n0] in boxes of box1 x 64.
 cudaError_t encode_3d(CUtensorMap *tm, const void *ptr, int n0, int n1, int n2, int box1)
@@ -1561,7 +1546,7 @@ cudaError_t adapters_mma_forward(const AdaptersArgs &a, const DeviceInfo &dev, c
     sp.status = ep.status = dev.status;
     ep.njobs = a.nproj;
     ep.tokens = a.tokens;
-    RowMaps mx;
+    Rows mx;
     e = encode_rows(&mx, a.x, a.tokens, a.n_in, a.ldx, TM);
     for (int j = 0; j < a.nproj && e == cudaSuccess; ++j) {
         const AdapterProj &P = a.proj[j];
@@ -1614,7 +1599,7 @@ cudaError_t adapters_mma_backward(const AdaptersBwdArgs &b, const DeviceInfo &de
     const Plan plan = plan_at(L, ws);
     const int tiles = most_tiles(b.tokens, b.count);
     uint16_t *v[2][kParts];  // v, then u
-    RowMaps mx, mdy;
+    Rows mx, mdy;
     CUtensorMap mhi, mlo;
     for (int q = 0; q < 2; ++q)
         for (int i = 0; i < kParts; ++i) v[q][i] = reinterpret_cast<uint16_t *>(ws + L.v[q][i]);
@@ -1677,7 +1662,7 @@ cudaError_t adapters_mma_backward(const AdaptersBwdArgs &b, const DeviceInfo &de
         WgradJob &w = wp.job[q];
         w.x = q ? mdy : mx;
         if (e == cudaSuccess)
-            e = encode_2d(&w.x.all, q ? b.dy : b.x, b.tokens, q ? b.n_out : b.n_in, q ? b.lddy : b.ldx, true, 64);
+            e = encode_2d(&w.x.box, q ? b.dy : b.x, b.tokens, q ? b.n_out : b.n_in, q ? b.lddy : b.ldx, true, 64);
         for (int i = 0; i < kParts && e == cudaSuccess; ++i)
             e = encode_2d(&w.v[i], v[1 - q][i], tiles * TM, b.rank, b.rank, true, 64);
         w.n = q ? b.n_out : b.n_in;
