@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     extern __shared__ int hist[];  // [warp][bin]; bin `count`: no adapter
     __shared__ unsigned long long sums[kPlanWarps];
     __shared__ int first_tile[LB_MAX_ADAPTERS + 1], total[LB_MAX_ADAPTERS + 1];
-    __shared__ int16_t held[kHeld];
+    __shared__ int held[kHeld];  // bins, then slots
     const int bins = p.count + 1, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int rounds = (p.tokens + kPlanThreads - 1) / kPlanThreads;
     const int t0 = w * rounds * 32 + lane, bits = 32 - __clz(p.count);
@@ -104,11 +104,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
             ids[i] = t < p.tokens ? __ldg(p.ids + t) : -1;
         }
 #pragma unroll
-        for (int i = 0; i < kHeld / kPlanThreads; ++i) held[i * kPlanThreads + tid] = (int16_t)bin_of(ids[i]);
+        for (int i = 0; i < kHeld / kPlanThreads; ++i) held[i * kPlanThreads + tid] = bin_of(ids[i]);
     }
 #pragma unroll 1
     for (int i = tid; i < kPlanWarps * bins; i += kPlanThreads) hist[i] = 0;
     __syncthreads();
+    auto put = [&](int t, int slot, bool first, bool last) {
+        p.plan.perm[slot] = t;
+        if (first) p.plan.tiles[slot / TM].first = t;
+        if (last) p.plan.tiles[slot / TM].last = t;
+    };
+    constexpr int kFirst = 1 << 30, kLast = 1 << 29;  // of a tile; slots are below
+    bool waited = false;
+    auto wait_once = [&] {
+        if (!waited) {
+            pdl_wait();
+            pdl_launch_dependents();
+        }
+        waited = true;
+    };
+    int all_tiles = 0, tile0 = 0, n = 0, block0 = 0, all_blocks = 0;
     // pass 0 counts each warp's tokens of each bin, pass 1 gives them their slots
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
@@ -131,10 +146,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
                 const int rank = __popc(same & ((1u << lane) - 1u));
                 if (pass == 1) {
                     const int at = had + rank;
-                    p.plan.perm[first_tile[b] * TM + at] = t;
-                    Tile &tile = p.plan.tiles[first_tile[b] + at / TM];
-                    if (at % TM == 0) tile.first = t;
-                    if (at % TM == TM - 1 || at == total[b] - 1) tile.last = t;
+                    if (hold) {  // written with the others, after the wait
+                        held[t] = first_tile[b] * TM + at;
+                        if (at % TM == 0) held[t] |= kFirst;
+                        if (at % TM == TM - 1 || at == total[b] - 1) held[t] |= kLast;
+                    } else {
+                        put(t, first_tile[b] * TM + at, at % TM == 0, at % TM == TM - 1 || at == total[b] - 1);
+                    }
                 }
                 if (rank == 0) mine[b] = had + __popc(same);
             }
@@ -157,7 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         }
         __syncthreads();
         // one sum over the adapters of two 32-bit counts: tiles and blocks
-        const int n = tid < p.count ? total[tid] : 0;
+        n = tid < p.count ? total[tid] : 0;
         const int tiles = (n + TM - 1) / TM;
         const unsigned long long v = (unsigned long long)tiles | (unsigned long long)((n + 63) / 64) << 32;
         unsigned long long inc = v;
@@ -177,33 +195,44 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         const unsigned long long below = __shfl_sync(0xffffffffu, all, max(w - 1, 0));
         all = __shfl_sync(0xffffffffu, all, 31);
         const unsigned long long before = inc - v + (w > 0 ? below : 0);
-        const int all_tiles = (int)all, tile0 = (int)before;
-        pdl_wait();
-        pdl_launch_dependents();
-        if (tid < p.count) {
-            first_tile[tid] = tile0;
-            p.plan.tile0[tid] = tile0;
-            p.plan.tokens[tid] = n;
-            p.plan.block0[tid] = (int)(before >> 32);
-        }
-        if (tid == 0) {
-            first_tile[p.count] = all_tiles;
-            p.plan.counts[0] = all_tiles + (total[p.count] + TM - 1) / TM;
-            p.plan.counts[1] = all_tiles;
-            p.plan.counts[2] = p.plan.block0[p.count] = (int)(all >> 32);
-        }
+        all_tiles = (int)all;
+        tile0 = (int)before;
+        all_blocks = (int)(all >> 32);
+        block0 = (int)(before >> 32);
+        if (tid < p.count) first_tile[tid] = tile0;
+        if (tid == 0) first_tile[p.count] = all_tiles;
+        if (!hold) wait_once();
         __syncthreads();
-#pragma unroll 1
-        for (int b = w; b < bins; b += kPlanWarps) {  // the bin's tiles, and its slots without a token
-            const int m = total[b], at = first_tile[b], end = (m + TM - 1) / TM * TM;
-#pragma unroll 1
-            for (int i = lane; i * TM < m; i += 32) {
-                p.plan.tiles[at + i].adapter = b < p.count ? b : -1;
-                p.plan.tiles[at + i].rows = min(TM, m - i * TM);
-            }
-#pragma unroll 1
-            for (int s = m + lane; s < end; s += 32) p.plan.perm[at * TM + s] = p.tokens;
+    }
+    __syncthreads();
+    wait_once();
+    if (hold) {
+#pragma unroll 2
+        for (int t = tid; t < p.tokens; t += kPlanThreads) {
+            const int v = held[t];
+            put(t, v & (kLast - 1), (v & kFirst) != 0, (v & kLast) != 0);
         }
+    }
+    if (tid < p.count) {
+        p.plan.tile0[tid] = tile0;
+        p.plan.tokens[tid] = n;
+        p.plan.block0[tid] = block0;
+    }
+    if (tid == 0) {
+        p.plan.counts[0] = all_tiles + (total[p.count] + TM - 1) / TM;
+        p.plan.counts[1] = all_tiles;
+        p.plan.counts[2] = p.plan.block0[p.count] = all_blocks;
+    }
+#pragma unroll 1
+    for (int b = w; b < bins; b += kPlanWarps) {  // the bin's tiles, and its slots without a token
+        const int m = total[b], at = first_tile[b], end = (m + TM - 1) / TM * TM;
+#pragma unroll 1
+        for (int i = lane; i * TM < m; i += 32) {
+            p.plan.tiles[at + i].adapter = b < p.count ? b : -1;
+            p.plan.tiles[at + i].rows = min(TM, m - i * TM);
+        }
+#pragma unroll 1
+        for (int s = m + lane; s < end; s += 32) p.plan.perm[at * TM + s] = p.tokens;
     }
 }
 
@@ -321,6 +350,13 @@ struct Copier {
         chunk = tid & 7;
 #pragma unroll
         for (int i = 0; i < kN; ++i) row[i] = r0 + 16 * i < used ? perm[r0 + 16 * i] : -1;
+    }
+    __device__ __forceinline__ void run(int first, int used, int tid)
+    {
+        r0 = tid >> 3;
+        chunk = tid & 7;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) row[i] = r0 + 16 * i < used ? first + r0 + 16 * i : -1;
     }
     __device__ __forceinline__ void copy(uint32_t dst, const uint16_t *p, int64_t ld, int cols, int col, bool strict) const
     {
@@ -649,31 +685,55 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
 constexpr int kFinishThreads = 256, kFinishRows = 16;
 __global__ void __launch_bounds__(kFinishThreads) shrink_finish_kernel(const __grid_constant__ ShrinkParams p)
 {
+    // one thread finds what a unit adds: the index arithmetic of all threads
+    // took longer than the sums
+    struct Found {
+        int tile, job, used, rows, more;  // more: shared sums after the first
+        float scale;
+        const float *first, *rest;
+    };
+    __shared__ Found found;
     pdl_wait();
     pdl_launch_dependents();
-    const int live = p.plan.counts[1];
-    const Shares shares(live * p.per_tile, p.ctas);
-    for (int u = blockIdx.x; u < live * p.njobs * (TM / kFinishRows); u += gridDim.x) {
-        const int product = u / (TM / kFinishRows), tile = product % live, job = product / live;
-        const ShrinkJob &J = p.job[job];
-        int begin = tile * J.nkb;
-        for (int j = 0; j < job; ++j) begin += p.job[j].nkb * live;
-        const int first = shares.owner(begin), last = shares.owner(begin + J.nkb - 1);
-        if (first == last) continue;
-        const Tile T = p.plan.tiles[tile];
-        const int cols = J.rank / 4;
+    const int live = p.plan.counts[1], units = live * p.njobs * (TM / kFinishRows);
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        if (threadIdx.x == 0) {
+            const Shares shares(live * p.per_tile, p.ctas);
+            const int product = u / (TM / kFinishRows), tile = product % live, job = product / live;
+            const ShrinkJob &J = p.job[job];
+            int begin = tile * J.nkb;
+            for (int j = 0; j < job; ++j) begin += p.job[j].nkb * live;
+            const int first = shares.owner(begin), last = shares.owner(begin + J.nkb - 1);
+            found.more = last - first;
+            if (last > first) {
+                const Tile T = p.plan.tiles[tile];
+                found.tile = tile;
+                found.job = job;
+                found.rows = T.rows;
+                found.used = used_rank(J.ranks, J.rank, T.adapter);
+                found.scale = J.scale != nullptr ? __ldg(J.scale + T.adapter) : 1.0f;
+                // the others begin their shares inside the product
+                found.first = p.part + (int64_t)shares.slot(first, begin) * TM * p.part_rank;
+                found.rest = p.part + (int64_t)2 * (first + 1) * TM * p.part_rank;
+            }
+        }
+        __syncthreads();
+        const Found f = found;
+        __syncthreads();
+        if (f.more == 0) continue;
+        const ShrinkJob &J = p.job[f.job];
+        const int cols = J.rank / 4, stride = 2 * TM * p.part_rank;
         for (int i = threadIdx.x; i < kFinishRows * cols; i += kFinishThreads) {
-            const int row = u % (TM / kFinishRows) * kFinishRows + i / cols, c = 4 * (i % cols);
-            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-            for (int k = first; k <= last; ++k) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                    p.part + ((int64_t)shares.slot(k, begin) * TM + row) * p.part_rank + c));
+            const int r = i / cols, row = u % (TM / kFinishRows) * kFinishRows + r, c = 4 * (i - r * cols);
+            const int at = row * p.part_rank + c;
+            float4 s = __ldcg(reinterpret_cast<const float4 *>(f.first + at));
+            const float *q = f.rest + at;
+#pragma unroll 4
+            for (int k = 0; k < f.more; ++k) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(q + (int64_t)k * stride));
                 s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
             }
-            const int used = row < T.rows ? used_rank(J.ranks, J.rank, T.adapter) : 0;
-            const float scale = J.scale != nullptr ? __ldg(J.scale + T.adapter) : 1.0f;
-            store_v(J, ((int64_t)tile * TM + row) * J.rank + c, c, used, scale, s);
+            store_v(J, ((int64_t)f.tile * TM + row) * J.rank + c, c, row < f.rows ? f.used : 0, f.scale, s);
         }
     }
 }
@@ -755,8 +815,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
     pdl_launch_dependents();
 
     const int ntiles = p.plan.counts[0];
-    const int64_t units = (int64_t)ntiles * p.per_tile;
-    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+    const int units = ntiles * p.per_tile;
+    const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
     // Every role walks the same units, job by job, tile by tile.  What a unit
     // needs is in registers but where the tile changes (`fresh`): a parameter
     // read per unit and role costs as much as the unit's products.
@@ -776,11 +836,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
     };
     auto start = [&]() {
         Walk q{};
-        int64_t r = u0;
-        while (u0 < u1 && r >= (int64_t)p.job[q.job].chunks * ntiles) r -= (int64_t)p.job[q.job++].chunks * ntiles;
+        int r = u0;
+        while (u0 < u1 && r >= p.job[q.job].chunks * ntiles) r -= p.job[q.job++].chunks * ntiles;
         if (u0 < u1) {
-            q.tile = (int)(r / p.job[q.job].chunks);
-            q.chunk = (int)(r % p.job[q.job].chunks);
+            q.tile = r / p.job[q.job].chunks;
+            q.chunk = r - q.tile * p.job[q.job].chunks;
             enter(q);
         }
         return q;
@@ -808,7 +868,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
         int cols = 0;
         Copier<TM> mine;
         Walk q = start();
-        for (int64_t u = u0; u < u1; ++u) {  // to the end in every loader, whatever happens: they meet
+        for (int u = u0; u < u1; ++u) {  // to the end in every loader, whatever happens: they meet
             if (q.fresh && q.kind != 0) {
                 const ExpandJob &J = p.job[q.job];
                 mn = J.mn != 0;
@@ -885,7 +945,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
             uint32_t ph = 0, idesc = 0, wstep = 0;
             uint32_t v0 = 0, wd0 = 0;
             Walk q = start();
-            for (int64_t u = u0; u < u1 && !abort_flag; ++u) {
+            for (int u = u0; u < u1 && !abort_flag; ++u) {
                 if (q.fresh && q.kind == 2) {
                     const ExpandJob &J = p.job[q.job];
                     const bool mn = J.mn != 0;
@@ -946,7 +1006,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
         int row0 = 0;
         const CUtensorMap *my = nullptr;
         Walk q = start();
-        for (int64_t u = u0; u < u1; ++u) {
+        for (int u = u0; u < u1; ++u) {
             if (q.fresh) {
                 const ExpandJob &J = p.job[q.job];
                 tok = p.plan.perm[q.tile * TM + row];
@@ -1085,33 +1145,61 @@ struct Wgrad {
 };
 
 // The product at K-block w of all the work: adapter i has block0[i] .. blocks,
-// each of them `per` (products of both jobs) times.
-struct Product {
-    int adapter, job, n0, begin, nkb, kb;
-};
+// each of them `per` (products of both jobs) times.  From one product to the
+// next nothing is read but where the adapter changes: a search for each left
+// the copies idle for two microseconds.
 template <int NK>
-__device__ __forceinline__ Product product_at(const AdapterWgradParams &p, int w)
-{
-    const int per = p.job[0].products + p.job[1].products;
-    int lo = 0, hi = p.count;  // the last adapter with block0 * per <= w (those without blocks come before it)
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.plan.block0[mid] * per <= w)
-            lo = mid;
-        else
-            hi = mid;
+struct Product {
+    const AdapterWgradParams &p;
+    int per, job0, adapter, m, job, n0, begin, nkb, kb, tile0;
+    Tile first;  // the adapter's first tile
+    __device__ __forceinline__ Product(const AdapterWgradParams &params, int w, bool any) : p(params)
+    {
+        if (!any) return;  // a CTA without a share
+        job0 = p.job[0].products;
+        per = job0 + p.job[1].products;
+        int lo = 0, hi = p.count;  // the last adapter with block0 * per <= w (those without blocks come before it)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.plan.block0[mid] * per <= w)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        adapter = lo;
+        const int b0 = enter();
+        m = (w - b0) / nkb;
+        begin = b0 + m * nkb;
+        kb = w - begin;
+        locate();
     }
-    Product q;
-    q.adapter = lo;
-    const int b0 = p.plan.block0[lo] * per;
-    q.nkb = p.plan.block0[lo + 1] - p.plan.block0[lo];
-    const int m = (w - b0) / q.nkb;
-    q.begin = b0 + m * q.nkb;
-    q.kb = w - q.begin;
-    q.job = m >= p.job[0].products;
-    q.n0 = Wgrad<NK>::kCols * (q.job ? m - p.job[0].products : m);
-    return q;
-}
+    __device__ __forceinline__ int enter()
+    {
+        const int b0 = p.plan.block0[adapter];
+        nkb = p.plan.block0[adapter + 1] - b0;
+        tile0 = p.plan.tile0[adapter];
+        first = p.plan.tiles[tile0];
+        return b0 * per;
+    }
+    __device__ __forceinline__ void locate()
+    {
+        job = m >= job0;
+        n0 = Wgrad<NK>::kCols * (job ? m - job0 : m);
+    }
+    __device__ __forceinline__ void advance()  // not past the last one
+    {
+        begin += nkb;
+        kb = 0;
+        if (++m == per) {
+            m = 0;
+            do {
+                ++adapter;
+                enter();
+            } while (nkb == 0);
+        }
+        locate();
+    }
+};
 
 template <int NK>
 __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const __grid_constant__ AdapterWgradParams p)
@@ -1159,15 +1247,17 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
     if (warp == 0 || warp >= 2 + kWgradWarps) {
         int s = 0;
         uint32_t ph = 1;
+        Product<NK> q(p, w0, w0 < w1);
         for (int w = w0; w < w1;) {  // to the end in every loader, whatever happens: they meet
-            const Product q = product_at<NK>(p, w);
             const int n = min(q.nkb - q.kb, w1 - w);
             const WgradJob &J = p.job[q.job];
             const CUtensorMap *mx = &J.x.box, *mv = J.v;
             const uint16_t *x = J.x.p;
             const int64_t ld = J.x.ld;
-            const int tile0 = p.plan.tile0[q.adapter], end = q.kb + n;
-            Tile T = p.plan.tiles[tile0 + q.kb / 2], next = T;
+            const int tile0 = q.tile0, end = q.kb + n;
+            Tile T = q.first;
+            if (q.kb >= 2) T = p.plan.tiles[tile0 + q.kb / 2];
+            Tile next = T;
             for (int kb = q.kb; kb < end; ++kb) {
                 const int half = kb & 1;
                 if (half == 0) T = next;
@@ -1201,7 +1291,10 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
                 __syncwarp();
                 if (ok && !run) {  // zeros past the adapter's tokens: the slots are what is summed over
                     Copier<64> mine;
-                    mine.rows(p.plan.perm + slot, T.rows - 64 * half, 32 * loader + lane);
+                    if (T.run())
+                        mine.run(T.first + 64 * half, T.rows - 64 * half, 32 * loader + lane);
+                    else
+                        mine.rows(p.plan.perm + slot, T.rows - 64 * half, 32 * loader + lane);
 #pragma unroll
                     for (int c = 0; c < 2 * S::kTiles; ++c) mine.copy(dst + c * kBox, x, ld, J.x.cols, q.n0 + 64 * c, true);
                     mbar_arrive_after_copies(bar);
@@ -1209,6 +1302,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
                 if (++s == S::kStages) s = 0, ph ^= 1;
             }
             w += n;
+            if (w < w1) q.advance();
         }
         if (abort_flag) drain_copies();
     } else if (warp == 1) {
@@ -1220,8 +1314,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
             const uint32_t a0 = (uint32_t)smem_desc_mn(base), b0 = (uint32_t)smem_desc_mn(base + S::kX);
             int s = 0, na = 0;  // stage; segments so far
             uint32_t ph = 0;
+            Product<NK> q(p, w0, w0 < w1);
             for (int w = w0; w < w1 && !abort_flag;) {
-                const Product q = product_at<NK>(p, w);
                 const int n = min(q.nkb - q.kb, w1 - w);
                 for (int i = 0; i < n; ++i) {
                     const int ab = na & 1;
@@ -1252,6 +1346,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
                     if (++s == S::kStages) s = 0, ph ^= 1;
                 }
                 w += n;
+                if (w < w1) q.advance();
             }
             umma_commit(drain);
             if (!mbar_wait(drain, 0)) abort_flag = 1;
@@ -1265,8 +1360,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
         const uint32_t lane_at = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(NK == 1 ? 128 * part : 64 * part);
         const int nr = min(64, ((p.rank + 15) & ~15) - c0);
         int na = 0;
+        Product<NK> q(p, w0, w0 < w1);
         for (int w = w0; w < w1;) {
-            const Product q = product_at<NK>(p, w);
             const int n = min(q.nkb - q.kb, w1 - w);
             float sum[64];
 #pragma unroll
@@ -1318,6 +1413,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
                                             c0 + c + 2 < used ? sum[c + 2] : 0.0f, c0 + c + 3 < used ? sum[c + 3] : 0.0f);
                 }
             }
+            if (w < w1) q.advance();
         }
     }
     tc_fence_before();
@@ -1337,45 +1433,60 @@ template <int NK>
 __global__ void __launch_bounds__(kFinishThreads) wgrad_finish_kernel(const __grid_constant__ AdapterWgradParams p)
 {
     constexpr int kCols = Wgrad<NK>::kCols;
+    struct Found {
+        int adapter, job, n0, i0, used, sums;  // sums: shared sums, -1 nothing to do
+        const float *first, *rest;
+    };
+    __shared__ Found found;
     pdl_wait();
     pdl_launch_dependents();
     const int per = p.job[0].products + p.job[1].products;
-    const Shares shares(p.plan.counts[2] * per, p.ctas);
-    const int quads = kCols * p.rank / 4, units = (quads + kQuads - 1) / kQuads;
-    for (int64_t u = blockIdx.x; u < (int64_t)p.count * per * units; u += gridDim.x) {
-        const int adapter = (int)(u / (per * units)), r = (int)(u - (int64_t)adapter * per * units);
-        const int m = r / units, i0 = (r - m * units) * kQuads;
-        const int b0 = p.plan.block0[adapter], nkb = p.plan.block0[adapter + 1] - b0;
-        const int begin = b0 * per + m * nkb;
-        int first = 0, last = -1;
-        if (nkb > 0) {
-            first = shares.owner(begin);
-            last = shares.owner(begin + nkb - 1);
-            if (first == last) continue;
+    const int quads = kCols * p.rank / 4, each = (quads + kQuads - 1) / kQuads, units = p.count * per * each;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        if (threadIdx.x == 0) {
+            const int product = u / each, adapter = product / per, m = product - adapter * per;
+            const int b0 = p.plan.block0[adapter], nkb = p.plan.block0[adapter + 1] - b0;
+            found.sums = 0;
+            if (nkb > 0) {
+                const Shares shares(p.plan.counts[2] * per, p.ctas);
+                const int begin = b0 * per + m * nkb;
+                const int first = shares.owner(begin), last = shares.owner(begin + nkb - 1);
+                found.sums = last > first ? last - first + 1 : -1;
+                found.first = p.part + (int64_t)shares.slot(first, begin) * 4 * quads;
+                found.rest = p.part + (int64_t)2 * (first + 1) * 4 * quads;
+            }
+            found.adapter = adapter;
+            found.job = m >= p.job[0].products;
+            found.n0 = kCols * (found.job ? m - p.job[0].products : m);
+            found.i0 = (u - product * each) * kQuads;
+            found.used = used_rank(p.ranks, p.rank, adapter);
         }
-        const int job = m >= p.job[0].products;
-        const WgradJob &J = p.job[job];
-        const int n0 = kCols * (job ? m - p.job[0].products : m), used = used_rank(p.ranks, p.rank, adapter);
-        float *out = J.out + (int64_t)adapter * p.rank * J.n;
-#pragma unroll 4
-        for (int i = i0 + threadIdx.x; i < min(quads, i0 + kQuads); i += kFinishThreads) {
-            const int n = J.transposed ? 4 * (i % (kCols / 4)) : i / (p.rank / 4);
-            const int c = J.transposed ? i / (kCols / 4) : 4 * (i % (p.rank / 4));
-            if (n0 + n >= J.n) continue;
+        __syncthreads();
+        const Found f = found;
+        __syncthreads();
+        if (f.sums < 0) continue;
+        const WgradJob &J = p.job[f.job];
+        const int N = J.n, used = f.used, cols = p.rank / 4, transposed = J.transposed;
+        float *out = J.out + (int64_t)f.adapter * p.rank * N + (transposed ? f.n0 : (int64_t)f.n0 * p.rank);
+#pragma unroll
+        for (int j = 0; j < kQuads / kFinishThreads; ++j) {
+            const int i = f.i0 + j * kFinishThreads + threadIdx.x;
+            if (i >= quads) break;
+            const int q = transposed ? i / (kCols / 4) : i / cols;  // r, or n
+            const int n = transposed ? 4 * (i - q * (kCols / 4)) : q, c = transposed ? q : 4 * (i - q * cols);
+            if (f.n0 + n >= N) continue;
             float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int k = first; k <= last; ++k) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part) + (int64_t)shares.slot(k, begin) * quads + i);
-                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            if (f.sums > 0) {
+                s = __ldcg(reinterpret_cast<const float4 *>(f.first) + i);
+                for (int k = 0; k < f.sums - 1; ++k) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(f.rest) + (int64_t)k * 2 * quads + i);
+                    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+                }
             }
-            if (J.transposed) {
-                if (c >= used) s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                *reinterpret_cast<float4 *>(out + (int64_t)c * J.n + n0 + n) = s;
-            } else {
-                s = make_float4(c < used ? s.x : 0.0f, c + 1 < used ? s.y : 0.0f, c + 2 < used ? s.z : 0.0f,
-                                c + 3 < used ? s.w : 0.0f);
-                *reinterpret_cast<float4 *>(out + (int64_t)(n0 + n) * p.rank + c) = s;
-            }
+            // zeros past the adapter's rank
+            const int left = transposed ? (c < used ? 4 : 0) : used - c;
+            s = make_float4(left > 0 ? s.x : 0.0f, left > 1 ? s.y : 0.0f, left > 2 ? s.z : 0.0f, left > 3 ? s.w : 0.0f);
+            *reinterpret_cast<float4 *>(out + (transposed ? (int64_t)c * N + n : (int64_t)n * p.rank + c)) = s;
         }
     }
 }
