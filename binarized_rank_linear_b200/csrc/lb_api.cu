@@ -67,7 +67,7 @@ lb_status device_info(lb::DeviceInfo *out)
         return LB_ERR_CUDA;
     }
     if (lb::decode_prepare_device(info) != cudaSuccess || lb::prefill_prepare_device(info) != cudaSuccess ||
-        lb::wgrad_prepare_device(info) != cudaSuccess || lb::adapters_prepare_device(info) != cudaSuccess) {
+        lb::wgrad_prepare_device(info) != cudaSuccess || lb::adapters_prepare_device(info) != cudaSuccess || lb::heads_prepare_device(info) != cudaSuccess) {
         cudaGetLastError();
         return LB_ERR_CUDA;
     }
@@ -759,7 +759,7 @@ static lb_status check_heads(int64_t tokens, int64_t head_dim, int64_t rotary_di
     return LB_OK;
 }
 
-constexpr int64_t kMaxHeads = 4096;
+constexpr int64_t kMaxHeads = 4096, kMaxHeadsLd = int64_t(1) << 30;
 
 lb_status lb_heads_norm_rotate(int64_t tokens, int64_t head_dim, int64_t rotary_dim, lb_rotation rotation,
                                const int32_t *positions, const float *inv_freq, float eps, int ntensors,
@@ -778,6 +778,7 @@ lb_status lb_heads_norm_rotate(int64_t tokens, int64_t head_dim, int64_t rotary_
         if (t.heads < 1 || !t.in || !t.out) return LB_ERR_INVALID_ARGUMENT;
         total += t.heads;
         if (t.heads > kMaxHeads || total > kMaxHeads) return LB_ERR_UNSUPPORTED_SHAPE;
+        if (t.ld_in > kMaxHeadsLd || t.ld_out > kMaxHeadsLd) return LB_ERR_UNSUPPORTED_SHAPE;
         if (t.ld_in < t.heads * head_dim || t.ld_out < t.heads * head_dim) return LB_ERR_INVALID_ARGUMENT;
         if (t.in == t.out && t.ld_in != t.ld_out) return LB_ERR_INVALID_ARGUMENT;
         if (t.ld_in % 8 != 0 || t.ld_out % 8 != 0 || !aligned16(t.in) || !aligned16(t.out) || !aligned16(t.weight))
@@ -832,6 +833,7 @@ lb_status lb_heads_norm_rotate_backward(int64_t tokens, int64_t head_dim, int64_
         if (!aligned16(t.weight) || !aligned4(t.dweight)) return LB_ERR_MISALIGNED;
         if (tokens == 0) continue;
         const int64_t row = t.heads * head_dim;
+        if (t.ld_in > kMaxHeadsLd || t.ld_dout > kMaxHeadsLd || t.ld_din > kMaxHeadsLd) return LB_ERR_UNSUPPORTED_SHAPE;
         if (!t.dout || !t.din || t.ld_dout < row || t.ld_din < row) return LB_ERR_INVALID_ARGUMENT;
         if (t.weight && (!t.in || t.ld_in < row)) return LB_ERR_INVALID_ARGUMENT;
         if (t.din == t.dout && t.ld_din != t.ld_dout) return LB_ERR_INVALID_ARGUMENT;

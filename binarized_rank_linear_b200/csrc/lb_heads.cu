@@ -10,81 +10,133 @@
 //     dw = sum dn (.) x^,   dx = rstd (w (.) dn - x^ mean(w (.) dn (.) x^)).
 //
 // Every element is read and written once and costs a few operations, so DRAM
-// bounds both passes: 4 bytes an element forward, 6 backward.  The kernels
-// therefore keep a head in one pass: L = 8, 16 or 32 lanes hold 8 elements
-// each (both ends of a rotated pair in the same lane, so the rotation needs no
-// exchange), the norm's sum is a shuffle tree, and a CTA loads several heads
-// before it uses the first.  The angles of a CTA's tokens are computed once
-// and shared by all their heads.  An angle is p f / pi in 64 bits, reduced to
-// [-1, 1] before sincospi in 32: a 32-bit product would be wrong in the second
-// digit at positions near 10^6.  All arithmetic on values is fp32; each output
-// is rounded to bf16 once.
+// bounds both passes: 4 bytes an element forward, 6 backward.  What costs next
+// is instructions, and keeping enough bytes under way without them: one thread
+// brings the heads of the next tokens to shared memory by bulk copies, kStages
+// ahead, two warps compute those tokens' angles, once for all their heads, and
+// the other warps take token after token, a few lanes to a head with both ends
+// of a rotated pair in the same lane (so the rotation needs no exchange, and the
+// norm's sum is a shuffle tree), the head's weights in registers, 16 elements a
+// lane where the sizes allow it, else 8.  (For 8192 tokens of 40 + 8 heads of
+// 128: a CTA a token, 63 us; CTAs that stay, with the next tokens in registers,
+// 41 us forward and 86 us backward.)
+// An angle is p f / pi in 64 bits, reduced to [-1, 1] before sincospi in 32: a
+// 32-bit product would be wrong in the second digit at positions near 10^6.
+// All arithmetic on values is fp32; each output is rounded to bf16 once.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "lb_common.cuh"
 #include "lb_internal.h"
+#include "lb_tc.cuh"
 
 namespace lb {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTb = 8;       // tokens of a CTA's block
-constexpr int kUnroll = 3;      // heads a lane group loads before it uses the first
+using namespace tc;
+
+constexpr int kMaxCompute = 384;  // threads that have a head
+constexpr int kAngleWarps = 2;
+constexpr int kStages = 4;
+constexpr int kAngles = 1024;     // most angles of a stage
 
 struct HeadsParams {
     HeadGroup g[kMaxHeadGroups];
-    int first[kMaxHeadGroups + 1];  // forward: first head of each group; backward: first CTA
+    int first[kMaxHeadGroups + 1];  // first head of each tensor
     int ngroups;
-    int tokens, d, rd, tb;
+    int tokens, d, rd;
+    int tb;        // tokens of a stage: more than one where they have few heads
+    int chunk;     // heads of a CTA (grid.y chunks of them)
+    int warps;     // that have heads
+    int row_bytes, stage_bytes;  // a token's heads of one tensor kind (input, or dout); a stage
     const int32_t *positions;
     const float *inv_freq;
     float eps;
-    float *part;  // backward: dw partials [CTA][d]
+    float *part;  // backward: dw partials [CTA][tensor][d]
+    int *status;
 };
 
+// A lane's E elements of a head as rotated pairs (a[i], b[i]).  They lie in two
+// runs of E / 2: with halves the a and the b, with neighbours as pairs (and past
+// the rotated part) the first and the last of the pairs.
+template <int E>
 struct Vals {
-    float v[8];
+    float a[E / 2], b[E / 2];
 };
-
-// The 8 elements of a head that `lane` of L holds: PAIRS (or past the rotated
-// part): 8 lane ..; halves: 4 lane .. and rd/2 + 4 lane ..
-template <bool PAIRS>
-__device__ __forceinline__ void element_offsets(int lane, int rd, int &e0, int &e1)
+template <int E>
+struct Run {
+    uint32_t w[E / 4];
+};
+template <int E>
+__device__ __forceinline__ Run<E> load_run(const uint16_t *p)
 {
-    e0 = 8 * lane;
-    e1 = e0 + 4;
-    if (!PAIRS && 8 * lane < rd) {
-        e0 = 4 * lane;
-        e1 = (rd >> 1) + 4 * lane;
-    }
-}
-
-__device__ __forceinline__ void load8(const uint16_t *p, int e0, int e1, uint2 &a, uint2 &b)
-{
-    a = *reinterpret_cast<const uint2 *>(p + e0);
-    b = *reinterpret_cast<const uint2 *>(p + e1);
-}
-
-__device__ __forceinline__ Vals unpack8(const uint2 &a, const uint2 &b)
-{
-    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
-    Vals r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r.v[2 * i] = __uint_as_float(w[i] << 16);
-        r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    Run<E> r;
+    if constexpr (E == 16)
+        *reinterpret_cast<uint4 *>(r.w) = *reinterpret_cast<const uint4 *>(p);
+    else
+        *reinterpret_cast<uint2 *>(r.w) = *reinterpret_cast<const uint2 *>(p);
     return r;
 }
-
-__device__ __forceinline__ void store8(uint16_t *p, int e0, int e1, const Vals &r)
+__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+template <int E, bool PAIRS>
+__device__ __forceinline__ Vals<E> unpack(const Run<E> &x, const Run<E> &y)
 {
-    *reinterpret_cast<uint2 *>(p + e0) = make_uint2(pack_bf162(r.v[0], r.v[1]), pack_bf162(r.v[2], r.v[3]));
-    *reinterpret_cast<uint2 *>(p + e1) = make_uint2(pack_bf162(r.v[4], r.v[5]), pack_bf162(r.v[6], r.v[7]));
+    Vals<E> v;
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+        if (PAIRS) {
+            v.a[i] = lo_of(x.w[i]);
+            v.b[i] = hi_of(x.w[i]);
+            v.a[E / 4 + i] = lo_of(y.w[i]);
+            v.b[E / 4 + i] = hi_of(y.w[i]);
+        } else {
+            v.a[2 * i] = lo_of(x.w[i]);
+            v.a[2 * i + 1] = hi_of(x.w[i]);
+            v.b[2 * i] = lo_of(y.w[i]);
+            v.b[2 * i + 1] = hi_of(y.w[i]);
+        }
+    }
+    return v;
+}
+template <int E, bool PAIRS>
+__device__ __forceinline__ void store(uint16_t *p, int gap, const Vals<E> &v)
+{
+    Run<E> x, y;
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+        x.w[i] = PAIRS ? pack_bf162(v.a[i], v.b[i]) : pack_bf162(v.a[2 * i], v.a[2 * i + 1]);
+        y.w[i] = PAIRS ? pack_bf162(v.a[E / 4 + i], v.b[E / 4 + i]) : pack_bf162(v.b[2 * i], v.b[2 * i + 1]);
+    }
+    if constexpr (E == 16) {
+        *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(x.w);
+        *reinterpret_cast<uint4 *>(p + gap) = *reinterpret_cast<const uint4 *>(y.w);
+    } else {
+        *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(x.w);
+        *reinterpret_cast<uint2 *>(p + gap) = *reinterpret_cast<const uint2 *>(y.w);
+    }
+}
+// Where in the head pair i's a and b are, for a lane whose runs begin at e0 and e1.
+template <int E, bool PAIRS>
+__device__ __forceinline__ int place(int e0, int e1, int i, bool b)
+{
+    if (PAIRS) return (i < E / 4 ? e0 : e1) + 2 * (i % (E / 4)) + b;
+    return (b ? e1 : e0) + i;
 }
 
+template <int E>
+__device__ __forceinline__ float dot(const Vals<E> &x, const Vals<E> &y)
+{
+    float s = 0.0f, t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+        s = fmaf(x.a[i], y.a[i], s);
+        t = fmaf(x.b[i], y.b[i], t);
+    }
+    return s + t;
+}
 template <int L>
 __device__ __forceinline__ float group_sum(float s)
 {
@@ -93,204 +145,265 @@ __device__ __forceinline__ float group_sum(float s)
     return s;
 }
 
-// Rotates a lane's elements in place by the angles (cos, sin) of its pairs;
-// sgn = -1 is the transpose.  `cs`: this token's [rd / 2].
-template <bool PAIRS>
-__device__ __forceinline__ void rotate8(Vals &r, const float2 *cs, int lane, float sgn)
+// Bulk copy of `bytes` (a multiple of 16) to shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int a = PAIRS ? 2 * i : i, b = PAIRS ? 2 * i + 1 : i + 4;
-        const float2 t = cs[4 * lane + i];
-        const float sn = sgn * t.y;
-        const float x = r.v[a], y = r.v[b];
-        r.v[a] = x * t.x - y * sn;
-        r.v[b] = y * t.x + x * sn;
-    }
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+template <int E>
+__device__ __forceinline__ Run<E> shared_run(uint32_t at)
+{
+    Run<E> r;
+    if constexpr (E == 16)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                     : "r"(at)
+                     : "memory");
+    else
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(at) : "memory");
+    return r;
 }
 
-// cos and sin of the angles of tokens t0 .. t0 + nt - 1 into cs [nt][rd / 2].
-__device__ __forceinline__ void fill_angles(const HeadsParams &p, int t0, int nt, float2 *cs)
+// Rotates a lane's pairs by the angles from `cos` and `sin` on, or back.
+template <int E, bool BACK>
+__device__ __forceinline__ void rotate(Vals<E> &v, const float *cos, const float *sin)
 {
-    const int half = p.rd >> 1;
-    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int tok = i / half;
-        const double turns = (double)__ldg(p.positions + t0 + tok) * (double)__ldg(p.inv_freq + (i - tok * half)) *
-                             0.31830988618379067154;  // angle / pi
-        float s, c;
-        sincospif((float)(turns - 2.0 * rint(0.5 * turns)), &s, &c);
-        cs[i] = make_float2(c, s);
-    }
-}
-
-// One CTA per block of tb tokens; its lane groups take the block's heads (of
-// every tensor, tokens outermost) in turn.
-template <int L, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) heads_forward_kernel(const __grid_constant__ HeadsParams p)
-{
-    constexpr int kSlots = kThreads / L;
-    __shared__ float2 cs[kMaxTb * 128];
-    const int lane = threadIdx.x % L, slot = threadIdx.x / L;
-    const int t0 = blockIdx.x * p.tb, nt = min(p.tb, p.tokens - t0);
-    const int heads = p.first[p.ngroups], rows = nt * heads;
-    const bool on = 8 * lane < p.d;
-    const int ln = on ? lane : 0;  // lanes past a narrow head stay in the shuffles
-    int e0, e1;
-    element_offsets<PAIRS>(ln, p.rd, e0, e1);
-    const int half = p.rd >> 1;
-    fill_angles(p, t0, nt, cs);  // positions and frequencies come before the kernels this one waits for
-    pdl_wait();
-    pdl_launch_dependents();
-    __syncthreads();
-    for (int r0 = slot; r0 - slot < rows; r0 += kSlots * kUnroll) {
-        uint2 a[kUnroll], b[kUnroll];
-        int64_t off[kUnroll];
-        int tok[kUnroll], gi[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int r = min(r0 + u * kSlots, rows - 1);
-            tok[u] = r / heads;
-            const int h = r - tok[u] * heads;
-            int g = 0;
-            while (g + 1 < p.ngroups && h >= p.first[g + 1]) ++g;
-            gi[u] = g;
-            off[u] = (int64_t)(h - p.first[g]) * p.d;
-            load8(p.g[g].in + (int64_t)(t0 + tok[u]) * p.g[g].ld_in + off[u], e0, e1, a[u], b[u]);
-        }
+    for (int i = 0; i < E / 2; i += 4) {
+        const float4 c4 = *reinterpret_cast<const float4 *>(cos + i), s4 = *reinterpret_cast<const float4 *>(sin + i);
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const HeadGroup &G = p.g[gi[u]];
-            Vals x = unpack8(a[u], b[u]);
-            if (G.weight != nullptr || L < 32) {  // a warp's slots may hold heads of different tensors
-                float s = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s += x.v[i] * x.v[i];
-                s = group_sum<L>(on ? s : 0.0f);
-                if (G.weight != nullptr) {
-                    const float rstd = rsqrtf(s / (float)p.d + p.eps);
-                    uint2 wa, wb;
-                    load8(G.weight, e0, e1, wa, wb);
-                    const Vals w = unpack8(wa, wb);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x.v[i] = x.v[i] * rstd * w.v[i];
-                }
-            }
-            if (8 * ln < p.rd) rotate8<PAIRS>(x, cs + tok[u] * half, ln, 1.0f);
-            if (on && r0 + u * kSlots < rows)
-                store8(G.out + (int64_t)(t0 + tok[u]) * G.ld_out + off[u], e0, e1, x);
+        for (int j = 0; j < 4; ++j) {
+            const float x = v.a[i + j], y = v.b[i + j];
+            v.a[i + j] = BACK ? fmaf(y, s[j], x * c[j]) : fmaf(-y, s[j], x * c[j]);
+            v.b[i + j] = BACK ? fmaf(-x, s[j], y * c[j]) : fmaf(x, s[j], y * c[j]);
         }
     }
 }
 
-// CTAs first[g] .. first[g + 1] - 1 take tensor g; each walks over blocks of
-// tb tokens and keeps its lanes' part of dw in registers.
-template <int L, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) heads_backward_kernel(const __grid_constant__ HeadsParams p)
+// CTA (x, y): stages x, x + gridDim.x, ... of p.tb tokens, heads of chunk y.
+// Warps 0 .. p.warps - 1 have heads, L lanes each one of one token of a stage;
+// then the copying warp, then the angles'.
+template <int L, int E, bool PAIRS, bool BACK>
+__global__ void __launch_bounds__(kMaxCompute + 32 * (1 + kAngleWarps), BACK ? 1 : 2)
+    heads_kernel(const __grid_constant__ HeadsParams p)
 {
-    constexpr int kSlots = kThreads / L;
-    __shared__ float2 cs[2][kMaxTb * 128];
-    __shared__ float red[kSlots * 8 * L];
-    const int lane = threadIdx.x % L, slot = threadIdx.x / L;
-    int g = 0;
-    while (g + 1 < p.ngroups && (int)blockIdx.x >= p.first[g + 1]) ++g;
-    const HeadGroup &G = p.g[g];
-    const int cta = blockIdx.x - p.first[g], ctas = p.first[g + 1] - p.first[g];
-    const bool on = 8 * lane < p.d;
-    const int ln = on ? lane : 0;
-    int e0, e1;
-    element_offsets<PAIRS>(ln, p.rd, e0, e1);
-    const int half = p.rd >> 1, heads = G.heads;
-    const bool norm = G.weight != nullptr;
-    Vals w, acc;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc.v[i] = 0.0f, w.v[i] = 1.0f;
-    if (norm) {
-        uint2 wa, wb;
-        load8(G.weight, e0, e1, wa, wb);
-        w = unpack8(wa, wb);
-    }
-    pdl_wait();
-    pdl_launch_dependents();
-    const int blocks = (p.tokens + p.tb - 1) / p.tb;
-    int buf = 0;
-    for (int blk = cta; blk < blocks; blk += ctas, buf ^= 1) {
-        const int t0 = blk * p.tb, nt = min(p.tb, p.tokens - t0), rows = nt * heads;
-        fill_angles(p, t0, nt, cs[buf]);
-        __syncthreads();  // one barrier a block: the other buffer's readers passed the barrier before it
-        for (int r0 = slot; r0 - slot < rows; r0 += kSlots * kUnroll) {
-            uint2 xa[kUnroll], xb[kUnroll], da[kUnroll], db[kUnroll];
-            int64_t off[kUnroll];
-            int tok[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int r = min(r0 + u * kSlots, rows - 1);
-                tok[u] = r / heads;
-                off[u] = (int64_t)(r - tok[u] * heads) * p.d;
-                const int64_t t = t0 + tok[u];
-                load8(G.dout + t * G.ld_dout + off[u], e0, e1, da[u], db[u]);
-                if (norm) load8(G.in + t * G.ld_in + off[u], e0, e1, xa[u], xb[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const bool live = on && r0 + u * kSlots < rows;
-                Vals dn = unpack8(da[u], db[u]);
-                if (8 * ln < p.rd) rotate8<PAIRS>(dn, cs[buf] + tok[u] * half, ln, -1.0f);
-                if (norm) {  // uniform over the CTA
-                    Vals x = unpack8(xa[u], xb[u]);
-                    float ss = 0.0f, sd = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        ss += x.v[i] * x.v[i];
-                        sd += w.v[i] * dn.v[i] * x.v[i];
-                    }
-                    ss = group_sum<L>(on ? ss : 0.0f);
-                    sd = group_sum<L>(on ? sd : 0.0f);
-                    const float rstd = rsqrtf(ss / (float)p.d + p.eps);
-                    const float c = sd * rstd / (float)p.d;  // mean(w dn x^)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float xh = x.v[i] * rstd;
-                        if (live) acc.v[i] += dn.v[i] * xh;
-                        dn.v[i] = rstd * (w.v[i] * dn.v[i] - xh * c);
-                    }
-                }
-                if (live) store8(G.out + (int64_t)(t0 + tok[u]) * G.ld_out + off[u], e0, e1, dn);
-            }
+    extern __shared__ __align__(128) uint8_t shared[];
+    __shared__ alignas(8) unsigned long long bars[2 * kStages];
+    __shared__ int abort_shared;
+    volatile int &abort_flag = abort_shared;
+    const int warp = threadIdx.x >> 5, half = p.rd >> 1, tokens = p.tokens, tb = p.tb;
+    const int heads = p.first[p.ngroups], h0 = blockIdx.y * p.chunk, nh = min(p.chunk, heads - h0);
+    const uint32_t base = smem_u32(shared), full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
+    float *angles = reinterpret_cast<float *>(shared + kStages * p.stage_bytes);  // [stage][cos, sin][tb][half]
+    const int room = tb * half, stride = gridDim.x * tb, t0 = blockIdx.x * tb;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full0 + 8 * s, 1 + (half > 0 ? kAngleWarps : 0));
+            mbar_init(empty0 + 8 * s, p.warps);
         }
-    }
-    if (G.dweight == nullptr) return;  // uniform over the CTA
-    // this CTA's dw: the slots in order
-    if (on) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            red[slot * p.d + e0 + i] = acc.v[i];
-            red[slot * p.d + e1 + i] = acc.v[4 + i];
-        }
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.d; e += kThreads) {
+    pdl_launch_dependents();
+    if (warp == p.warps) {
+        pdl_wait();
+        if ((threadIdx.x & 31) == 0) {
+            int s = 0;
+            uint32_t ph = 1;
+            for (int t = t0; t < tokens; t += stride) {
+                if (!mbar_wait(empty0 + 8 * s, ph) || abort_flag) {
+                    abort_flag = 1;
+                    break;
+                }
+                const int n = min(tb, tokens - t);
+                const uint32_t bar = full0 + 8 * s, dst = base + s * p.stage_bytes;
+                uint32_t tx = 0;
+                for (int g = 0; g < p.ngroups; ++g) {
+                    const int a = max(p.first[g], h0), b = min(p.first[g + 1], h0 + nh);
+                    if (a < b) tx += (uint32_t)(n * (b - a) * p.d * 2) * (!BACK ? 1u : p.g[g].weight != nullptr ? 2u : 1u);
+                }
+                mbar_arrive_expect_tx(bar, tx);
+                for (int g = 0; g < p.ngroups; ++g) {
+                    const HeadGroup &G = p.g[g];
+                    const int a = max(p.first[g], h0), b = min(p.first[g + 1], h0 + nh);
+                    if (a >= b) continue;
+                    const uint32_t bytes = (uint32_t)((b - a) * p.d * 2), at = dst + (uint32_t)((a - h0) * p.d * 2);
+                    const int64_t off = (int64_t)(a - p.first[g]) * p.d;
+                    for (int k = 0; k < n; ++k) {
+                        if (!BACK || G.weight != nullptr)
+                            bulk_load(at + k * p.row_bytes, G.in + (int64_t)(t + k) * G.ld_in + off, bytes, bar);
+                        if (BACK)
+                            bulk_load(at + (tb + k) * p.row_bytes, G.dout + (int64_t)(t + k) * G.ld_dout + off, bytes, bar);
+                    }
+                }
+                if (++s == kStages) s = 0, ph ^= 1;
+            }
+            if (abort_flag) {  // copies in flight land within microseconds
+                const unsigned long long since = globaltimer();
+                while (globaltimer() - since < 200000ull) {
+                }
+            }
+        }
+    } else if (warp > p.warps) {
+        const int tid = threadIdx.x - 32 * (p.warps + 1);
+        int s = 0;
+        uint32_t ph = 1;
+        for (int t = t0; half > 0 && t < tokens; t += stride) {
+            const bool ok = mbar_wait(empty0 + 8 * s, ph) && !abort_flag;
+            if (!__all_sync(0xffffffffu, ok)) {
+                abort_flag = 1;
+                break;
+            }
+            float *cos = angles + 2 * s * room, *sin = cos + room;
+            const int n = min(tb, tokens - t) * half;
+            for (int i = tid; i < n; i += 32 * kAngleWarps) {
+                const int tok = i / half;
+                const double turns = (double)__ldg(p.positions + t + tok) * (double)__ldg(p.inv_freq + (i - tok * half)) *
+                                     0.31830988618379067154;  // angle / pi
+                sincospif((float)(turns - 2.0 * rint(0.5 * turns)), sin + i, cos + i);
+            }
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(full0 + 8 * s);
+            if (++s == kStages) s = 0, ph ^= 1;
+        }
+    }
+    const int lane = threadIdx.x % L, slot = threadIdx.x / L;
+    const bool in_head = E * lane < p.d;
+    const int ln = in_head ? lane : 0;  // lanes past a narrow head stay in the shuffles
+    const bool turned = E * ln < p.rd;
+    const int e0 = !PAIRS && turned ? E / 2 * ln : E * ln, gap = !PAIRS && turned ? half : E / 2;
+    Vals<E> acc;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) acc.a[i] = acc.b[i] = 0.0f;
+    if (warp < p.warps) {
+        const float inv_d = 1.0f / (float)p.d, eps = p.eps;
+        // this lane group's token within a stage (past every token where it has no head) and head
+        const bool on = slot < tb * nh;
+        const int off = on ? slot / nh : tokens, h = h0 + (on ? slot - off * nh : 0);
+        int g = 0;
+        while (g + 1 < p.ngroups && h >= p.first[g + 1]) ++g;
+        const HeadGroup &G = p.g[g];
+        const bool norm = G.weight != nullptr, live0 = on && in_head;
+        const int64_t step = (int64_t)stride * G.ld_out;
+        uint16_t *out = G.out + (int64_t)(h - p.first[g]) * p.d + e0 + (on ? (int64_t)(t0 + off) * G.ld_out : 0);
+        Run<E> w0{}, w1{};
+        if (norm) {
+            w0 = load_run<E>(G.weight + e0);
+            w1 = load_run<E>(G.weight + e0 + gap);
+        }
+        const Vals<E> w = unpack<E, PAIRS>(w0, w1);
+        const bool any_norm = __any_sync(0xffffffffu, norm);
+        const uint32_t mine = base + (uint32_t)((on ? off : 0) * p.row_bytes + ((h - h0) * p.d + e0) * 2), gap2 = 2 * gap;
+        const uint32_t douts = (uint32_t)(tb * p.row_bytes), stage_bytes = p.stage_bytes;
+        const float *cos0 = angles + (on ? off : 0) * half + E / 2 * ln;
+        int s = 0, left = on ? tokens - off : 0;  // tokens from this group's on
+        uint32_t ph = 0;
+        for (int t = t0; t < tokens; t += stride) {
+            const bool ok = mbar_wait(full0 + 8 * s, ph) && !abort_flag;
+            if (!__all_sync(0xffffffffu, ok)) {
+                abort_flag = 1;
+                break;
+            }
+            const uint32_t at = mine + s * stage_bytes;
+            const float *cos = cos0 + 2 * s * room, *sin = cos + room;
+            const bool live = live0 && t < left;
+            if (!BACK) {
+                Vals<E> x = unpack<E, PAIRS>(shared_run<E>(at), shared_run<E>(at + gap2));
+                if (any_norm) {
+                    const float q = group_sum<L>(in_head ? dot(x, x) : 0.0f);
+                    const float rstd = rsqrtf(fmaf(q, inv_d, eps));
+                    if (norm) {
+#pragma unroll
+                        for (int i = 0; i < E / 2; ++i) {
+                            x.a[i] *= rstd * w.a[i];
+                            x.b[i] *= rstd * w.b[i];
+                        }
+                    }
+                }
+                if (turned) rotate<E, false>(x, cos, sin);
+                __syncwarp();
+                if ((threadIdx.x & 31) == 0) mbar_arrive(empty0 + 8 * s);
+                if (live) store<E, PAIRS>(out, gap, x);
+            } else {
+                Vals<E> dn = unpack<E, PAIRS>(shared_run<E>(at + douts), shared_run<E>(at + douts + gap2));
+                if (turned) rotate<E, true>(dn, cos, sin);
+                if (any_norm) {
+                    const Vals<E> x = unpack<E, PAIRS>(shared_run<E>(at), shared_run<E>(at + gap2));
+                    __syncwarp();
+                    if ((threadIdx.x & 31) == 0) mbar_arrive(empty0 + 8 * s);
+                    Vals<E> wd;
+#pragma unroll
+                    for (int i = 0; i < E / 2; ++i) {
+                        wd.a[i] = w.a[i] * dn.a[i];
+                        wd.b[i] = w.b[i] * dn.b[i];
+                    }
+                    const float ss = group_sum<L>(in_head ? dot(x, x) : 0.0f);
+                    const float sd = group_sum<L>(in_head ? dot(wd, x) : 0.0f);
+                    const float rstd = rsqrtf(fmaf(ss, inv_d, eps));
+                    const float c = -sd * rstd * inv_d;  // - mean(w dn x^)
+                    if (norm) {
+#pragma unroll
+                        for (int i = 0; i < E / 2; ++i) {
+                            const float ha = x.a[i] * rstd, hb = x.b[i] * rstd;  // x^
+                            if (live) {
+                                acc.a[i] = fmaf(dn.a[i], ha, acc.a[i]);
+                                acc.b[i] = fmaf(dn.b[i], hb, acc.b[i]);
+                            }
+                            dn.a[i] = rstd * fmaf(ha, c, wd.a[i]);
+                            dn.b[i] = rstd * fmaf(hb, c, wd.b[i]);
+                        }
+                    }
+                } else {
+                    __syncwarp();
+                    if ((threadIdx.x & 31) == 0) mbar_arrive(empty0 + 8 * s);
+                }
+                if (live) store<E, PAIRS>(out, gap, dn);
+            }
+            out += step;
+            if (++s == kStages) s = 0, ph ^= 1;
+        }
+    }
+    __syncthreads();
+    if (abort_flag && threadIdx.x == 0) set_status(p.status, LB_ERR_DEVICE_TIMEOUT);
+    if (!BACK || p.part == nullptr) return;
+    // this CTA's dw of each tensor: the lane groups' in order, where the stages were
+    float *red = reinterpret_cast<float *>(shared);
+    if (slot < tb * nh && in_head) {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            red[slot * p.d + place<E, PAIRS>(e0, e0 + gap, i, false)] = acc.a[i];
+            red[slot * p.d + place<E, PAIRS>(e0, e0 + gap, i, true)] = acc.b[i];
+        }
+    }
+    __syncthreads();
+    const int64_t cta = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    for (int i = threadIdx.x; i < p.ngroups * p.d; i += (int)blockDim.x) {
+        const int q = i / p.d, e = i - q * p.d;
         float s = 0.0f;
-        for (int q = 0; q < kSlots; ++q) s += red[q * p.d + e];
-        p.part[(int64_t)blockIdx.x * p.d + e] = s;
+        for (int k = 0; k < tb; ++k)
+            for (int j = max(p.first[q], h0); j < min(p.first[q + 1], h0 + nh); ++j) s += red[(k * nh + j - h0) * p.d + e];
+        p.part[cta * p.ngroups * p.d + i] = s;
     }
 }
 
-// dweight of tensor blockIdx.y: its CTAs' partial rows, 32 columns a CTA; warp
-// q adds rows q, q + 8, ... and warp 0 the eight sums, always in that order.
-__global__ void __launch_bounds__(256) heads_dweight_kernel(const __grid_constant__ HeadsParams p)
+// dweight of tensor blockIdx.y: its partials of all `ctas`, 32 columns a CTA; warp
+// q adds CTAs q, q + 8, ... and warp 0 the eight sums, always in that order.
+__global__ void __launch_bounds__(256) heads_dweight_kernel(const __grid_constant__ HeadsParams p, int ctas)
 {
     __shared__ float sums[8][32];
     const HeadGroup &G = p.g[blockIdx.y];
-    if (G.dweight == nullptr) {
-        pdl_wait();
-        return;
-    }
     const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
     const int e = blockIdx.x * 32 + lane;
     pdl_wait();
+    if (G.dweight == nullptr) return;
     float s = 0.0f;
     if (e < p.d)
-        for (int r = p.first[blockIdx.y] + q; r < p.first[blockIdx.y + 1]; r += 8) s += p.part[(int64_t)r * p.d + e];
+#pragma unroll 4
+        for (int r = q; r < ctas; r += 8) s += p.part[((int64_t)r * p.ngroups + blockIdx.y) * p.d + e];
     sums[q][lane] = s;
     __syncthreads();
     if (q == 0 && e < p.d) {
@@ -301,25 +414,54 @@ __global__ void __launch_bounds__(256) heads_dweight_kernel(const __grid_constan
     }
 }
 
-template <typename K>
-cudaError_t launch_pdl(K kernel, dim3 grid, const HeadsParams &p, cudaStream_t stream)
+template <typename K, typename... A>
+cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args)
 {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-HeadsParams make_params(const HeadsArgs &a)
+// CTAs of a heads launch: chunks of heads, and for each as many CTAs as the
+// device runs at once, or as there are stages.
+template <int L, int E, bool BACK>
+cudaError_t launch_heads(const HeadsArgs &a, HeadsParams &p, const DeviceInfo &dev, cudaStream_t stream, int *ctas)
 {
-    HeadsParams p{};
-    for (int g = 0; g < a.ngroups; ++g) p.g[g] = a.group[g];
+    const int heads = p.first[a.ngroups], slots = kMaxCompute / L;
+    const int chunks = (heads + slots - 1) / slots;
+    p.chunk = (heads + chunks - 1) / chunks;
+    // tokens of a stage, while every SM still has one
+    const int per_sm = std::max(1, a.tokens / dev.sm_count), half = std::max(1, a.rotary_dim / 2);
+    p.tb = std::max(1, std::min({slots / p.chunk, per_sm, kAngles / half}));
+    p.warps = (p.tb * p.chunk * L + 31) / 32;
+    p.row_bytes = p.chunk * a.head_dim * 2;
+    p.stage_bytes = ((BACK ? 2 : 1) * p.tb * p.row_bytes + 127) & ~127;
+    p.status = dev.status;
+    const size_t smem = (size_t)kStages * ((size_t)p.stage_bytes + sizeof(float) * (size_t)(p.tb * a.rotary_dim));
+    const int stages = (a.tokens + p.tb - 1) / p.tb;
+    dim3 grid((unsigned)std::min(stages, std::max(1, (BACK ? 1 : 2) * dev.sm_count / chunks)), (unsigned)chunks);
+    if (BACK) grid.x = std::min(grid.x, (unsigned)std::max(1, kMaxHeadCtas / chunks));
+    *ctas = (int)(grid.x * grid.y);
+    const int threads = 32 * (p.warps + 1 + kAngleWarps);
+    return a.pairs ? launch_pdl(heads_kernel<L, E, true, BACK>, grid, threads, smem, stream, p)
+                   : launch_pdl(heads_kernel<L, E, false, BACK>, grid, threads, smem, stream, p);
+}
+
+template <bool BACK>
+cudaError_t dispatch_heads(const HeadsArgs &a, HeadsParams &p, const DeviceInfo &dev, cudaStream_t stream, int *ctas)
+{
+    for (int g = 0; g < a.ngroups; ++g) {
+        p.g[g] = a.group[g];
+        p.first[g + 1] = p.first[g] + a.group[g].heads;
+    }
     p.ngroups = a.ngroups;
     p.tokens = a.tokens;
     p.d = a.head_dim;
@@ -327,69 +469,67 @@ HeadsParams make_params(const HeadsArgs &a)
     p.positions = a.positions;
     p.inv_freq = a.inv_freq;
     p.eps = a.eps;
-    return p;
+    const int d = a.head_dim;
+    if (d % 16 == 0 && a.rotary_dim % 16 == 0)
+        return d <= 64    ? launch_heads<4, 16, BACK>(a, p, dev, stream, ctas)
+               : d <= 128 ? launch_heads<8, 16, BACK>(a, p, dev, stream, ctas)
+                          : launch_heads<16, 16, BACK>(a, p, dev, stream, ctas);
+    return d <= 64    ? launch_heads<8, 8, BACK>(a, p, dev, stream, ctas)
+           : d <= 128 ? launch_heads<16, 8, BACK>(a, p, dev, stream, ctas)
+                      : launch_heads<32, 8, BACK>(a, p, dev, stream, ctas);
 }
-
-int lanes_of(int d) { return d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
 }  // namespace
 
-size_t heads_backward_workspace_bytes(int head_dim) { return sizeof(float) * (size_t)kMaxHeadCtas * (size_t)head_dim; }
+// A row of dw partials for each tensor of every CTA (there are at most 256 chunks of heads).
+size_t heads_backward_workspace_bytes(int head_dim)
+{
+    return sizeof(float) * (size_t)kMaxHeadCtas * (size_t)kMaxHeadGroups * (size_t)head_dim;
+}
 
 cudaError_t heads_forward(const HeadsArgs &a, const DeviceInfo &dev, cudaStream_t stream)
 {
-    HeadsParams p = make_params(a);
-    for (int g = 0; g < a.ngroups; ++g) p.first[g + 1] = p.first[g] + a.group[g].heads;
-    const int heads = p.first[a.ngroups], L = lanes_of(a.head_dim), slots = kThreads / L;
-    // tokens a CTA: enough rows for every lane group to load kUnroll heads at
-    // once, while that leaves a CTA for every SM
-    p.tb = std::max(1, std::min({kMaxTb, slots * kUnroll / heads, a.tokens / dev.sm_count}));
-    const dim3 grid((unsigned)((a.tokens + p.tb - 1) / p.tb));
-    const bool pairs = a.pairs != 0;
-    if (L == 8)
-        return pairs ? launch_pdl(heads_forward_kernel<8, true>, grid, p, stream)
-                     : launch_pdl(heads_forward_kernel<8, false>, grid, p, stream);
-    if (L == 16)
-        return pairs ? launch_pdl(heads_forward_kernel<16, true>, grid, p, stream)
-                     : launch_pdl(heads_forward_kernel<16, false>, grid, p, stream);
-    return pairs ? launch_pdl(heads_forward_kernel<32, true>, grid, p, stream)
-                 : launch_pdl(heads_forward_kernel<32, false>, grid, p, stream);
+    HeadsParams p{};
+    int ctas;
+    return dispatch_heads<false>(a, p, dev, stream, &ctas);
 }
 
 cudaError_t heads_backward(const HeadsArgs &a, float *workspace, const DeviceInfo &dev, cudaStream_t stream)
 {
-    HeadsParams p = make_params(a);
-    p.part = workspace;
-    const int L = lanes_of(a.head_dim), slots = kThreads / L;
-    int heads = 0, fewest = 1 << 30;
+    HeadsParams p{};
     bool any = false;
-    for (int g = 0; g < a.ngroups; ++g) {
-        heads += a.group[g].heads;
-        fewest = std::min(fewest, a.group[g].heads);
-        any = any || a.group[g].dweight != nullptr;
-    }
-    p.tb = std::max(1, std::min({kMaxTb, slots * kUnroll / fewest, a.tokens / dev.sm_count}));
-    const int blocks = (a.tokens + p.tb - 1) / p.tb;
-    // about four CTAs an SM, shared out by the tensors' heads
-    const int total = std::min(kMaxHeadCtas - kMaxHeadGroups, 4 * dev.sm_count);
-    for (int g = 0; g < a.ngroups; ++g) {
-        const int n = (int)((int64_t)total * a.group[g].heads / heads);
-        p.first[g + 1] = p.first[g] + std::max(1, std::min(n, blocks));
-    }
-    const dim3 grid((unsigned)p.first[a.ngroups]);
-    const bool pairs = a.pairs != 0;
-    cudaError_t e;
-    if (L == 8)
-        e = pairs ? launch_pdl(heads_backward_kernel<8, true>, grid, p, stream)
-                  : launch_pdl(heads_backward_kernel<8, false>, grid, p, stream);
-    else if (L == 16)
-        e = pairs ? launch_pdl(heads_backward_kernel<16, true>, grid, p, stream)
-                  : launch_pdl(heads_backward_kernel<16, false>, grid, p, stream);
-    else
-        e = pairs ? launch_pdl(heads_backward_kernel<32, true>, grid, p, stream)
-                  : launch_pdl(heads_backward_kernel<32, false>, grid, p, stream);
+    for (int g = 0; g < a.ngroups; ++g) any = any || a.group[g].dweight != nullptr;
+    p.part = any ? workspace : nullptr;
+    int ctas;
+    const cudaError_t e = dispatch_heads<true>(a, p, dev, stream, &ctas);
     if (e != cudaSuccess || !any) return e;
-    return launch_pdl(heads_dweight_kernel, dim3((unsigned)((a.head_dim + 31) / 32), (unsigned)a.ngroups), p, stream);
+    return launch_pdl(heads_dweight_kernel, dim3((unsigned)((a.head_dim + 31) / 32), (unsigned)a.ngroups), 256, 0, stream, p, ctas);
+}
+
+cudaError_t heads_prepare_device(const DeviceInfo &dev)
+{
+    (void)dev;
+    // stages of two tensors of kMaxCompute * 16 elements, and the angles
+    const int bytes = kStages * (2 * kMaxCompute * 16 * 2 + 128 + 2 * kAngles * (int)sizeof(float));
+    cudaError_t e = cudaSuccess;
+    auto allow = [&](auto kernel) {
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    };
+    auto all = [&](auto l, auto n) {
+        constexpr int L = decltype(l)::value, E = decltype(n)::value;
+        allow(heads_kernel<L, E, false, false>);
+        allow(heads_kernel<L, E, true, false>);
+        allow(heads_kernel<L, E, false, true>);
+        allow(heads_kernel<L, E, true, true>);
+    };
+    using std::integral_constant;
+    all(integral_constant<int, 4>{}, integral_constant<int, 16>{});
+    all(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+    all(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+    all(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    all(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+    all(integral_constant<int, 32>{}, integral_constant<int, 8>{});
+    return e;
 }
 
 }  // namespace lb

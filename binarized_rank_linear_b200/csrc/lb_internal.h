@@ -289,6 +289,7 @@ struct HeadsArgs {
 size_t heads_backward_workspace_bytes(int head_dim);
 cudaError_t heads_forward(const HeadsArgs &a, const DeviceInfo &dev, cudaStream_t stream);
 cudaError_t heads_backward(const HeadsArgs &a, float *workspace, const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t heads_prepare_device(const DeviceInfo &dev);
 
 // Either contraction alone, the latent in caller memory: z fp16 [tokens][ldz]
 // (token-major, the paths side by side, path 0 first); any number of tokens
