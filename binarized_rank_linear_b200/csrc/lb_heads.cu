@@ -126,16 +126,47 @@ __device__ __forceinline__ int place(int e0, int e1, int i, bool b)
     return (b ? e1 : e0) + i;
 }
 
+// Two fp32 operations in one instruction, on neighbours of an array.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair_of(const float *v)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v[0]), "f"(v[1]));
+    return r;
+}
+__device__ __forceinline__ f32x2 both(float v)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ void put_pair(float *v, f32x2 p) { asm("mov.b64 {%0, %1}, %2;" : "=f"(v[0]), "=f"(v[1]) : "l"(p)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 template <int E>
 __device__ __forceinline__ float dot(const Vals<E> &x, const Vals<E> &y)
 {
-    float s = 0.0f, t = 0.0f;
+    f32x2 s = mul2(pair_of(x.a), pair_of(y.a)), t = mul2(pair_of(x.b), pair_of(y.b));
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-        s = fmaf(x.a[i], y.a[i], s);
-        t = fmaf(x.b[i], y.b[i], t);
+    for (int i = 2; i < E / 2; i += 2) {
+        s = fma2(pair_of(x.a + i), pair_of(y.a + i), s);
+        t = fma2(pair_of(x.b + i), pair_of(y.b + i), t);
     }
-    return s + t;
+    float f[4];
+    put_pair(f, s);
+    put_pair(f + 2, t);
+    return (f[0] + f[1]) + (f[2] + f[3]);
 }
 template <int L>
 __device__ __forceinline__ float group_sum(float s)
@@ -317,10 +348,11 @@ __global__ void __launch_bounds__(kMaxCompute + 32 * (1 + kAngleWarps), BACK ? 1
                     const float q = group_sum<L>(in_head ? dot(x, x) : 0.0f);
                     const float rstd = rsqrtf(fmaf(q, inv_d, eps));
                     if (norm) {
+                        const f32x2 r2 = both(rstd);
 #pragma unroll
-                        for (int i = 0; i < E / 2; ++i) {
-                            x.a[i] *= rstd * w.a[i];
-                            x.b[i] *= rstd * w.b[i];
+                        for (int i = 0; i < E / 2; i += 2) {
+                            put_pair(x.a + i, mul2(pair_of(x.a + i), mul2(r2, pair_of(w.a + i))));
+                            put_pair(x.b + i, mul2(pair_of(x.b + i), mul2(r2, pair_of(w.b + i))));
                         }
                     }
                 }
@@ -337,24 +369,25 @@ __global__ void __launch_bounds__(kMaxCompute + 32 * (1 + kAngleWarps), BACK ? 1
                     if ((threadIdx.x & 31) == 0) mbar_arrive(empty0 + 8 * s);
                     Vals<E> wd;
 #pragma unroll
-                    for (int i = 0; i < E / 2; ++i) {
-                        wd.a[i] = w.a[i] * dn.a[i];
-                        wd.b[i] = w.b[i] * dn.b[i];
+                    for (int i = 0; i < E / 2; i += 2) {
+                        put_pair(wd.a + i, mul2(pair_of(w.a + i), pair_of(dn.a + i)));
+                        put_pair(wd.b + i, mul2(pair_of(w.b + i), pair_of(dn.b + i)));
                     }
                     const float ss = group_sum<L>(in_head ? dot(x, x) : 0.0f);
                     const float sd = group_sum<L>(in_head ? dot(wd, x) : 0.0f);
                     const float rstd = rsqrtf(fmaf(ss, inv_d, eps));
                     const float c = -sd * rstd * inv_d;  // - mean(w dn x^)
                     if (norm) {
+                        const f32x2 r2 = both(rstd), c2 = both(c);
 #pragma unroll
-                        for (int i = 0; i < E / 2; ++i) {
-                            const float ha = x.a[i] * rstd, hb = x.b[i] * rstd;  // x^
+                        for (int i = 0; i < E / 2; i += 2) {
+                            const f32x2 ha = mul2(pair_of(x.a + i), r2), hb = mul2(pair_of(x.b + i), r2);  // x^
                             if (live) {
-                                acc.a[i] = fmaf(dn.a[i], ha, acc.a[i]);
-                                acc.b[i] = fmaf(dn.b[i], hb, acc.b[i]);
+                                put_pair(acc.a + i, fma2(pair_of(dn.a + i), ha, pair_of(acc.a + i)));
+                                put_pair(acc.b + i, fma2(pair_of(dn.b + i), hb, pair_of(acc.b + i)));
                             }
-                            dn.a[i] = rstd * fmaf(ha, c, wd.a[i]);
-                            dn.b[i] = rstd * fmaf(hb, c, wd.b[i]);
+                            put_pair(dn.a + i, mul2(r2, fma2(ha, c2, pair_of(wd.a + i))));
+                            put_pair(dn.b + i, mul2(r2, fma2(hb, c2, pair_of(wd.b + i))));
                         }
                     }
                 } else {
