@@ -103,6 +103,8 @@ ROTATE_HALVES, ROTATE_PAIRS = 0, 1
 def lib() -> ctypes.CDLL:
     """Load ``liblb.so`` (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -207,9 +209,15 @@ def forward_workspace_bytes(tokens: int, n_in: int, n_out: int, rank_main: int,
 
 # ------------------------------------------------------------------ device calls
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_handle(stream) -> ctypes.c_void_p:
@@ -547,7 +555,7 @@ def _require_rows(t, name: str, rows: int, cols: int, dtype, device) -> int:
     lives on `device`; returns its row stride in elements."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (rows, cols):
+    if tuple(t.shape) != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
@@ -582,6 +590,30 @@ def _held(t, stream):
     if stream is not None:
         t.record_stream(stream)
     return t
+
+
+# A decode step calls these for microseconds of work on the device, so the calls
+# check all of a tensor in one expression and only go through the checks that
+# name the fault when it fails, and allocate by the cheapest of torch's calls.
+
+def _rows_ld(t, name: str, rows: int, cols: int, dtype, device) -> int:
+    """_require_rows, at once where nothing is wrong."""
+    ld, inner = t.stride() if t.ndim == 2 else (0, 0)
+    if inner == 1 and t.dtype is dtype and t.shape == (rows, cols) and t.device == device:
+        return ld if rows > 1 else cols
+    return _require_rows(t, name, rows, cols, dtype, device)
+
+
+def _vector_ptr(t, name: str, n: int, dtype, device) -> int:
+    """_require_vector, at once where nothing is wrong; the vector's address."""
+    if t.dtype is not dtype or t.shape != (n,) or t.device != device or not t.is_contiguous():
+        _require_vector(t, name, n, dtype, device)
+    return t.data_ptr()
+
+
+def _new_workspace(like, need: int, stream):
+    """Scratch of `need` bytes on the device of the bf16 tensor `like`."""
+    return _held(like.new_empty(max(need, 16) + 1 >> 1), stream)
 
 
 @dataclass(frozen=True)
@@ -648,7 +680,7 @@ def adapters_forward(x, ids, pools, bases=None, ys=None, workspace=None, stream=
     device = _current(x, "x")
     _require(x, "x", bf16)
     tokens, n_in = x.shape
-    _require_vector(ids, "ids", tokens, torch.int32, device)
+    ids_ptr = _vector_ptr(ids, "ids", tokens, torch.int32, device)
     n = len(pools)
     if not 1 <= n <= MAX_SIBLINGS:
         raise ValueError(f"1 to {MAX_SIBLINGS} pools, got {n}")
@@ -657,36 +689,40 @@ def adapters_forward(x, ids, pools, bases=None, ys=None, workspace=None, stream=
     if (bases is not None and len(bases) != n) or (ys is not None and len(ys) != n):
         raise ValueError(f"bases and ys must have one tensor for each of the {n} pools")
     arr = (LbAdapterProjection * n)()
-    made = []
+    made, ranks = [], []
     for j, pool in enumerate(pools):
-        pool.as_c()
+        c = pool.as_c()
         if pool.n_in != n_in or pool.device != device:
             raise ValueError(f"pools[{j}] has n_in = {pool.n_in} on {pool.device}, x {n_in} on {device}")
+        ranks.append(c.rank)
         n_out, e = pool.n_out, arr[j]
         e.n_out = n_out
         e.adapters = pool._p
+        if bases is not None:
+            base = bases[j]
+            e.ldbase = _rows_ld(base, f"bases[{j}]", tokens, n_out, bf16, device)
+            e.base = base.data_ptr()
         if ys is None:
-            y = _held(torch.empty((tokens, n_out), dtype=bf16, device=device), stream)
+            y = torch.empty_strided((tokens, n_out), (n_out, 1), dtype=bf16, device=device)
+            if stream is not None:
+                y.record_stream(stream)
             made.append(y)
             e.ldy = n_out
         else:
             y = ys[j]
-            e.ldy = _require_rows(y, f"ys[{j}]", tokens, n_out, bf16, device)
+            e.ldy = _rows_ld(y, f"ys[{j}]", tokens, n_out, bf16, device)
         e.y = y.data_ptr()
-        if bases is not None:
-            e.ldbase = _require_rows(bases[j], f"bases[{j}]", tokens, n_out, bf16, device)
-            e.base = bases[j].data_ptr()
     if workspace is None:
-        need = adapters_workspace_bytes(tokens, n_in, pools[0]._c.count, tuple([p._c.rank for p in pools]))
-        workspace = _held(torch.empty(max(need, 16), dtype=torch.uint8, device=device), stream)
+        workspace = _new_workspace(x, adapters_workspace_bytes(tokens, n_in, c.count, tuple(ranks)), stream)
     else:
         _require_workspace(workspace)
     _check(lib().lb_adapters_forward(
-        x.data_ptr(), tokens, n_in, x.stride(0) if tokens > 1 else n_in, ids.data_ptr(), n, arr, workspace.data_ptr(),
+        x.data_ptr(), tokens, n_in, x.stride(0) if tokens > 1 else n_in, ids_ptr, n, arr, workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream_handle(stream)), "lb_adapters_forward")
     return made if ys is None else ys
 
 
+@functools.lru_cache(maxsize=4096)
 def adapters_backward_workspace_bytes(tokens: int, n_in: int, n_out: int, count: int, rank: int) -> int:
     return int(lib().lb_adapters_backward_workspace_bytes(tokens, n_in, n_out, count, rank))
 
@@ -708,17 +744,17 @@ def adapters_backward(x, dy, ids, pool: AdapterPool, dx_base=None, dx=None, want
     n_out = pool.n_out
     if pool.n_in != n_in or pool.device != device:
         raise ValueError(f"pool has n_in = {pool.n_in} on {pool.device}, x {n_in} on {device}")
-    lddy = _require_rows(dy, "dy", tokens, n_out, bf16, device)
-    _require_vector(ids, "ids", tokens, torch.int32, device)
+    lddy = _rows_ld(dy, "dy", tokens, n_out, bf16, device)
+    ids_ptr = _vector_ptr(ids, "ids", tokens, torch.int32, device)
     if want_dx and dx is None:
         if dx_base is None:
             raise ValueError("give dx_base, or dx to update in place, or want_dx=False")
-        dx = _held(torch.empty((tokens, n_in), dtype=bf16, device=device), stream)
+        dx = _held(torch.empty_strided((tokens, n_in), (n_in, 1), dtype=bf16, device=device), stream)
     if not want_dx:
         dx = None
-    lddx = _require_rows(dx, "dx", tokens, n_in, bf16, device) if dx is not None else n_in
+    lddx = _rows_ld(dx, "dx", tokens, n_in, bf16, device) if dx is not None else n_in
     with_base = dx is not None and dx_base is not None
-    ldbase = _require_rows(dx_base, "dx_base", tokens, n_in, bf16, device) if with_base else n_in
+    ldbase = _rows_ld(dx_base, "dx_base", tokens, n_in, bf16, device) if with_base else n_in
     for name, t, shape in (("da", da, (c.count, c.rank, n_in)), ("db", db, (c.count, n_out, c.rank))):
         if t is not None and (t.dtype != f32 or t.shape != shape or not t.is_contiguous() or t.device != device):
             raise ValueError(f"{name} must be a contiguous {shape} float32 tensor on {device}")
@@ -728,11 +764,11 @@ def adapters_backward(x, dy, ids, pool: AdapterPool, dx_base=None, dx=None, want
         db = _held(torch.empty((c.count, n_out, c.rank), dtype=f32, device=device), stream)
     if workspace is None:
         need = adapters_backward_workspace_bytes(tokens, n_in, n_out, c.count, c.rank)
-        workspace = _held(torch.empty(max(need, 16), dtype=torch.uint8, device=device), stream)
+        workspace = _new_workspace(x, need, stream)
     else:
         _require_workspace(workspace)
     _check(lib().lb_adapters_backward(
-        x.data_ptr(), dy.data_ptr(), tokens, n_in, n_out, x.stride(0) if tokens > 1 else n_in, lddy, ids.data_ptr(),
+        x.data_ptr(), dy.data_ptr(), tokens, n_in, n_out, x.stride(0) if tokens > 1 else n_in, lddy, ids_ptr,
         pool._p, dx_base.data_ptr() if with_base else None, ldbase, dx.data_ptr() if dx is not None else None, lddx,
         da.data_ptr(), db.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _stream_handle(stream)), "lb_adapters_backward")
@@ -776,10 +812,10 @@ def _heads_call(tensors, positions, rotation: HeadRotation, weights, name: str):
     tokens = tensors[0].shape[0]
     if rotation.rotary_dim == 0:
         return device, tokens, None, None
-    _require_vector(positions, "positions", tokens, torch.int32, device)
+    pos = _vector_ptr(positions, "positions", tokens, torch.int32, device)
     if rotation.inv_freq.device != device:
         raise ValueError(f"inv_freq must be on {device}, got {rotation.inv_freq.device}")
-    return device, tokens, positions.data_ptr(), rotation.inv_freq.data_ptr()
+    return device, tokens, pos, rotation.inv_freq.data_ptr()
 
 
 def _heads_of(t, name: str, head_dim: int) -> int:
@@ -805,24 +841,24 @@ def heads_norm_rotate(tensors, positions, rotation: HeadRotation, weights=None, 
         e = arr[j]
         e.heads = _heads_of(t, f"tensors[{j}]", d)
         cols = t.shape[1]
-        e.ld_in = _require_rows(t, f"tensors[{j}]", tokens, cols, bf16, device)
+        e.ld_in = _rows_ld(t, f"tensors[{j}]", tokens, cols, bf16, device)
         e.in_ = t.data_ptr()
         if outs is None:
-            o = _held(torch.empty((tokens, cols), dtype=bf16, device=device), stream)
+            o = _held(torch.empty_strided((tokens, cols), (cols, 1), dtype=bf16, device=device), stream)
             made.append(o)
             e.ld_out = cols
         else:
             o = outs[j]
-            e.ld_out = _require_rows(o, f"outs[{j}]", tokens, cols, bf16, device)
+            e.ld_out = _rows_ld(o, f"outs[{j}]", tokens, cols, bf16, device)
         e.out = o.data_ptr()
         if weights is not None and weights[j] is not None:
-            _require_vector(weights[j], f"weights[{j}]", d, bf16, device)
-            e.weight = weights[j].data_ptr()
+            e.weight = _vector_ptr(weights[j], f"weights[{j}]", d, bf16, device)
     _check(lib().lb_heads_norm_rotate(tokens, d, rotation.rotary_dim, rotation.code, pos, freq, rotation.eps,
                                       len(tensors), arr, _stream_handle(stream)), "lb_heads_norm_rotate")
     return made if outs is None else outs
 
 
+@functools.lru_cache(maxsize=256)
 def heads_backward_workspace_bytes(head_dim: int) -> int:
     return int(lib().lb_heads_backward_workspace_bytes(head_dim))
 
@@ -848,29 +884,27 @@ def heads_norm_rotate_backward(tensors, douts, positions, rotation: HeadRotation
         e = arr[j]
         e.heads = _heads_of(t, f"tensors[{j}]", d)
         cols = t.shape[1]
-        e.ld_in = _require_rows(t, f"tensors[{j}]", tokens, cols, bf16, device)
+        e.ld_in = _rows_ld(t, f"tensors[{j}]", tokens, cols, bf16, device)
         e.in_ = t.data_ptr()
-        e.ld_dout = _require_rows(douts[j], f"douts[{j}]", tokens, cols, bf16, device)
+        e.ld_dout = _rows_ld(douts[j], f"douts[{j}]", tokens, cols, bf16, device)
         e.dout = douts[j].data_ptr()
         if dins is None:
-            din = _held(torch.empty((tokens, cols), dtype=bf16, device=device), stream)
+            din = _held(torch.empty_strided((tokens, cols), (cols, 1), dtype=bf16, device=device), stream)
             e.ld_din = cols
         else:
             din = dins[j]
-            e.ld_din = _require_rows(din, f"dins[{j}]", tokens, cols, bf16, device)
+            e.ld_din = _rows_ld(din, f"dins[{j}]", tokens, cols, bf16, device)
         e.din = din.data_ptr()
         out.append({"din": din})
         if weights is not None and weights[j] is not None:
-            _require_vector(weights[j], f"weights[{j}]", d, bf16, device)
-            e.weight = weights[j].data_ptr()
+            e.weight = _vector_ptr(weights[j], f"weights[{j}]", d, bf16, device)
             if want_dweight:
-                dw = _held(torch.empty((d,), dtype=torch.float32, device=device), stream)
+                dw = _held(torch.empty_strided((d,), (1,), dtype=torch.float32, device=device), stream)
                 e.dweight = dw.data_ptr()
                 out[j]["dweight"] = dw
                 sums = True
     if workspace is None:
-        workspace = _held(torch.empty(max(heads_backward_workspace_bytes(d), 16) if sums else 16, dtype=torch.uint8,
-                                      device=device), stream)
+        workspace = _new_workspace(tensors[0], heads_backward_workspace_bytes(d) if sums else 0, stream)
     else:
         _require_workspace(workspace)
     _check(lib().lb_heads_norm_rotate_backward(tokens, d, rotation.rotary_dim, rotation.code, pos, freq, rotation.eps, n,
