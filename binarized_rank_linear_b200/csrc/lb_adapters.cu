@@ -1,22 +1,28 @@
 // lb_adapters.cu - low-rank adapters of many requests beside a shared
-// projection: the dispatch by token count and the CUDA-core kernels for small
-// batches.
+// projection: the dispatch by token count and the kernels for small batches.
 //
 //     y[m] = base[m] + s_i B_i (A_i x[m]),  i = ids[m]
 //
 // At decode a batch reads the adapters its tokens use and little else: 2 r (n_in
-// + n_out) bytes an adapter against 4 r (n_in + n_out) operations a token, far
-// below what DRAM or the launches cost, so the products run on CUDA cores in
-// fp32 straight from the weights as they lie.  Two launches:
-//   shrink  a CTA takes up to kGroup tokens of one adapter and a slice of n_in;
-//           a warp per row of A, 16 bytes a lane, the slice's x of those tokens
-//           in shared memory; v partials [slice][token][rank] in fp32
-//   expand  a CTA takes the same tokens and 256 outputs: a thread per output
-//           row of B, the tokens' v (the slices added in order, scaled) in
-//           shared memory
-// Tokens that share an adapter thus read its weights once per kGroup of them,
-// wherever they stand in the batch.  Both launches fetch their weights before
-// they wait for the launch they depend on (programmatic dependent launch).
+// + n_out) bytes an adapter against 4 r (n_in + n_out) operations a token.  What
+// counts is how few round trips to memory the two launches make:
+//   shrink  a CTA takes up to kGroup tokens of one adapter, 16 rows of A and
+//           1024 columns; a warp 128 of the columns; v partials
+//           [slice][token][rank] in fp32
+//   expand  a CTA takes the same tokens and 256 outputs, a warp 32 of them; the
+//           slices are added in order, scaled, and split for the products
+// The tokens are the 16 rows of register matrix products (m16n8k16) whose
+// operands come straight from memory: which column is which k does not matter to
+// a product as long as both operands agree, so a lane takes 16 bytes at once - 8
+// columns of one row - and feeds them to two products.  Everything a CTA reads is
+// asked for at once; weights before the launch this one depends on has finished
+// (programmatic dependent launch).  (fp32 FMAs on CUDA cores in place of the
+// products, a thread a row of B: 44 us for the expand of 100 tokens, 16 adapters
+// of rank 32 and 34816 outputs, most of it spent unpacking and on 16-byte pieces
+// of 32 rows at a time.)
+// Tokens that share an adapter read its weights once per kGroup of them, wherever
+// they stand in the batch.  CTA y of either launch finds the y-th group for
+// itself; there are no more of them than adapters and full groups.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -29,61 +35,81 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroup = 8;       // tokens of one adapter that a CTA takes together
-constexpr int kStep = 256;      // columns of A a warp reads at once (16 bytes a lane)
-constexpr int kMaxSteps = 4;    // steps of a shrink CTA's slice
-static_assert(kAdapterSmallTokens <= kThreads, "one thread for each token looks for its adapter");
+constexpr int kGroup = 16;             // tokens of one adapter that a CTA takes together
+constexpr int kRows = 16;              // rows of A of a shrink CTA
+constexpr int kWarpCols = 128;         // columns of A of a shrink warp
+constexpr int kSlice = kWarps * kWarpCols;
+constexpr int kWarpOuts = 32;          // outputs of an expand warp
+constexpr int kOutputs = kWarps * kWarpOuts;
+static_assert(kAdapterSmallTokens <= kThreads && kAdapterSmallTokens % 4 == 0, "one thread for each token looks for its adapter");
+static_assert(kGroup * kRows == kThreads, "one thread for each partial of a shrink CTA");
 
 struct SmallParams {
     const uint16_t *x;
     int64_t ldx;
     const int32_t *ids;
-    int tokens, n_in, count, steps, slices;
+    int tokens, n_in, count, slices;
     AdapterProj proj[kMaxSiblings];
     float *part[kMaxSiblings];        // [slice][token][rank]
-    int chunk0[kMaxSiblings + 1];     // expand: first 256-output chunk of each projection
+    int chunk0[kMaxSiblings + 1];     // expand: first chunk of kOutputs of each projection
+    int row0[kMaxSiblings + 1];       // shrink: first kRows rows of each projection
     int nproj;
     int *status;
 };
 
-// The tokens of this CTA: blockIdx.y = m leads a group when the number of
-// earlier tokens with m's adapter is a multiple of kGroup; it then takes m and
-// the next ones, up to kGroup.  Returns their number, 0 for a CTA that leads
-// none; `id` is the adapter, or -1.  One thread per token; ends in a barrier.
+// The tokens of this CTA, group blockIdx.y: the adapters' tokens in order, cut
+// every kGroup; a group stands where its first token does.  Returns their
+// number, 0 where there is no such group; `id` is the adapter, or -1.  One
+// thread per token.
 struct Group {
     int tok[kGroup];
+    int id, size;
 };
-__device__ __forceinline__ int find_group(const SmallParams &p, Group &g, uint32_t *masks, int &id)
+__device__ __forceinline__ int find_group(const SmallParams &p, Group &g, int *ids, uint32_t *masks, int &id)
 {
-    const int m = blockIdx.y, t = threadIdx.x, lane = t & 31, w = t >> 5;
-    int mine = __ldg(p.ids + m);
-    if (mine >= p.count) {
-        if (t == 0 && blockIdx.x == 0 && blockIdx.z == 0) set_status(p.status, LB_ERR_INVALID_ARGUMENT);
-        mine = -1;
-    }
-    id = mine < 0 ? -1 : mine;
-    int other = -2;
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    int mine = -1;
     if (t < p.tokens) {
-        other = __ldg(p.ids + t);
-        if (other < 0 || other >= p.count) other = -1;
+        mine = __ldg(p.ids + t);
+        if (mine >= p.count) {
+            if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) set_status(p.status, LB_ERR_INVALID_ARGUMENT);
+            mine = -1;
+        }
+        mine = max(mine, -1);
     }
-    const bool eq = other == id;
-    const uint32_t mask = __ballot_sync(0xffffffffu, eq);
+    if (p.tokens == 1) {
+        if (t == 0) g.tok[0] = 0, g.id = mine;
+        __syncthreads();
+        id = g.id;
+        return 1;
+    }
+    if (t < kAdapterSmallTokens) ids[t] = t < p.tokens ? mine : -2;
+    if (t == 0) g.size = 0;
+    __syncthreads();
+    int before = 0;  // earlier tokens of the same adapter
+    if (t < p.tokens) {
+        for (int j = 0; j < t; j += 4) {  // ids past the last token are no token's
+            const int4 v = *reinterpret_cast<const int4 *>(ids + j);
+            before += (v.x == mine) + (v.y == mine && j + 1 < t) + (v.z == mine && j + 2 < t) + (v.w == mine && j + 3 < t);
+        }
+    }
+    const bool leads = t < p.tokens && before % kGroup == 0;
+    const uint32_t mask = __ballot_sync(0xffffffffu, leads);
     if (lane == 0) masks[w] = mask;
     __syncthreads();
-    int before = 0, total = 0, upto = 0;  // matches before m, in all, and before t
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        const uint32_t k = masks[i];
-        total += __popc(k);
-        before += __popc(i < (m >> 5) ? k : i == (m >> 5) ? k & ((1u << (m & 31)) - 1u) : 0u);
-        upto += __popc(i < w ? k : i == w ? k & ((1u << lane) - 1u) : 0u);
+    int at = __popc(mask & ((1u << lane) - 1u));  // groups led before t
+    for (int i = 0; i < w; ++i) at += __popc(masks[i]);
+    if (leads && at == (int)blockIdx.y) {
+        g.id = mine;
+        g.size = 1 + before;  // for now: where the group begins among its adapter's tokens
     }
-    if (before % kGroup != 0) return 0;
-    const int n = min(kGroup, total - before);
-    if (eq && upto >= before && upto < before + n) g.tok[upto - before] = t;
     __syncthreads();
-    return n;
+    const int from = g.size - 1;
+    if (from < 0) return 0;
+    id = g.id;
+    const bool in = t < p.tokens && mine == id && before >= from && before < from + kGroup;
+    if (in) g.tok[before - from] = t;
+    return __syncthreads_count(in);
 }
 
 __device__ __forceinline__ int rank_of(const AdapterProj &P, int id)
@@ -91,176 +117,176 @@ __device__ __forceinline__ int rank_of(const AdapterProj &P, int id)
     return P.ranks == nullptr ? P.rank : max(0, min(P.rank, __ldg(P.ranks + id)));
 }
 
-__device__ __forceinline__ void fma8(float &acc, const uint4 &w, const uint4 &x)
+// d += A B of 16 rows (tokens), 8 columns and 16 k.  A lane holds of A the rows
+// lane / 4 and lane / 4 + 8, of B the column lane / 4, of d those rows and the
+// columns 2 (lane % 4) and the next; of k each lane % 4 has four.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w}, b[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        acc += __uint_as_float(a[i] << 16) * __uint_as_float(b[i] << 16);
-        acc += __uint_as_float(a[i] & 0xffff0000u) * __uint_as_float(b[i] & 0xffff0000u);
-    }
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same over 32 k: `lo` and `hi` are 16 bytes of A's two rows, b of B's column.
+__device__ __forceinline__ void mma32(float (&d)[4], const uint4 &lo, const uint4 &hi, const uint4 &b)
+{
+    mma(d, lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+    mma(d, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
 }
 
-// grid (slices, tokens, projections)
+// grid (slices, groups, rows of every projection's A by kRows)
 __global__ void __launch_bounds__(kThreads) small_shrink_kernel(const __grid_constant__ SmallParams p)
 {
     __shared__ Group grp;
     __shared__ uint32_t masks[kWarps];
-    __shared__ uint4 xs[kGroup][kMaxSteps * 32];
-    int id;
-    const int n = find_group(p, grp, masks, id);
-    const AdapterProj &P = p.proj[blockIdx.z];
+    __shared__ alignas(16) int ids[kAdapterSmallTokens];
+    __shared__ float red[kWarps][kGroup][kRows + 2];
+    int id = -1;
+    const int n = find_group(p, grp, ids, masks, id);
+    int j = 0;
+    while (j + 1 < p.nproj && (int)blockIdx.z >= p.row0[j + 1]) ++j;
+    const AdapterProj &P = p.proj[j];
+    const int r0 = ((int)blockIdx.z - p.row0[j]) * kRows;
     const int rank = n > 0 && id >= 0 ? rank_of(P, id) : 0;
-    if (rank == 0) {  // uniform over the CTA
+    if (r0 >= rank) {  // uniform over the CTA
         pdl_wait();
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int k0 = blockIdx.x * p.steps * kStep + 8 * lane;
-    const uint16_t *a = P.a + (int64_t)id * P.rank * p.n_in;
+    const int k0 = blockIdx.x * kSlice + warp * kWarpCols + 8 * (lane & 3);
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    auto load_row = [&](int r, uint4(&w)[kMaxSteps]) {
+    constexpr int kSteps = kWarpCols / 32;
+    uint4 w[kSteps][2], lo[kSteps], hi[kSteps];
+    const int row = r0 + (lane >> 2);  // and the one 8 below
+    const uint16_t *a = P.a + ((int64_t)id * P.rank + row) * p.n_in + k0;
 #pragma unroll
-        for (int s = 0; s < kMaxSteps; ++s) {
-            const int k = k0 + s * kStep;
-            w[s] = r < rank && s < p.steps && k < p.n_in ? ldg_early_v4(a + (int64_t)r * p.n_in + k) : zero;
-        }
-    };
-    uint4 w0[kMaxSteps], w1[kMaxSteps];
-    load_row(warp, w0);  // weights do not depend on the launch before
-    load_row(warp + kWarps, w1);
+    for (int s = 0; s < kSteps; ++s) {
+        const bool in = k0 + 32 * s < p.n_in;
+        w[s][0] = in && row < rank ? ldg_early_v4(a + 32 * s) : zero;
+        w[s][1] = in && row + 8 < rank ? ldg_early_v4(a + (int64_t)8 * p.n_in + 32 * s) : zero;
+    }
     pdl_wait();
     pdl_launch_dependents();
-    for (int i = threadIdx.x; i < n * p.steps * 32; i += kThreads) {
-        const int g = i / (p.steps * 32), c = i - g * (p.steps * 32);
-        const int k = blockIdx.x * p.steps * kStep + 8 * c;
-        xs[g][c] = k < p.n_in ? *reinterpret_cast<const uint4 *>(p.x + (int64_t)grp.tok[g] * p.ldx + k) : zero;
+    const int t0 = lane >> 2, t1 = t0 + 8;
+    const uint16_t *x0 = p.x + (int64_t)grp.tok[t0 < n ? t0 : 0] * p.ldx + k0;
+    const uint16_t *x1 = p.x + (int64_t)grp.tok[t1 < n ? t1 : 0] * p.ldx + k0;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const bool in = k0 + 32 * s < p.n_in;
+        lo[s] = in && t0 < n ? *reinterpret_cast<const uint4 *>(x0 + 32 * s) : zero;
+        hi[s] = in && t1 < n ? *reinterpret_cast<const uint4 *>(x1 + 32 * s) : zero;
+    }
+    float d[2][4] = {};
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        mma32(d[0], lo[s], hi[s], w[s][0]);
+        mma32(d[1], lo[s], hi[s], w[s][1]);
+    }
+    const int c = 2 * (lane & 3);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        *reinterpret_cast<float2 *>(&red[warp][t0][8 * h + c]) = make_float2(d[h][0], d[h][1]);
+        *reinterpret_cast<float2 *>(&red[warp][t1][8 * h + c]) = make_float2(d[h][2], d[h][3]);
     }
     __syncthreads();
-    float *part = p.part[blockIdx.z] + (int64_t)blockIdx.x * p.tokens * P.rank;
-    for (int r = warp; r < rank; r += 2 * kWarps) {
-        if (r != warp) {
-            load_row(r, w0);
-            load_row(r + kWarps, w1);
-        }
-        for (int g = 0; g < n; ++g) {
-            float s0 = 0.0f, s1 = 0.0f;
+    const int g = threadIdx.x / kRows, r = threadIdx.x % kRows;
+    float v = 0.0f;
 #pragma unroll
-            for (int s = 0; s < kMaxSteps; ++s) {
-                if (s < p.steps) {
-                    const uint4 xv = xs[g][32 * s + lane];
-                    fma8(s0, w0[s], xv);
-                    fma8(s1, w1[s], xv);
-                }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-                s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-            }
-            if (lane == 0) {
-                float *v = part + (int64_t)grp.tok[g] * P.rank + r;
-                v[0] = s0;
-                if (r + kWarps < rank) v[kWarps] = s1;
-            }
-        }
-    }
+    for (int i = 0; i < kWarps; ++i) v += red[i][g][r];
+    if (g < n && r0 + r < rank)
+        p.part[j][((int64_t)blockIdx.x * p.tokens + grp.tok[g]) * P.rank + r0 + r] = v;
 }
 
-// grid (256-output chunks of every projection, tokens)
+// grid (chunks of kOutputs of every projection, groups); KS: 32 columns of B are
+// a step, and `rank` has at most KS of them.
+template <int KS>
 __global__ void __launch_bounds__(kThreads) small_expand_kernel(const __grid_constant__ SmallParams p)
 {
     __shared__ Group grp;
     __shared__ uint32_t masks[kWarps];
-    __shared__ alignas(16) float vs[kGroup][LB_MAX_ADAPTER_RANK];
-    int id;
-    const int n = find_group(p, grp, masks, id);
+    __shared__ alignas(16) int ids[kAdapterSmallTokens];
+    // s_i v in three bf16 parts, 24 bits: nothing of the fp32 value is lost
+    constexpr int kPitch = 32 * KS + 8;  // 16-byte reads of 8 rows fall into 8 different bank groups
+    __shared__ alignas(16) uint16_t vs[3][kGroup][kPitch];
+    int id = -1;
+    const int n = find_group(p, grp, ids, masks, id);
     int j = 0;
     while (j + 1 < p.nproj && (int)blockIdx.x >= p.chunk0[j + 1]) ++j;
     const AdapterProj &P = p.proj[j];
-    const int o = ((int)blockIdx.x - p.chunk0[j]) * kThreads + threadIdx.x;
     const int rank = n > 0 && id >= 0 ? rank_of(P, id) : 0;
     if (n == 0 || (rank == 0 && P.base == P.y)) {  // uniform over the CTA
         pdl_wait();
         return;
     }
-    const bool on = o < P.n_out;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int out0 = ((int)blockIdx.x - p.chunk0[j]) * kOutputs + warp * kWarpOuts;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint16_t *b = P.b + ((int64_t)max(id, 0) * P.n_out + o) * P.rank;
-    constexpr int kPre = 4;
-    uint4 w[kPre];
+    // Column g of product b is output 8 (g / 2) + 2 b + g % 2 of the warp's, so that
+    // a lane's columns of the four products are 8 outputs in a row, from 8 q on.
+    uint4 w[KS][4];
 #pragma unroll
-    for (int q = 0; q < kPre; ++q) w[q] = on && 8 * q < rank ? ldg_early_v4(b + 8 * q) : zero;
+    for (int b = 0; b < 4; ++b) {
+        const int o = out0 + 8 * (g >> 1) + 2 * b + (g & 1);
+        const uint16_t *B = P.b + ((int64_t)max(id, 0) * P.n_out + o) * P.rank + 8 * q;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) w[k][b] = o < P.n_out && 32 * k + 8 * q < rank ? ldg_early_v4(B + 32 * k) : zero;
+    }
     const float scale = P.scale != nullptr && rank > 0 ? __ldg(P.scale + id) : 1.0f;
     pdl_wait();
     pdl_launch_dependents();
-    float acc[kGroup];
+    const int o = out0 + 8 * q;
+    uint4 y[2] = {zero, zero};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (o < P.n_out && g + 8 * h < n)
+            y[h] = *reinterpret_cast<const uint4 *>(P.base + (int64_t)grp.tok[g + 8 * h] * P.ldbase + o);
     if (rank > 0) {
-        const int r8 = (rank + 7) & ~7;
-        for (int i = threadIdx.x; i < n * r8; i += kThreads) {
-            const int g = i / r8, r = i - g * r8;
-            const float *v = p.part[j] + (int64_t)grp.tok[g] * P.rank + r;
-            float s = 0.0f;
-            if (r < rank)
-                for (int q = 0; q < p.slices; ++q) s += v[(int64_t)q * p.tokens * P.rank];
-            vs[g][r] = s * scale;
+        const int64_t next = (int64_t)p.tokens * P.rank;
+        for (int i = threadIdx.x; i < n * 32 * KS; i += kThreads) {
+            const int t = i / (32 * KS), r = i % (32 * KS);
+            float v = 0.0f;
+            if (r < rank) {
+                const float *part = p.part[j] + (int64_t)grp.tok[t] * P.rank + r;
+#pragma unroll 4
+                for (int s = 0; s < p.slices; ++s) v += part[s * next];
+            }
+            v *= scale;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {  // truncated, so that no part can overflow
+                const uint32_t top = __float_as_uint(v) & 0xffff0000u;
+                vs[k][t][r] = (uint16_t)(top >> 16);
+                v = isfinite(v) ? v - __uint_as_float(top) : 0.0f;
+            }
         }
         __syncthreads();
+        float d[4][4] = {};
 #pragma unroll
-        for (int g = 0; g < kGroup; ++g) acc[g] = 0.0f;
-        for (int q0 = 0; 8 * q0 < rank; q0 += kPre) {
-            if (q0 > 0) {
+        for (int k = 0; k < KS; ++k) {
+            if (32 * k < rank) {
 #pragma unroll
-                for (int q = 0; q < kPre; ++q) w[q] = on && 8 * (q0 + q) < rank ? ldg_early_v4(b + 8 * (q0 + q)) : zero;
-            }
+                for (int i = 0; i < 3; ++i) {
+                    const uint4 lo = g < n ? *reinterpret_cast<const uint4 *>(&vs[i][g][32 * k + 8 * q]) : zero;
+                    const uint4 hi = g + 8 < n ? *reinterpret_cast<const uint4 *>(&vs[i][g + 8][32 * k + 8 * q]) : zero;
 #pragma unroll
-            for (int q = 0; q < kPre; ++q) {
-                if (8 * (q0 + q) < rank) {
-                    const uint32_t k[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
-                    float f[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        f[2 * i] = __uint_as_float(k[i] << 16);
-                        f[2 * i + 1] = __uint_as_float(k[i] & 0xffff0000u);
-                    }
-#pragma unroll
-                    for (int g = 0; g < kGroup; ++g) {
-                        if (g < n) {
-                            const float4 v0 = *reinterpret_cast<const float4 *>(&vs[g][8 * (q0 + q)]);
-                            const float4 v1 = *reinterpret_cast<const float4 *>(&vs[g][8 * (q0 + q) + 4]);
-                            acc[g] += f[0] * v0.x + f[1] * v0.y + f[2] * v0.z + f[3] * v0.w + f[4] * v1.x + f[5] * v1.y +
-                                      f[6] * v1.z + f[7] * v1.w;
-                        }
-                    }
+                    for (int b = 0; b < 4; ++b) mma32(d[b], lo, hi, w[k][b]);
                 }
             }
         }
-    }
-    if (!on) return;
 #pragma unroll
-    for (int g = 0; g < kGroup; ++g) {
-        if (g < n) {
-            const int64_t t = grp.tok[g];
-            const uint16_t y = P.base[t * P.ldbase + o];
-            P.y[t * P.ldy + o] = rank > 0 ? float_to_bf16_bits(bf16_bits_to_float(y) + acc[g]) : y;
+        for (int h = 0; h < 2; ++h) {
+            uint32_t e[4] = {y[h].x, y[h].y, y[h].z, y[h].w};
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                e[b] = pack_bf162(__uint_as_float(e[b] << 16) + d[b][2 * h], __uint_as_float(e[b] & 0xffff0000u) + d[b][2 * h + 1]);
+            y[h] = make_uint4(e[0], e[1], e[2], e[3]);
         }
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (o < P.n_out && g + 8 * h < n)
+            *reinterpret_cast<uint4 *>(P.y + (int64_t)grp.tok[g + 8 * h] * P.ldy + o) = y[h];
 }
 
-// Columns of n_in per shrink CTA, in steps of 256: as many as leave about two
-// CTAs for every SM.
-int small_steps(int tokens, int n_in, int nproj)
-{
-    const int all = (n_in + kStep - 1) / kStep;
-    int steps = kMaxSteps;
-    while (steps > 1 && tokens * nproj * ((all + steps - 1) / steps) < 296) --steps;
-    return steps;
-}
-int small_slices(int tokens, int n_in, int nproj)
-{
-    const int cols = small_steps(tokens, n_in, nproj) * kStep;
-    return (n_in + cols - 1) / cols;
-}
+int small_slices(int n_in) { return (n_in + kSlice - 1) / kSlice; }
 
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
@@ -290,26 +316,33 @@ cudaError_t small_adapters(const AdaptersArgs &a, const DeviceInfo &dev, cudaStr
     p.n_in = a.n_in;
     p.count = a.count;
     p.nproj = a.nproj;
-    p.steps = small_steps(M, a.n_in, a.nproj);
-    p.slices = small_slices(M, a.n_in, a.nproj);
+    p.slices = small_slices(a.n_in);
     p.status = dev.status;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    int rank = 0;
     for (int j = 0; j < a.nproj; ++j) {
         p.proj[j] = a.proj[j];
         p.part[j] = reinterpret_cast<float *>(ws);
         ws += align256(sizeof(float) * (size_t)p.slices * (size_t)M * (size_t)a.proj[j].rank);
-        p.chunk0[j + 1] = p.chunk0[j] + (a.proj[j].n_out + kThreads - 1) / kThreads;
+        p.chunk0[j + 1] = p.chunk0[j] + (a.proj[j].n_out + kOutputs - 1) / kOutputs;
+        p.row0[j + 1] = p.row0[j] + (a.proj[j].rank + kRows - 1) / kRows;
+        rank = std::max(rank, a.proj[j].rank);
     }
-    cudaError_t e = launch_pdl(small_shrink_kernel, dim3((unsigned)p.slices, (unsigned)M, (unsigned)a.nproj), p, stream);
+    // groups: one for each adapter in use and for the tokens without one, and the full ones
+    const unsigned groups = (unsigned)std::min(M, std::min(a.count + 1, M) + M / kGroup);
+    const cudaError_t e = launch_pdl(small_shrink_kernel, dim3((unsigned)p.slices, groups, (unsigned)p.row0[a.nproj]), p, stream);
     if (e != cudaSuccess) return e;
-    return launch_pdl(small_expand_kernel, dim3((unsigned)p.chunk0[a.nproj], (unsigned)M), p, stream);
+    const dim3 grid((unsigned)p.chunk0[a.nproj], groups);
+    return rank <= 32   ? launch_pdl(small_expand_kernel<1>, grid, p, stream)
+           : rank <= 64 ? launch_pdl(small_expand_kernel<2>, grid, p, stream)
+                        : launch_pdl(small_expand_kernel<4>, grid, p, stream);
 }
 
 size_t small_workspace(int M, int n_in, int nproj, const int *ranks)
 {
     size_t b = 0;
     for (int j = 0; j < nproj; ++j)
-        b += align256(sizeof(float) * (size_t)small_slices(M, n_in, nproj) * (size_t)M * (size_t)ranks[j]);
+        b += align256(sizeof(float) * (size_t)small_slices(n_in) * (size_t)M * (size_t)ranks[j]);
     return b;
 }
 
