@@ -21,8 +21,10 @@
 // of rank 32 and 34816 outputs, most of it spent unpacking and on 16-byte pieces
 // of 32 rows at a time.)
 // Tokens that share an adapter read its weights once per kGroup of them, wherever
-// they stand in the batch.  CTA y of either launch finds the y-th group for
-// itself; there are no more of them than adapters and full groups.
+// they stand in the batch.  Each CTA finds the groups for itself, once, and then
+// takes its units one after the other, the next one's weights asked for before
+// the last is written (a CTA a unit: 29 us for that expand, most of it spent
+// finding groups, one wave of CTAs after the other).
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -42,6 +44,9 @@ constexpr int kSlice = kWarps * kWarpCols;
 constexpr int kWarpOuts = 32;          // outputs of an expand warp
 constexpr int kOutputs = kWarps * kWarpOuts;
 static_assert(kAdapterSmallTokens <= kThreads && kAdapterSmallTokens % 4 == 0, "one thread for each token looks for its adapter");
+constexpr int kShrinkCtas = 3;          // CTAs an SM: what their registers leave room for
+constexpr int expand_ctas(int ks) { return ks < 2 ? 3 : 2; }
+static_assert(kAdapterSmallTokens <= 256 && LB_MAX_ADAPTER_RANK < 256, "8 bits hold a token and a rank");
 static_assert(kGroup * kRows == kThreads, "one thread for each partial of a shrink CTA");
 
 struct SmallParams {
@@ -57,64 +62,88 @@ struct SmallParams {
     int *status;
 };
 
-// The tokens of this CTA, group blockIdx.y: the adapters' tokens in order, cut
-// every kGroup; a group stands where its first token does.  Returns their
-// number, 0 where there is no such group; `id` is the adapter, or -1.  One
-// thread per token.
-struct Group {
-    int tok[kGroup];
-    int id, size;
+// The groups of a call: each adapter's tokens in order, cut every kGroup; a group
+// stands where its first token does.  One thread per token.
+struct Groups {
+    int ids[kAdapterSmallTokens];                // of each token, then of each group (-1: no adapter)
+    int at[kAdapterSmallTokens];                 // of a group's first token: the group
+    int size[kAdapterSmallTokens];
+    uint8_t tok[kAdapterSmallTokens][kGroup];
+    uint8_t rank[kMaxSiblings][kAdapterSmallTokens];
+    uint32_t masks[kWarps];
 };
-__device__ __forceinline__ int find_group(const SmallParams &p, Group &g, int *ids, uint32_t *masks, int &id)
+__device__ __forceinline__ int find_groups(const SmallParams &p, Groups &g)
 {
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     int mine = -1;
-    if (t < p.tokens) {
-        mine = __ldg(p.ids + t);
+    if (t < p.tokens || p.tokens == 1) {
+        mine = __ldg(p.ids + (p.tokens == 1 ? 0 : t));
         if (mine >= p.count) {
-            if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) set_status(p.status, LB_ERR_INVALID_ARGUMENT);
+            if (blockIdx.x == 0) set_status(p.status, LB_ERR_INVALID_ARGUMENT);
             mine = -1;
         }
         mine = max(mine, -1);
     }
-    if (p.tokens == 1) {
-        if (t == 0) g.tok[0] = 0, g.id = mine;
+    auto rank_of = [&](const AdapterProj &P, int id) {
+        return (uint8_t)(id < 0 ? 0 : P.ranks == nullptr ? P.rank : max(0, min(P.rank, __ldg(P.ranks + id))));
+    };
+    if (p.tokens == 1) {  // every thread has its id
+        if (t < p.nproj) g.rank[t][0] = rank_of(p.proj[t], mine);
+        if (t == 0) {
+            g.ids[0] = mine;
+            g.size[0] = 1;
+            g.tok[0][0] = 0;
+        }
         __syncthreads();
-        id = g.id;
         return 1;
     }
-    if (t < kAdapterSmallTokens) ids[t] = t < p.tokens ? mine : -2;
-    if (t == 0) g.size = 0;
+    if (t < kAdapterSmallTokens) {
+        g.ids[t] = mine;
+        g.size[t] = 0;
+    }
     __syncthreads();
-    int before = 0;  // earlier tokens of the same adapter
+    int before = 0, first = t;  // earlier tokens of the same adapter; the group's first token
     if (t < p.tokens) {
-        for (int j = 0; j < t; j += 4) {  // ids past the last token are no token's
-            const int4 v = *reinterpret_cast<const int4 *>(ids + j);
-            before += (v.x == mine) + (v.y == mine && j + 1 < t) + (v.z == mine && j + 2 < t) + (v.w == mine && j + 3 < t);
+        for (int j = 0; j < t; j += 4) {
+            const int4 v = *reinterpret_cast<const int4 *>(g.ids + j);
+            const int k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (k[i] == mine && j + i < t) {
+                    if (before % kGroup == 0) first = j + i;
+                    ++before;
+                }
+            }
         }
+        if (before % kGroup == 0) first = t;
     }
-    const bool leads = t < p.tokens && before % kGroup == 0;
+    const bool leads = t < p.tokens && first == t;
     const uint32_t mask = __ballot_sync(0xffffffffu, leads);
-    if (lane == 0) masks[w] = mask;
+    if (lane == 0) g.masks[w] = mask;
     __syncthreads();
-    int at = __popc(mask & ((1u << lane) - 1u));  // groups led before t
-    for (int i = 0; i < w; ++i) at += __popc(masks[i]);
-    if (leads && at == (int)blockIdx.y) {
-        g.id = mine;
-        g.size = 1 + before;  // for now: where the group begins among its adapter's tokens
+    int at = __popc(mask & ((1u << lane) - 1u)), n = 0;  // groups led before t; all groups
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        const int c = __popc(g.masks[i]);
+        at += i < w ? c : 0;
+        n += c;
+    }
+    if (leads) {
+        g.at[t] = at;
+        g.ids[at] = mine;
     }
     __syncthreads();
-    const int from = g.size - 1;
-    if (from < 0) return 0;
-    id = g.id;
-    const bool in = t < p.tokens && mine == id && before >= from && before < from + kGroup;
-    if (in) g.tok[before - from] = t;
-    return __syncthreads_count(in);
-}
-
-__device__ __forceinline__ int rank_of(const AdapterProj &P, int id)
-{
-    return P.ranks == nullptr ? P.rank : max(0, min(P.rank, __ldg(P.ranks + id)));
+    if (t < p.tokens) {
+        at = g.at[first];
+        g.tok[at][before % kGroup] = (uint8_t)t;
+        atomicAdd(&g.size[at], 1);
+    }
+    for (int i = t; i < n * p.nproj; i += kThreads) {
+        const int j = i / n, k = i - j * n;
+        g.rank[j][k] = rank_of(p.proj[j], g.ids[k]);
+    }
+    __syncthreads();
+    return n;
 }
 
 // d += A B of 16 rows (tokens), 8 columns and 16 k.  A lane holds of A the rows
@@ -133,157 +162,204 @@ __device__ __forceinline__ void mma32(float (&d)[4], const uint4 &lo, const uint
     mma(d, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
 }
 
-// grid (slices, groups, rows of every projection's A by kRows)
-__global__ void __launch_bounds__(kThreads) small_shrink_kernel(const __grid_constant__ SmallParams p)
+// Units (group, kRows rows of a projection's A, slice), one after the other
+__global__ void __launch_bounds__(kThreads, kShrinkCtas) small_shrink_kernel(const __grid_constant__ SmallParams p)
 {
-    __shared__ Group grp;
-    __shared__ uint32_t masks[kWarps];
-    __shared__ alignas(16) int ids[kAdapterSmallTokens];
-    __shared__ float red[kWarps][kGroup][kRows + 2];
-    int id = -1;
-    const int n = find_group(p, grp, ids, masks, id);
-    int j = 0;
-    while (j + 1 < p.nproj && (int)blockIdx.z >= p.row0[j + 1]) ++j;
-    const AdapterProj &P = p.proj[j];
-    const int r0 = ((int)blockIdx.z - p.row0[j]) * kRows;
-    const int rank = n > 0 && id >= 0 ? rank_of(P, id) : 0;
-    if (r0 >= rank) {  // uniform over the CTA
-        pdl_wait();
-        return;
-    }
+    __shared__ alignas(16) Groups grp;
+    __shared__ float red[2][kWarps][kGroup][kRows + 2];
+    const int groups = find_groups(p, grp);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int k0 = blockIdx.x * kSlice + warp * kWarpCols + 8 * (lane & 3);
+    const int kw = warp * kWarpCols + 8 * (lane & 3);
+    const int t0 = lane >> 2, t1 = t0 + 8;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     constexpr int kSteps = kWarpCols / 32;
-    uint4 w[kSteps][2], lo[kSteps], hi[kSteps];
-    const int row = r0 + (lane >> 2);  // and the one 8 below
-    const uint16_t *a = P.a + ((int64_t)id * P.rank + row) * p.n_in + k0;
+    const int blocks = p.row0[p.nproj], units = groups * blocks * p.slices;
+    // the next unit from `unit` on that has something to do; its place
+    int g, j, r0, slice, rank;
+    auto find = [&](int unit) {
+        for (; unit < units; unit += gridDim.x) {
+            const int i = unit / p.slices;
+            slice = unit - i * p.slices;
+            g = i / blocks;
+            const int row = i - g * blocks;
+            j = 0;
+            while (j + 1 < p.nproj && row >= p.row0[j + 1]) ++j;
+            r0 = (row - p.row0[j]) * kRows;
+            rank = grp.rank[j][g];
+            if (r0 < rank) break;
+        }
+        return unit;
+    };
+    uint4 w[kSteps][2];
+    auto load = [&]() {
+        const int k0 = slice * kSlice + kw, row = r0 + t0;  // and the one 8 below
+        const uint16_t *a = p.proj[j].a + ((int64_t)grp.ids[g] * p.proj[j].rank + row) * p.n_in + k0;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const bool in = k0 + 32 * s < p.n_in;
-        w[s][0] = in && row < rank ? ldg_early_v4(a + 32 * s) : zero;
-        w[s][1] = in && row + 8 < rank ? ldg_early_v4(a + (int64_t)8 * p.n_in + 32 * s) : zero;
-    }
+        for (int s = 0; s < kSteps; ++s) {
+            const bool in = k0 + 32 * s < p.n_in;
+            w[s][0] = in && row < rank ? ldg_early_v4(a + 32 * s) : zero;
+            w[s][1] = in && row + 8 < rank ? ldg_early_v4(a + (int64_t)8 * p.n_in + 32 * s) : zero;
+        }
+    };
+    int unit = find(blockIdx.x);
+    if (unit < units) load();
     pdl_wait();
     pdl_launch_dependents();
-    const int t0 = lane >> 2, t1 = t0 + 8;
-    const uint16_t *x0 = p.x + (int64_t)grp.tok[t0 < n ? t0 : 0] * p.ldx + k0;
-    const uint16_t *x1 = p.x + (int64_t)grp.tok[t1 < n ? t1 : 0] * p.ldx + k0;
+    for (int turn = 0; unit < units; turn ^= 1) {
+        const int n = grp.size[g], k0 = slice * kSlice + kw;
+        const uint16_t *x0 = p.x + (int64_t)grp.tok[g][t0 < n ? t0 : 0] * p.ldx + k0;
+        const uint16_t *x1 = p.x + (int64_t)grp.tok[g][t1 < n ? t1 : 0] * p.ldx + k0;
+        uint4 lo[kSteps], hi[kSteps];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const bool in = k0 + 32 * s < p.n_in;
-        lo[s] = in && t0 < n ? *reinterpret_cast<const uint4 *>(x0 + 32 * s) : zero;
-        hi[s] = in && t1 < n ? *reinterpret_cast<const uint4 *>(x1 + 32 * s) : zero;
-    }
-    float d[2][4] = {};
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        mma32(d[0], lo[s], hi[s], w[s][0]);
-        mma32(d[1], lo[s], hi[s], w[s][1]);
-    }
-    const int c = 2 * (lane & 3);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        *reinterpret_cast<float2 *>(&red[warp][t0][8 * h + c]) = make_float2(d[h][0], d[h][1]);
-        *reinterpret_cast<float2 *>(&red[warp][t1][8 * h + c]) = make_float2(d[h][2], d[h][3]);
-    }
-    __syncthreads();
-    const int g = threadIdx.x / kRows, r = threadIdx.x % kRows;
-    float v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) v += red[i][g][r];
-    if (g < n && r0 + r < rank)
-        p.part[j][((int64_t)blockIdx.x * p.tokens + grp.tok[g]) * P.rank + r0 + r] = v;
-}
-
-// grid (chunks of kOutputs of every projection, groups); KS: 32 columns of B are
-// a step, and `rank` has at most KS of them.
-template <int KS>
-__global__ void __launch_bounds__(kThreads) small_expand_kernel(const __grid_constant__ SmallParams p)
-{
-    __shared__ Group grp;
-    __shared__ uint32_t masks[kWarps];
-    __shared__ alignas(16) int ids[kAdapterSmallTokens];
-    // s_i v in three bf16 parts, 24 bits: nothing of the fp32 value is lost
-    constexpr int kPitch = 32 * KS + 8;  // 16-byte reads of 8 rows fall into 8 different bank groups
-    __shared__ alignas(16) uint16_t vs[3][kGroup][kPitch];
-    int id = -1;
-    const int n = find_group(p, grp, ids, masks, id);
-    int j = 0;
-    while (j + 1 < p.nproj && (int)blockIdx.x >= p.chunk0[j + 1]) ++j;
-    const AdapterProj &P = p.proj[j];
-    const int rank = n > 0 && id >= 0 ? rank_of(P, id) : 0;
-    if (n == 0 || (rank == 0 && P.base == P.y)) {  // uniform over the CTA
-        pdl_wait();
-        return;
-    }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-    const int out0 = ((int)blockIdx.x - p.chunk0[j]) * kOutputs + warp * kWarpOuts;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    // Column g of product b is output 8 (g / 2) + 2 b + g % 2 of the warp's, so that
-    // a lane's columns of the four products are 8 outputs in a row, from 8 q on.
-    uint4 w[KS][4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const int o = out0 + 8 * (g >> 1) + 2 * b + (g & 1);
-        const uint16_t *B = P.b + ((int64_t)max(id, 0) * P.n_out + o) * P.rank + 8 * q;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) w[k][b] = o < P.n_out && 32 * k + 8 * q < rank ? ldg_early_v4(B + 32 * k) : zero;
-    }
-    const float scale = P.scale != nullptr && rank > 0 ? __ldg(P.scale + id) : 1.0f;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int o = out0 + 8 * q;
-    uint4 y[2] = {zero, zero};
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (o < P.n_out && g + 8 * h < n)
-            y[h] = *reinterpret_cast<const uint4 *>(P.base + (int64_t)grp.tok[g + 8 * h] * P.ldbase + o);
-    if (rank > 0) {
-        const int64_t next = (int64_t)p.tokens * P.rank;
-        for (int i = threadIdx.x; i < n * 32 * KS; i += kThreads) {
-            const int t = i / (32 * KS), r = i % (32 * KS);
-            float v = 0.0f;
-            if (r < rank) {
-                const float *part = p.part[j] + (int64_t)grp.tok[t] * P.rank + r;
-#pragma unroll 4
-                for (int s = 0; s < p.slices; ++s) v += part[s * next];
-            }
-            v *= scale;
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {  // truncated, so that no part can overflow
-                const uint32_t top = __float_as_uint(v) & 0xffff0000u;
-                vs[k][t][r] = (uint16_t)(top >> 16);
-                v = isfinite(v) ? v - __uint_as_float(top) : 0.0f;
-            }
+        for (int s = 0; s < kSteps; ++s) {
+            const bool in = k0 + 32 * s < p.n_in;
+            lo[s] = in && t0 < n ? *reinterpret_cast<const uint4 *>(x0 + 32 * s) : zero;
+            hi[s] = in && t1 < n ? *reinterpret_cast<const uint4 *>(x1 + 32 * s) : zero;
         }
-        __syncthreads();
-        float d[4][4] = {};
+        float d[2][4] = {};
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            if (32 * k < rank) {
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    const uint4 lo = g < n ? *reinterpret_cast<const uint4 *>(&vs[i][g][32 * k + 8 * q]) : zero;
-                    const uint4 hi = g + 8 < n ? *reinterpret_cast<const uint4 *>(&vs[i][g + 8][32 * k + 8 * q]) : zero;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) mma32(d[b], lo, hi, w[k][b]);
-                }
-            }
+        for (int s = 0; s < kSteps; ++s) {
+            mma32(d[0], lo[s], hi[s], w[s][0]);
+            mma32(d[1], lo[s], hi[s], w[s][1]);
         }
+        // where the partial of this thread goes: token threadIdx.x / kRows, row r0 + threadIdx.x % kRows
+        const int t = threadIdx.x / kRows, r = threadIdx.x % kRows;
+        float *to = t < n && r0 + r < rank
+                        ? p.part[j] + ((int64_t)slice * p.tokens + grp.tok[g][t]) * p.proj[j].rank + r0 + r
+                        : nullptr;
+        unit = find(unit + gridDim.x);
+        if (unit < units) load();
+        const int c = 2 * (lane & 3);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t e[4] = {y[h].x, y[h].y, y[h].z, y[h].w};
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                e[b] = pack_bf162(__uint_as_float(e[b] << 16) + d[b][2 * h], __uint_as_float(e[b] & 0xffff0000u) + d[b][2 * h + 1]);
-            y[h] = make_uint4(e[0], e[1], e[2], e[3]);
+            *reinterpret_cast<float2 *>(&red[turn][warp][t0][8 * h + c]) = make_float2(d[h][0], d[h][1]);
+            *reinterpret_cast<float2 *>(&red[turn][warp][t1][8 * h + c]) = make_float2(d[h][2], d[h][3]);
         }
-    }
+        __syncthreads();  // the next unit writes the other half of `red`
+        float v = 0.0f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (o < P.n_out && g + 8 * h < n)
-            *reinterpret_cast<uint4 *>(P.y + (int64_t)grp.tok[g + 8 * h] * P.ldy + o) = y[h];
+        for (int i = 0; i < kWarps; ++i) v += red[turn][i][t][r];
+        if (to != nullptr) *to = v;
+    }
+}
+
+// Units (group, kOutputs outputs of a projection), one after the other.  KS: 32
+// columns of B are a step, and `rank` has at most KS of them.
+template <int KS>
+__global__ void __launch_bounds__(kThreads, expand_ctas(KS)) small_expand_kernel(const __grid_constant__ SmallParams p)
+{
+    __shared__ alignas(16) Groups grp;
+    // s_i v in three bf16 parts, 24 bits: nothing of the fp32 value is lost
+    constexpr int kPitch = 32 * KS + 8;  // 16-byte reads of 8 rows fall into 8 different bank groups
+    __shared__ alignas(16) uint16_t vs[2][3][kGroup][kPitch];
+    const int groups = find_groups(p, grp);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane >> 2, q = lane & 3;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    constexpr int kAtOnce = 8;  // partials a thread asks for at once
+    const int chunks = p.chunk0[p.nproj], units = groups * chunks;
+    int g, j, out0, rank;
+    auto find = [&](int unit) {
+        for (; unit < units; unit += gridDim.x) {
+            g = unit / chunks;
+            const int c = unit - g * chunks;
+            j = 0;
+            while (j + 1 < p.nproj && c >= p.chunk0[j + 1]) ++j;
+            out0 = (c - p.chunk0[j]) * kOutputs + warp * kWarpOuts;
+            rank = grp.rank[j][g];
+            if (rank > 0 || p.proj[j].base != p.proj[j].y) break;
+        }
+        return unit;
+    };
+    // Column `row` of product b is output 8 (row / 2) + 2 b + row % 2 of the warp's,
+    // so that a lane's columns of the four products are 8 outputs in a row, from 8 q on.
+    uint4 w[KS][4];
+    float scale;
+    auto load = [&]() {
+        const AdapterProj &P = p.proj[j];
+        const int id = max(grp.ids[g], 0);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int o = out0 + 8 * (row >> 1) + 2 * b + (row & 1);
+            const uint16_t *B = P.b + ((int64_t)id * P.n_out + o) * P.rank + 8 * q;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) w[k][b] = o < P.n_out && 32 * k + 8 * q < rank ? ldg_early_v4(B + 32 * k) : zero;
+        }
+        scale = P.scale != nullptr ? __ldg(P.scale + id) : 1.0f;
+    };
+    int unit = find(blockIdx.x);
+    if (unit < units) load();
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int turn = 0; unit < units;) {
+        const AdapterProj &P = p.proj[j];
+        const int n = grp.size[g], o = out0 + 8 * q;
+        uint4 y[2] = {zero, zero};
+        uint16_t *to[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            to[h] = nullptr;
+            if (o < P.n_out && row + 8 * h < n) {
+                const int64_t t = grp.tok[g][row + 8 * h];
+                to[h] = P.y + t * P.ldy + o;
+                y[h] = *reinterpret_cast<const uint4 *>(P.base + t * P.ldbase + o);
+            }
+        }
+        if (rank > 0) {
+            const int64_t next = (int64_t)p.tokens * P.rank;
+            for (int i = threadIdx.x; i < n * 16 * KS; i += kThreads) {
+                const int t = i / (16 * KS), r = i % (16 * KS) * 2;  // and r + 1
+                float2 v = make_float2(0.0f, 0.0f);
+                if (r < rank) {
+                    const float *part = p.part[j] + (int64_t)grp.tok[g][t] * P.rank + r;
+                    for (int s0 = 0; s0 < p.slices; s0 += kAtOnce) {
+                        float2 e[kAtOnce];
+#pragma unroll
+                        for (int s = 0; s < kAtOnce; ++s)
+                            e[s] = s0 + s < p.slices ? *reinterpret_cast<const float2 *>(part + (s0 + s) * next) : make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int s = 0; s < kAtOnce; ++s) v.x += e[s].x, v.y += e[s].y;
+                    }
+                }
+                v.x *= scale;
+                v.y = r + 1 < rank ? v.y * scale : 0.0f;  // nothing was written past the rank
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {  // truncated, so that no part can overflow
+                    const uint32_t x = __float_as_uint(v.x) & 0xffff0000u, y = __float_as_uint(v.y) & 0xffff0000u;
+                    *reinterpret_cast<uint32_t *>(&vs[turn][k][t][r]) = x >> 16 | y;
+                    v.x = isfinite(v.x) ? v.x - __uint_as_float(x) : 0.0f;
+                    v.y = isfinite(v.y) ? v.y - __uint_as_float(y) : 0.0f;
+                }
+            }
+            __syncthreads();  // the next unit writes the other half of `vs`
+            float d[4][4] = {};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                if (32 * k < rank) {
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const uint4 lo = row < n ? *reinterpret_cast<const uint4 *>(&vs[turn][i][row][32 * k + 8 * q]) : zero;
+                        const uint4 hi = row + 8 < n ? *reinterpret_cast<const uint4 *>(&vs[turn][i][row + 8][32 * k + 8 * q]) : zero;
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) mma32(d[b], lo, hi, w[k][b]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t e[4] = {y[h].x, y[h].y, y[h].z, y[h].w};
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    e[b] = pack_bf162(__uint_as_float(e[b] << 16) + d[b][2 * h], __uint_as_float(e[b] & 0xffff0000u) + d[b][2 * h + 1]);
+                y[h] = make_uint4(e[0], e[1], e[2], e[3]);
+            }
+            turn ^= 1;  // only where the barrier above was passed
+        }
+        unit = find(unit + gridDim.x);
+        if (unit < units) load();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (to[h] != nullptr) *reinterpret_cast<uint4 *>(to[h]) = y[h];
+    }
 }
 
 int small_slices(int n_in) { return (n_in + kSlice - 1) / kSlice; }
@@ -329,13 +405,15 @@ cudaError_t small_adapters(const AdaptersArgs &a, const DeviceInfo &dev, cudaStr
         rank = std::max(rank, a.proj[j].rank);
     }
     // groups: one for each adapter in use and for the tokens without one, and the full ones
-    const unsigned groups = (unsigned)std::min(M, std::min(a.count + 1, M) + M / kGroup);
-    const cudaError_t e = launch_pdl(small_shrink_kernel, dim3((unsigned)p.slices, groups, (unsigned)p.row0[a.nproj]), p, stream);
+    const int groups = std::min(M, std::min(a.count + 1, M) + M / kGroup);
+    const int sms = dev.sm_count;
+    auto grid = [&](int units, int ctas) { return dim3((unsigned)std::min(units, sms * ctas)); };
+    const cudaError_t e = launch_pdl(small_shrink_kernel, grid(groups * p.row0[a.nproj] * p.slices, kShrinkCtas), p, stream);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)p.chunk0[a.nproj], groups);
-    return rank <= 32   ? launch_pdl(small_expand_kernel<1>, grid, p, stream)
-           : rank <= 64 ? launch_pdl(small_expand_kernel<2>, grid, p, stream)
-                        : launch_pdl(small_expand_kernel<4>, grid, p, stream);
+    const int units = groups * p.chunk0[a.nproj];
+    return rank <= 32   ? launch_pdl(small_expand_kernel<1>, grid(units, expand_ctas(1)), p, stream)
+           : rank <= 64 ? launch_pdl(small_expand_kernel<2>, grid(units, expand_ctas(2)), p, stream)
+                        : launch_pdl(small_expand_kernel<4>, grid(units, expand_ctas(4)), p, stream);
 }
 
 size_t small_workspace(int M, int n_in, int nproj, const int *ranks)
