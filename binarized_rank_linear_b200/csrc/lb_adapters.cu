@@ -16,15 +16,24 @@
 // a product as long as both operands agree, so a lane takes 16 bytes at once - 8
 // columns of one row - and feeds them to two products.  Everything a CTA reads is
 // asked for at once; weights before the launch this one depends on has finished
-// (programmatic dependent launch).  (fp32 FMAs on CUDA cores in place of the
-// products, a thread a row of B: 44 us for the expand of 100 tokens, 16 adapters
-// of rank 32 and 34816 outputs, most of it spent unpacking and on 16-byte pieces
-// of 32 rows at a time.)
-// Tokens that share an adapter read its weights once per kGroup of them, wherever
-// they stand in the batch.  Each CTA finds the groups for itself, once, and then
-// takes its units one after the other, the next one's weights asked for before
-// the last is written (a CTA a unit: 29 us for that expand, most of it spent
-// finding groups, one wave of CTAs after the other).
+// (programmatic dependent launch).  Tokens that share an adapter read its weights
+// once per kGroup of them, wherever they stand in the batch.  Each CTA finds the
+// groups for itself, once, and takes its units one after the other, the next one's
+// weights asked for before the last is written.
+// Measured, both launches, operands not in L2: 1 token and three projections of
+// 4096 x 4096, rank 16, 3.9 us; 100 tokens, 16 adapters of rank 32, 5120 to 2 x
+// 17408 columns, 20 us, 3.0 TB/s (60 us with fp32 FMAs, a thread a row of B: most
+// of it spent unpacking and on 16-byte pieces of 32 rows at a time; 36 us with the
+// products but a CTA a unit: most of it spent finding groups, one wave of CTAs
+// after the other); 128 tokens, 32 adapters of rank 128, 4096 x 4096, 19 us, 3.6
+// TB/s.  What is left is the chain of each unit: partials, split, product, store.
+//
+// Up to kAdapterSmallTokens (256) tokens; beyond, and for the backward pass, the
+// tcgen05 kernels of lb_adapters_mma.cu, whose tiles hold 128 tokens of one
+// adapter.  At 256 tokens, here and there: 8 adapters of rank 16, 4096 x 4096, 6.5
+// and 18.5 us; 64 of rank 16, 5120 to 7168, 21 and 86 us; 16 of rank 32, 5120 to
+// 34816, 30 and 63 us; 2 of rank 128, 4096 x 4096, 13 and 25 us; only all tokens
+// on one adapter of rank 64 with 28672 outputs, 29 and 22 us.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -62,16 +71,20 @@ struct SmallParams {
     int *status;
 };
 
-// The groups of a call: each adapter's tokens in order, cut every kGroup; a group
-// stands where its first token does.  One thread per token.
+// The groups of a call: each adapter's tokens in order, cut every kGroup; an
+// adapter's groups stand where its first token does.  One thread per token: those
+// of a warp with the same adapter find each other (match), and a table by adapter
+// holds their number in each warp.
 struct Groups {
-    int ids[kAdapterSmallTokens];                // of each token, then of each group (-1: no adapter)
-    int at[kAdapterSmallTokens];                 // of a group's first token: the group
+    int ids[kAdapterSmallTokens];                // of each group (-1: no adapter)
     int size[kAdapterSmallTokens];
     uint8_t tok[kAdapterSmallTokens][kGroup];
     uint8_t rank[kMaxSiblings][kAdapterSmallTokens];
-    uint32_t masks[kWarps];
+    int warp[kWarps];                            // groups that begin in each warp
+    uint64_t in_warp[LB_MAX_ADAPTERS + 1];       // by id + 1: tokens in each warp, a byte each
+    uint16_t first[LB_MAX_ADAPTERS + 1];         // by id + 1: its first group
 };
+static_assert(kWarps == 8, "a byte for each warp");
 __device__ __forceinline__ int find_groups(const SmallParams &p, Groups &g)
 {
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
@@ -97,47 +110,49 @@ __device__ __forceinline__ int find_groups(const SmallParams &p, Groups &g)
         __syncthreads();
         return 1;
     }
-    if (t < kAdapterSmallTokens) {
-        g.ids[t] = mine;
-        g.size[t] = 0;
-    }
+    const bool on = t < p.tokens;
+    const uint32_t peers = __match_any_sync(0xffffffffu, on ? mine : -2), earlier = peers & ((1u << lane) - 1u);
+    if (on) g.in_warp[mine + 1] = 0;
     __syncthreads();
-    int before = 0, first = t;  // earlier tokens of the same adapter; the group's first token
-    if (t < p.tokens) {
-        for (int j = 0; j < t; j += 4) {
-            const int4 v = *reinterpret_cast<const int4 *>(g.ids + j);
-            const int k[4] = {v.x, v.y, v.z, v.w};
+    if (on && earlier == 0) reinterpret_cast<uint8_t *>(&g.in_warp[mine + 1])[w] = (uint8_t)__popc(peers);
+    __syncthreads();
+    int before = __popc(earlier), all = 0;  // tokens of the same adapter: earlier ones; all
+    if (on) {
+        const uint64_t c = g.in_warp[mine + 1];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (k[i] == mine && j + i < t) {
-                    if (before % kGroup == 0) first = j + i;
-                    ++before;
-                }
-            }
+        for (int i = 0; i < kWarps; ++i) {
+            const int k = (int)(c >> (8 * i)) & 0xff;
+            before += i < w ? k : 0;
+            all += k;
         }
-        if (before % kGroup == 0) first = t;
     }
-    const bool leads = t < p.tokens && first == t;
-    const uint32_t mask = __ballot_sync(0xffffffffu, leads);
-    if (lane == 0) g.masks[w] = mask;
+    const int mygroups = on && before == 0 ? (all + kGroup - 1) / kGroup : 0;
+    int at = mygroups;  // inclusive over the warp, then exclusive over the call
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int k = __shfl_up_sync(0xffffffffu, at, o);
+        at += lane >= o ? k : 0;
+    }
+    if (lane == 31) g.warp[w] = at;
     __syncthreads();
-    int at = __popc(mask & ((1u << lane) - 1u)), n = 0;  // groups led before t; all groups
+    at -= mygroups;
+    int n = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-        const int c = __popc(g.masks[i]);
-        at += i < w ? c : 0;
-        n += c;
+        at += i < w ? g.warp[i] : 0;
+        n += g.warp[i];
     }
-    if (leads) {
-        g.at[t] = at;
-        g.ids[at] = mine;
+    if (mygroups > 0) g.first[mine + 1] = (uint16_t)at;
+    __syncthreads();
+    if (on) {
+        const int k = g.first[mine + 1] + before / kGroup;
+        g.tok[k][before % kGroup] = (uint8_t)t;
+        if (before % kGroup == 0) {
+            g.ids[k] = mine;
+            g.size[k] = min(kGroup, all - before);
+        }
     }
     __syncthreads();
-    if (t < p.tokens) {
-        at = g.at[first];
-        g.tok[at][before % kGroup] = (uint8_t)t;
-        atomicAdd(&g.size[at], 1);
-    }
     for (int i = t; i < n * p.nproj; i += kThreads) {
         const int j = i / n, k = i - j * n;
         g.rank[j][k] = rank_of(p.proj[j], g.ids[k]);

@@ -388,7 +388,7 @@ LB_API lb_status lb_linear_backward(const uint16_t *x, const uint16_t *dy, int64
  * Errors as lb_linear_forward. */
 #define LB_MAX_ADAPTERS 1024
 #define LB_MAX_ADAPTER_RANK 128
-#define LB_ADAPTERS_SMALL_TOKENS 128
+#define LB_ADAPTERS_SMALL_TOKENS 256
 typedef struct {
     const uint16_t *a;
     const uint16_t *b;
