@@ -376,14 +376,18 @@ __device__ __forceinline__ int used_rank(const int32_t *ranks, int rank, int ada
     return ranks == nullptr ? rank : max(0, min(rank, __ldg(ranks + adapter)));
 }
 
-// `work` K-blocks in equal runs over up to `most` CTAs, at least kLeastBlocks to
+// `work` K-blocks in equal runs over up to `most` CTAs, at least `least` to
 // each: CTA c has start(c) .. start(c + 1) - 1.
+// Shrink takes 4 or more: sums that a CTA shares cost a read and a write of them.
+// A weight gradient has few K-blocks where there are few tokens, and one each
+// spreads its products: 30 tokens, 2 adapters, 34 us at 4 and 26 us at 1; 148
+// tokens, 4 adapters of rank 64, 43 and 33 us.
 constexpr int kLeastBlocks = 4;
 struct Shares {
     int ctas, base, rem;
-    __device__ __forceinline__ Shares(int work, int most)
+    __device__ __forceinline__ Shares(int work, int most, int least)
     {
-        ctas = max(1, min(most, work / kLeastBlocks));
+        ctas = max(1, min(most, work / least));
         base = work / ctas;
         rem = work - base * ctas;
     }
@@ -424,7 +428,10 @@ struct ShrinkParams {
 
 constexpr int kShrinkThreads = 32 * (2 + 4 + kLoaders - 1);
 constexpr uint32_t kXBytes = TM * 128;  // a K-block of a tile's rows: 64 columns
-constexpr int kMaxRank = LB_MAX_ADAPTER_RANK;
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
 template <int NK>
 struct Shrink {
     static constexpr uint32_t kStage = kXBytes + NK * kBox;
@@ -484,6 +491,11 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
         __syncwarp();
         tmem_alloc(smem_u32(tmem_slot), 256);
         tc_fence_before();
+    } else if (warp == 0 && elect_one()) {
+        for (int j = 0; j < p.njobs; ++j) {
+            prefetch_map(&p.job[j].x.box);
+            prefetch_map(&p.job[j].w);
+        }
     }
     __syncthreads();
     tc_fence_after();
@@ -492,7 +504,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
     pdl_launch_dependents();
 
     const int live = p.plan.counts[1], cta = blockIdx.x;
-    const Shares shares(live * p.per_tile, p.ctas);
+    const Shares shares(live * p.per_tile, p.ctas, kLeastBlocks);
     const int w0 = cta < shares.ctas ? shares.start(cta) : 0, w1 = cta < shares.ctas ? shares.start(cta + 1) : 0;
     // the part of one product that begins at K-block w of this CTA's share
     struct Piece {
@@ -698,7 +710,7 @@ __global__ void __launch_bounds__(kFinishThreads) shrink_finish_kernel(const __g
     const int live = p.plan.counts[1], units = live * p.njobs * (TM / kFinishRows);
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         if (threadIdx.x == 0) {
-            const Shares shares(live * p.per_tile, p.ctas);
+            const Shares shares(live * p.per_tile, p.ctas, kLeastBlocks);
             const int product = u / (TM / kFinishRows), tile = product % live, job = product / live;
             const ShrinkJob &J = p.job[job];
             int begin = tile * J.nkb;
@@ -807,6 +819,15 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
         __syncwarp();
         tmem_alloc(smem_u32(tmem_slot), 256);
         tc_fence_before();
+    } else if (warp == 0 && elect_one()) {
+        for (int j = 0; j < p.njobs; ++j) {
+            const ExpandJob &J = p.job[j];
+            prefetch_map(&J.base.box);
+            prefetch_map(&J.w);
+            prefetch_map(&J.hi);
+            prefetch_map(&J.lo);
+            prefetch_map(&J.y);
+        }
     }
     __syncthreads();
     tc_fence_after();
@@ -1126,6 +1147,7 @@ struct WgradJob {
 struct AdapterWgradParams {
     WgradJob job[2];
     int rank, count, ctas;
+    int behind_expand;  // the launch before this one
     const int32_t *ranks;
     Plan plan;
     float *part;  // [slot][kCols * rank], the gradient's order
@@ -1232,15 +1254,23 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
         __syncwarp();
         tmem_alloc(smem_u32(tmem_slot), 512);
         tc_fence_before();
+    } else if (warp == 0 && elect_one()) {
+        for (int j = 0; j < 2; ++j) {
+            prefetch_map(&p.job[j].x.box);
+            for (int i = 0; i < kParts; ++i) prefetch_map(p.job[j].v + i);
+        }
     }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();
+    // Behind expand, what this kernel reads was complete before any of expand's
+    // CTAs let it start (each has waited for the launches before its own): it
+    // begins on the SMs that expand leaves, and only ends after it.
+    if (!p.behind_expand) pdl_wait();
     pdl_launch_dependents();
 
     const int cta = blockIdx.x;
-    const Shares shares(p.plan.counts[2] * (p.job[0].products + p.job[1].products), p.ctas);
+    const Shares shares(p.plan.counts[2] * (p.job[0].products + p.job[1].products), p.ctas, 1);
     const int w0 = cta < shares.ctas ? shares.start(cta) : 0, w1 = cta < shares.ctas ? shares.start(cta + 1) : 0;
 
     const int loader = warp == 0 ? 0 : warp - 1 - kWgradWarps;
@@ -1416,6 +1446,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
             if (w < w1) q.advance();
         }
     }
+    if (p.behind_expand) pdl_wait();
     tc_fence_before();
     __syncthreads();
     if (abort_flag && threadIdx.x == 0) set_status(p.status, LB_ERR_DEVICE_TIMEOUT);
@@ -1448,7 +1479,7 @@ __global__ void __launch_bounds__(kFinishThreads) wgrad_finish_kernel(const __gr
             const int b0 = p.plan.block0[adapter], nkb = p.plan.block0[adapter + 1] - b0;
             found.sums = 0;
             if (nkb > 0) {
-                const Shares shares(p.plan.counts[2] * per, p.ctas);
+                const Shares shares(p.plan.counts[2] * per, p.ctas, 1);
                 const int begin = b0 * per + m * nkb;
                 const int first = shares.owner(begin), last = shares.owner(begin + nkb - 1);
                 found.sums = last > first ? last - first + 1 : -1;
@@ -1765,6 +1796,7 @@ cudaError_t adapters_mma_backward(const AdaptersBwdArgs &b, const DeviceInfo &de
     AdapterWgradParams wp{};
     wp.rank = b.rank;
     wp.count = b.count;
+    wp.behind_expand = b.dx != nullptr;
     wp.ranks = b.ranks;
     wp.plan = plan;
     wp.part = reinterpret_cast<float *>(ws + L.grads);
