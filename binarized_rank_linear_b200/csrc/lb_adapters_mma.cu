@@ -705,11 +705,10 @@ __global__ void __launch_bounds__(kFinishThreads) shrink_finish_kernel(const __g
         const float *first, *rest;
     };
     __shared__ Found found;
-    pdl_wait();
-    pdl_launch_dependents();
+    // the plan was complete before shrink let this launch start
     const int live = p.plan.counts[1], units = live * p.njobs * (TM / kFinishRows);
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        if (threadIdx.x == 0) {
+    auto find = [&](int u) {
+        if (threadIdx.x == 0 && u < units) {
             const Shares shares(live * p.per_tile, p.ctas, kLeastBlocks);
             const int product = u / (TM / kFinishRows), tile = product % live, job = product / live;
             const ShrinkJob &J = p.job[job];
@@ -729,9 +728,15 @@ __global__ void __launch_bounds__(kFinishThreads) shrink_finish_kernel(const __g
                 found.rest = p.part + (int64_t)2 * (first + 1) * TM * p.part_rank;
             }
         }
+    };
+    find(blockIdx.x);
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
         __syncthreads();
         const Found f = found;
         __syncthreads();
+        find(u + gridDim.x);
         if (f.more == 0) continue;
         const ShrinkJob &J = p.job[f.job];
         const int cols = J.rank / 4, stride = 2 * TM * p.part_rank;
@@ -832,8 +837,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();
-    pdl_launch_dependents();
+    // Only v comes from the launch before; the plan was complete before that one
+    // let this one start, and base and W are older still.  So the copies begin at
+    // once, and loader 1, which fetches v, waits.
 
     const int ntiles = p.plan.counts[0];
     const int units = ntiles * p.per_tile;
@@ -903,22 +909,6 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
                     mine.rows(p.plan.perm + q.tile * TM, q.t.rows, 32 * loader + lane);
                     loaders_meet();  // the first is here, so nobody is ahead of the ring
                 }
-                if (q.kind == 2 && loader == 0) {
-                    const int b = nv % S::kVBufs;
-                    const bool ok = !abort_flag && mbar_wait(vempty0 + 8 * b, ((uint32_t)(nv / S::kVBufs) & 1u) ^ 1u);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        abort_flag = 1;
-                    } else if (elect_one()) {
-                        const uint32_t bar = vfull0 + 8 * b, dst = sV + b * S::kV;
-                        mbar_arrive_expect_tx(bar, S::kV);
-                        for (int k = 0; k < NK; ++k) {
-                            tma_load_2d(dst + (2 * k) * kVBytes, &J.hi, 64 * k, q.tile * TM, bar);
-                            tma_load_2d(dst + (2 * k + 1) * kVBytes, &J.lo, 64 * k, q.tile * TM, bar);
-                        }
-                    }
-                    __syncwarp();
-                    ++nv;
-                }
             }
             if (q.kind != 0) {
                 const uint32_t dst = sS + s * S::kStage, bar = full0 + 8 * s;
@@ -957,7 +947,34 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
                 }
                 if (++s == S::kStages) s = 0, ph ^= 1;
             }
+            if (loader == 1) {
+                if (u == u0) {
+                    pdl_wait();
+                    pdl_launch_dependents();
+                }
+                if (q.fresh && q.kind == 2) {
+                    const ExpandJob &J = p.job[q.job];
+                    const int b = nv % S::kVBufs;
+                    const bool ok = !abort_flag && mbar_wait(vempty0 + 8 * b, ((uint32_t)(nv / S::kVBufs) & 1u) ^ 1u);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        abort_flag = 1;
+                    } else if (elect_one()) {
+                        const uint32_t bar = vfull0 + 8 * b, dst = sV + b * S::kV;
+                        mbar_arrive_expect_tx(bar, S::kV);
+                        for (int k = 0; k < NK; ++k) {
+                            tma_load_2d(dst + (2 * k) * kVBytes, &J.hi, 64 * k, q.tile * TM, bar);
+                            tma_load_2d(dst + (2 * k + 1) * kVBytes, &J.lo, 64 * k, q.tile * TM, bar);
+                        }
+                    }
+                    __syncwarp();
+                    ++nv;
+                }
+            }
             if (u + 1 < u1) advance(q);
+        }
+        if (loader == 1 && u0 == u1) {
+            pdl_wait();
+            pdl_launch_dependents();
         }
         if (abort_flag) drain_copies();
     } else if (warp == 1) {
@@ -1469,12 +1486,10 @@ __global__ void __launch_bounds__(kFinishThreads) wgrad_finish_kernel(const __gr
         const float *first, *rest;
     };
     __shared__ Found found;
-    pdl_wait();
-    pdl_launch_dependents();
     const int per = p.job[0].products + p.job[1].products;
     const int quads = kCols * p.rank / 4, each = (quads + kQuads - 1) / kQuads, units = p.count * per * each;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        if (threadIdx.x == 0) {
+    auto find = [&](int u) {  // by the plan, as in shrink's finish
+        if (threadIdx.x == 0 && u < units) {
             const int product = u / each, adapter = product / per, m = product - adapter * per;
             const int b0 = p.plan.block0[adapter], nkb = p.plan.block0[adapter + 1] - b0;
             found.sums = 0;
@@ -1492,9 +1507,15 @@ __global__ void __launch_bounds__(kFinishThreads) wgrad_finish_kernel(const __gr
             found.i0 = (u - product * each) * kQuads;
             found.used = used_rank(p.ranks, p.rank, adapter);
         }
+    };
+    find(blockIdx.x);
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
         __syncthreads();
         const Found f = found;
         __syncthreads();
+        find(u + gridDim.x);
         if (f.sums < 0) continue;
         const WgradJob &J = p.job[f.job];
         const int N = J.n, used = f.used, cols = p.rank / 4, transposed = J.transposed;
@@ -1509,6 +1530,7 @@ __global__ void __launch_bounds__(kFinishThreads) wgrad_finish_kernel(const __gr
             float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (f.sums > 0) {
                 s = __ldcg(reinterpret_cast<const float4 *>(f.first) + i);
+#pragma unroll 4
                 for (int k = 0; k < f.sums - 1; ++k) {
                     const float4 v = __ldcg(reinterpret_cast<const float4 *>(f.rest) + (int64_t)k * 2 * quads + i);
                     s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
