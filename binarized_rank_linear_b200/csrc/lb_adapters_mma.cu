@@ -772,6 +772,7 @@ struct ExpandParams {
     ExpandJob job[kMaxSiblings];
     int njobs, per_tile;  // chunks of a tile in all jobs
     int tokens;
+    int behind_wgrad;  // wgrad is the launch before this one, and v older
     Plan plan;
     int *status;
 };
@@ -839,8 +840,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
     const uint32_t tmem = *tmem_slot;
     // Only v comes from the launch before; the plan was complete before that one
     // let this one start, and base and W are older still.  So the copies begin at
-    // once, and loader 1, which fetches v, waits.
-
+    // once, and loader 1, which fetches v, waits.  Behind wgrad v is older too:
+    // this launch begins on the SMs that wgrad leaves, and only ends after it.
     const int ntiles = p.plan.counts[0];
     const int units = ntiles * p.per_tile;
     const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
@@ -949,7 +950,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
             }
             if (loader == 1) {
                 if (u == u0) {
-                    pdl_wait();
+                    if (!p.behind_wgrad) pdl_wait();
                     pdl_launch_dependents();
                 }
                 if (q.fresh && q.kind == 2) {
@@ -972,7 +973,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
             }
             if (u + 1 < u1) advance(q);
         }
-        if (loader == 1 && u0 == u1) {
+        if (loader == 1 && (u0 == u1 || p.behind_wgrad)) {
             pdl_wait();
             pdl_launch_dependents();
         }
@@ -1164,7 +1165,6 @@ struct WgradJob {
 struct AdapterWgradParams {
     WgradJob job[2];
     int rank, count, ctas;
-    int behind_expand;  // the launch before this one
     const int32_t *ranks;
     Plan plan;
     float *part;  // [slot][kCols * rank], the gradient's order
@@ -1280,11 +1280,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // Behind expand, what this kernel reads was complete before any of expand's
-    // CTAs let it start (each has waited for the launches before its own): it
-    // begins on the SMs that expand leaves, and only ends after it.
-    if (!p.behind_expand) pdl_wait();
-    pdl_launch_dependents();
+    // Only v comes from the launch before: as in expand, the other copies begin
+    // at once, and loader 1, which fetches v, waits.
 
     const int cta = blockIdx.x;
     const Shares shares(p.plan.counts[2] * (p.job[0].products + p.job[1].products), p.ctas, 1);
@@ -1295,6 +1292,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
         int s = 0;
         uint32_t ph = 1;
         Product<NK> q(p, w0, w0 < w1);
+        bool waited = false;
         for (int w = w0; w < w1;) {  // to the end in every loader, whatever happens: they meet
             const int n = min(q.nkb - q.kb, w1 - w);
             const WgradJob &J = p.job[q.job];
@@ -1316,7 +1314,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
                 const bool run = T.run() && T.rows >= 64 * half + 64;
                 if (!run) loaders_meet();  // the first is here, so nobody is ahead of the ring
                 bool ok = true;
-                if (loader == 0 || !run) {
+                if (loader <= 1 || !run) {
                     ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) abort_flag = 1;
@@ -1329,11 +1327,6 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
                         for (int c = 0; c < 2 * S::kTiles; ++c)
                             tma_load_2d(dst + c * kBox, mx, q.n0 + 64 * c, T.first + 64 * half, bar);
                     }
-#pragma unroll
-                    for (int i = 0; i < kParts; ++i)
-#pragma unroll
-                        for (int k = 0; k < NK; ++k)
-                            tma_load_2d(dst + S::kX + (i * NK + k) * kBox, mv + i, 64 * k, slot, bar);
                 }
                 __syncwarp();
                 if (ok && !run) {  // zeros past the adapter's tokens: the slots are what is summed over
@@ -1346,10 +1339,29 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
                     for (int c = 0; c < 2 * S::kTiles; ++c) mine.copy(dst + c * kBox, x, ld, J.x.cols, q.n0 + 64 * c, true);
                     mbar_arrive_after_copies(bar);
                 }
+                if (loader == 1) {
+                    if (!waited) {
+                        waited = true;
+                        pdl_wait();
+                        pdl_launch_dependents();
+                    }
+                    if (ok && elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                            for (int k = 0; k < NK; ++k)
+                                tma_load_2d(dst + S::kX + (i * NK + k) * kBox, mv + i, 64 * k, slot, bar);
+                    }
+                    __syncwarp();
+                }
                 if (++s == S::kStages) s = 0, ph ^= 1;
             }
             w += n;
             if (w < w1) q.advance();
+        }
+        if (loader == 1 && !waited) {
+            pdl_wait();
+            pdl_launch_dependents();
         }
         if (abort_flag) drain_copies();
     } else if (warp == 1) {
@@ -1463,7 +1475,6 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
             if (w < w1) q.advance();
         }
     }
-    if (p.behind_expand) pdl_wait();
     tc_fence_before();
     __syncthreads();
     if (abort_flag && threadIdx.x == 0) set_status(p.status, LB_ERR_DEVICE_TIMEOUT);
@@ -1653,8 +1664,7 @@ cudaError_t launch_wgrad(AdapterWgradParams &p, const DeviceInfo &dev, cudaStrea
 {
     for (WgradJob &J : p.job) J.products = (J.n + Wgrad<NK>::kCols - 1) / Wgrad<NK>::kCols;
     p.ctas = std::min(dev.sm_count, kMostCtas);
-    const cudaError_t e = launch(adapter_wgrad_kernel<NK>, p.ctas, kWgradThreads, Wgrad<NK>::kSmem, p, stream);
-    return e != cudaSuccess ? e : launch(wgrad_finish_kernel<NK>, 8 * dev.sm_count, kFinishThreads, 0, p, stream);
+    return launch(adapter_wgrad_kernel<NK>, p.ctas, kWgradThreads, Wgrad<NK>::kSmem, p, stream);
 }
 size_t wgrad_shared_floats(int rank)
 {
@@ -1792,9 +1802,29 @@ cudaError_t adapters_mma_backward(const AdaptersBwdArgs &b, const DeviceInfo &de
     sp.part_rank = b.rank;
     if (e == cudaSuccess) e = launch_plan(b.ids, b.tokens, b.count, plan, dev, stream);
     if (e == cudaSuccess) e = launch_shrink(sp, tiles, dev, stream);
+    AdapterWgradParams wp{};
+    wp.rank = b.rank;
+    wp.count = b.count;
+    wp.ranks = b.ranks;
+    wp.plan = plan;
+    wp.part = reinterpret_cast<float *>(ws + L.grads);
+    wp.status = dev.status;
+    for (int q = 0; q < 2; ++q) {  // dA from x and u, dB from dy and v
+        WgradJob &w = wp.job[q];
+        w.x = q ? mdy : mx;
+        if (e == cudaSuccess)
+            e = encode_2d(&w.x.box, q ? b.dy : b.x, b.tokens, q ? b.n_out : b.n_in, q ? b.lddy : b.ldx, true, 64);
+        for (int i = 0; i < kParts && e == cudaSuccess; ++i)
+            e = encode_2d(&w.v[i], v[1 - q][i], tiles * TM, b.rank, b.rank, true, 64);
+        w.n = q ? b.n_out : b.n_in;
+        w.transposed = !q;
+        w.out = q ? b.db : b.da;
+    }
+    if (e == cudaSuccess) e = b.rank <= 64 ? launch_wgrad<1>(wp, dev, stream) : launch_wgrad<2>(wp, dev, stream);
     if (b.dx != nullptr && e == cudaSuccess) {
         ExpandParams ep{};
         ep.plan = plan;
+        ep.behind_wgrad = 1;
         ep.status = dev.status;
         ep.njobs = 1;
         ep.tokens = b.tokens;
@@ -1815,27 +1845,8 @@ cudaError_t adapters_mma_backward(const AdaptersBwdArgs &b, const DeviceInfo &de
         if (e == cudaSuccess) e = launch_expand(ep, b.rank, dev, stream);
     }
     if (e != cudaSuccess) return e;
-    AdapterWgradParams wp{};
-    wp.rank = b.rank;
-    wp.count = b.count;
-    wp.behind_expand = b.dx != nullptr;
-    wp.ranks = b.ranks;
-    wp.plan = plan;
-    wp.part = reinterpret_cast<float *>(ws + L.grads);
-    wp.status = dev.status;
-    for (int q = 0; q < 2; ++q) {  // dA from x and u, dB from dy and v
-        WgradJob &w = wp.job[q];
-        w.x = q ? mdy : mx;
-        if (e == cudaSuccess)
-            e = encode_2d(&w.x.box, q ? b.dy : b.x, b.tokens, q ? b.n_out : b.n_in, q ? b.lddy : b.ldx, true, 64);
-        for (int i = 0; i < kParts && e == cudaSuccess; ++i)
-            e = encode_2d(&w.v[i], v[1 - q][i], tiles * TM, b.rank, b.rank, true, 64);
-        w.n = q ? b.n_out : b.n_in;
-        w.transposed = !q;
-        w.out = q ? b.db : b.da;
-    }
-    if (e != cudaSuccess) return e;
-    return b.rank <= 64 ? launch_wgrad<1>(wp, dev, stream) : launch_wgrad<2>(wp, dev, stream);
+    return b.rank <= 64 ? launch(wgrad_finish_kernel<1>, 8 * dev.sm_count, kFinishThreads, 0, wp, stream)
+                        : launch(wgrad_finish_kernel<2>, 8 * dev.sm_count, kFinishThreads, 0, wp, stream);
 }
 
 }  // namespace lb
