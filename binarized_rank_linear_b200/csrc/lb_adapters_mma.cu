@@ -695,6 +695,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
 
 // The products of shrink that several CTAs share, kFinishRows rows a unit.
 constexpr int kFinishThreads = 256, kFinishRows = 16;
+// Sums a thread asks for at once: a long row in a small batch is shared by many
+// CTAs (40 tokens, 16160 columns: 60 of them, 10 us in fours).
+constexpr int kAtOnce = 16;
 __global__ void __launch_bounds__(kFinishThreads) shrink_finish_kernel(const __grid_constant__ ShrinkParams p)
 {
     // one thread finds what a unit adds: the index arithmetic of all threads
@@ -745,10 +748,21 @@ __global__ void __launch_bounds__(kFinishThreads) shrink_finish_kernel(const __g
             const int at = row * p.part_rank + c;
             float4 s = __ldcg(reinterpret_cast<const float4 *>(f.first + at));
             const float *q = f.rest + at;
-#pragma unroll 4
-            for (int k = 0; k < f.more; ++k) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(q + (int64_t)k * stride));
-                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            int k0 = 0;
+            if (f.more <= kAtOnce / 4) {
+                for (; k0 < f.more; ++k0) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(q + (int64_t)k0 * stride));
+                    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+                }
+            }
+            for (; k0 < f.more; k0 += kAtOnce) {
+                float4 v[kAtOnce];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+                    v[k] = k0 + k < f.more ? __ldcg(reinterpret_cast<const float4 *>(q + (int64_t)(k0 + k) * stride))
+                                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
             }
             store_v(J, ((int64_t)f.tile * TM + row) * J.rank + c, c, row < f.rows ? f.used : 0, f.scale, s);
         }
