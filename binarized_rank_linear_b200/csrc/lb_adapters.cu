@@ -21,19 +21,22 @@
 // groups for itself, once, and takes its units one after the other, the next one's
 // weights asked for before the last is written.
 // Measured, both launches, operands not in L2: 1 token and three projections of
-// 4096 x 4096, rank 16, 3.9 us; 100 tokens, 16 adapters of rank 32, 5120 to 2 x
-// 17408 columns, 20 us, 3.0 TB/s (60 us with fp32 FMAs, a thread a row of B: most
+// 4096 x 4096, rank 16, 3.7 us; 100 tokens, 16 adapters of rank 32, 5120 to 2 x
+// 17408 columns, 20.6 us, 3.0 TB/s (60 us with fp32 FMAs, a thread a row of B: most
 // of it spent unpacking and on 16-byte pieces of 32 rows at a time; 36 us with the
 // products but a CTA a unit: most of it spent finding groups, one wave of CTAs
 // after the other); 128 tokens, 32 adapters of rank 128, 4096 x 4096, 19 us, 3.6
 // TB/s.  What is left is the chain of each unit: partials, split, product, store.
 //
-// Up to kAdapterSmallTokens (256) tokens; beyond, and for the backward pass, the
-// tcgen05 kernels of lb_adapters_mma.cu, whose tiles hold 128 tokens of one
-// adapter.  At 256 tokens, here and there: 8 adapters of rank 16, 4096 x 4096, 6.5
-// and 18.5 us; 64 of rank 16, 5120 to 7168, 21 and 86 us; 16 of rank 32, 5120 to
-// 34816, 30 and 63 us; 2 of rank 128, 4096 x 4096, 13 and 25 us; only all tokens
-// on one adapter of rank 64 with 28672 outputs, 29 and 22 us.
+// For up to 128 + 48 x adapters of the pool tokens, at most kAdapterSmallTokens
+// (512); beyond, and for the backward pass, the tcgen05 kernels of
+// lb_adapters_mma.cu, whose tiles hold 128 tokens of one adapter: they pay where
+// an adapter has many tokens, and how many it has is bounded by the pool.  Here
+// and there: 8 adapters of rank 16, 4096 x 4096, 256 tokens 7.6 and 17.0 us, 512
+// tokens 10.5 and 17.3; 64 of rank 16, 5120 to 7168 columns, 512 tokens 28 and 90;
+// 16 of rank 32, 5120 to 34816, 512 tokens 51 and 66; 4 of rank 64, 4096 to 11008,
+// 320 tokens 17.8 and 19.8, 512 tokens 26 and 23; 1 of rank 64, 4096 to 28672, 128
+// tokens 16.1 and 15.6, 192 tokens 23 and 19.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -52,10 +55,12 @@ constexpr int kWarpCols = 128;         // columns of A of a shrink warp
 constexpr int kSlice = kWarps * kWarpCols;
 constexpr int kWarpOuts = 32;          // outputs of an expand warp
 constexpr int kOutputs = kWarps * kWarpOuts;
-static_assert(kAdapterSmallTokens <= kThreads && kAdapterSmallTokens % 4 == 0, "one thread for each token looks for its adapter");
 constexpr int kShrinkCtas = 3;          // CTAs an SM: what their registers leave room for
 constexpr int expand_ctas(int ks) { return ks < 2 ? 3 : 2; }
-static_assert(kAdapterSmallTokens <= 256 && LB_MAX_ADAPTER_RANK < 256, "8 bits hold a token and a rank");
+constexpr int kRounds = kAdapterSmallTokens / kThreads;  // tokens of a thread that looks for their groups
+constexpr int kRuns = kRounds * kWarps;                  // of 32 tokens
+static_assert(kAdapterSmallTokens % kThreads == 0 && kRuns == 16 && LB_MAX_ADAPTER_RANK < 256 && LB_MAX_ADAPTERS < 32768,
+              "two words of bytes hold an adapter's tokens in each run, a byte a rank, 16 bits an adapter");
 static_assert(kGroup * kRows == kThreads, "one thread for each partial of a shrink CTA");
 
 struct SmallParams {
@@ -72,88 +77,113 @@ struct SmallParams {
 };
 
 // The groups of a call: each adapter's tokens in order, cut every kGroup; an
-// adapter's groups stand where its first token does.  One thread per token: those
-// of a warp with the same adapter find each other (match), and a table by adapter
-// holds their number in each warp.
+// adapter's groups stand where its first token does.  A thread takes a token, or
+// two: those of a run of 32 with the same adapter find each other (match), and a
+// table by adapter holds their number in each run.
 struct Groups {
-    int ids[kAdapterSmallTokens];                // of each group (-1: no adapter)
-    int size[kAdapterSmallTokens];
-    uint8_t tok[kAdapterSmallTokens][kGroup];
+    int16_t ids[kAdapterSmallTokens];            // of each group (-1: no adapter)
+    uint8_t size[kAdapterSmallTokens];
     uint8_t rank[kMaxSiblings][kAdapterSmallTokens];
-    int warp[kWarps];                            // groups that begin in each warp
-    uint64_t in_warp[LB_MAX_ADAPTERS + 1];       // by id + 1: tokens in each warp, a byte each
+    int starts[kRuns];                           // groups that begin in each run
     uint16_t first[LB_MAX_ADAPTERS + 1];         // by id + 1: its first group
+    union {                                      // the table is read before the first token is written
+        ulonglong2 in_run[LB_MAX_ADAPTERS + 1];  // by id + 1: tokens in each run, a byte each
+        uint16_t tok[kAdapterSmallTokens][kGroup];
+    };
 };
-static_assert(kWarps == 8, "a byte for each warp");
 __device__ __forceinline__ int find_groups(const SmallParams &p, Groups &g)
 {
-    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    int mine = -1;
-    if (t < p.tokens || p.tokens == 1) {
-        mine = __ldg(p.ids + (p.tokens == 1 ? 0 : t));
-        if (mine >= p.count) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int rounds = p.tokens > kThreads ? kRounds : 1;
+    auto id_of = [&](int t) {
+        int id = __ldg(p.ids + t);
+        if (id >= p.count) {
             if (blockIdx.x == 0) set_status(p.status, LB_ERR_INVALID_ARGUMENT);
-            mine = -1;
+            id = -1;
         }
-        mine = max(mine, -1);
-    }
+        return max(id, -1);
+    };
     auto rank_of = [&](const AdapterProj &P, int id) {
         return (uint8_t)(id < 0 ? 0 : P.ranks == nullptr ? P.rank : max(0, min(P.rank, __ldg(P.ranks + id))));
     };
     if (p.tokens == 1) {  // every thread has its id
-        if (t < p.nproj) g.rank[t][0] = rank_of(p.proj[t], mine);
-        if (t == 0) {
-            g.ids[0] = mine;
+        const int id = id_of(0);
+        if (threadIdx.x < p.nproj) g.rank[threadIdx.x][0] = rank_of(p.proj[threadIdx.x], id);
+        if (threadIdx.x == 0) {
+            g.ids[0] = (int16_t)id;
             g.size[0] = 1;
             g.tok[0][0] = 0;
         }
         __syncthreads();
         return 1;
     }
-    const bool on = t < p.tokens;
-    const uint32_t peers = __match_any_sync(0xffffffffu, on ? mine : -2), earlier = peers & ((1u << lane) - 1u);
-    if (on) g.in_warp[mine + 1] = 0;
-    __syncthreads();
-    if (on && earlier == 0) reinterpret_cast<uint8_t *>(&g.in_warp[mine + 1])[w] = (uint8_t)__popc(peers);
-    __syncthreads();
-    int before = __popc(earlier), all = 0;  // tokens of the same adapter: earlier ones; all
-    if (on) {
-        const uint64_t c = g.in_warp[mine + 1];
+    int mine[kRounds], before[kRounds], all[kRounds], led[kRounds];
+    uint32_t peers[kRounds];
+    const uint32_t lower = (1u << lane) - 1u;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            const int k = (int)(c >> (8 * i)) & 0xff;
-            before += i < w ? k : 0;
-            all += k;
+    for (int i = 0; i < kRounds; ++i) {
+        const int t = i * kThreads + threadIdx.x;
+        mine[i] = t < p.tokens ? id_of(t) : -2;
+        if (i < rounds) peers[i] = __match_any_sync(0xffffffffu, mine[i]);
+        if (mine[i] > -2) g.in_run[mine[i] + 1] = make_ulonglong2(0, 0);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+        if (mine[i] > -2 && (peers[i] & lower) == 0)
+            reinterpret_cast<uint8_t *>(&g.in_run[mine[i] + 1])[i * kWarps + w] = (uint8_t)__popc(peers[i]);
+    __syncthreads();
+    int begin[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        before[i] = all[i] = 0;  // tokens of the same adapter: earlier ones; all
+        if (mine[i] > -2) {
+            const ulonglong2 c = g.in_run[mine[i] + 1];
+            before[i] = __popc(peers[i] & lower);
+#pragma unroll
+            for (int k = 0; k < kRuns; ++k) {
+                const int n = (int)((k < 8 ? c.x : c.y) >> (8 * (k & 7))) & 0xff;
+                before[i] += k < i * kWarps + w ? n : 0;
+                all[i] += n;
+            }
         }
-    }
-    const int mygroups = on && before == 0 ? (all + kGroup - 1) / kGroup : 0;
-    int at = mygroups;  // inclusive over the warp, then exclusive over the call
+        led[i] = mine[i] > -2 && before[i] == 0 ? (all[i] + kGroup - 1) / kGroup : 0;
+        begin[i] = led[i];
+        if (i < rounds) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int k = __shfl_up_sync(0xffffffffu, at, o);
-        at += lane >= o ? k : 0;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int k = __shfl_up_sync(0xffffffffu, begin[i], o);
+                begin[i] += lane >= o ? k : 0;
+            }
+        }
+        if (lane == 31) g.starts[i * kWarps + w] = begin[i];
+        begin[i] -= led[i];
     }
-    if (lane == 31) g.warp[w] = at;
     __syncthreads();
-    at -= mygroups;
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        at += i < w ? g.warp[i] : 0;
-        n += g.warp[i];
+    for (int k = 0; k < kRuns; ++k) {
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) begin[i] += k < i * kWarps + w ? g.starts[k] : 0;
+        n += g.starts[k];
     }
-    if (mygroups > 0) g.first[mine + 1] = (uint16_t)at;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+        if (led[i] > 0) g.first[mine[i] + 1] = (uint16_t)begin[i];
     __syncthreads();
-    if (on) {
-        const int k = g.first[mine + 1] + before / kGroup;
-        g.tok[k][before % kGroup] = (uint8_t)t;
-        if (before % kGroup == 0) {
-            g.ids[k] = mine;
-            g.size[k] = min(kGroup, all - before);
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        if (mine[i] > -2) {
+            const int k = g.first[mine[i] + 1] + before[i] / kGroup;
+            g.tok[k][before[i] % kGroup] = (uint16_t)(i * kThreads + threadIdx.x);
+            if (before[i] % kGroup == 0) {
+                g.ids[k] = (int16_t)mine[i];
+                g.size[k] = (uint8_t)min(kGroup, all[i] - before[i]);
+            }
         }
     }
     __syncthreads();
-    for (int i = t; i < n * p.nproj; i += kThreads) {
+    for (int i = threadIdx.x; i < n * p.nproj; i += kThreads) {
         const int j = i / n, k = i - j * n;
         g.rank[j][k] = rank_of(p.proj[j], g.ids[k]);
     }
@@ -291,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, expand_ctas(KS)) small_expand_kernel
     float scale;
     auto load = [&]() {
         const AdapterProj &P = p.proj[j];
-        const int id = max(grp.ids[g], 0);
+        const int id = max((int)grp.ids[g], 0);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const int o = out0 + 8 * (row >> 1) + 2 * b + (row & 1);
@@ -441,17 +471,20 @@ size_t small_workspace(int M, int n_in, int nproj, const int *ranks)
 
 }  // namespace
 
+// Whether a call runs here: see the top of this file.
+static bool small_batch(int tokens, int count) { return tokens <= std::min(kAdapterSmallTokens, 128 + 48 * count); }
+
 size_t adapters_workspace_bytes(int tokens, int n_in, int count, int nproj, const int *ranks)
 {
-    return tokens > kAdapterSmallTokens ? adapters_mma_workspace_bytes(tokens, count, nproj, ranks)
-                                        : small_workspace(tokens, n_in, nproj, ranks);
+    return small_batch(tokens, count) ? small_workspace(tokens, n_in, nproj, ranks)
+                                      : adapters_mma_workspace_bytes(tokens, count, nproj, ranks);
 }
 
 cudaError_t adapters_prepare_device(const DeviceInfo &dev) { return adapters_mma_prepare_device(dev); }
 
 cudaError_t adapters_forward(const AdaptersArgs &a, const DeviceInfo &dev, cudaStream_t stream)
 {
-    return a.tokens > kAdapterSmallTokens ? adapters_mma_forward(a, dev, stream) : small_adapters(a, dev, stream);
+    return small_batch(a.tokens, a.count) ? small_adapters(a, dev, stream) : adapters_mma_forward(a, dev, stream);
 }
 
 size_t adapters_backward_workspace_bytes(int tokens, int count, int rank)

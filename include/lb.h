@@ -365,11 +365,13 @@ LB_API lb_status lb_linear_backward(const uint16_t *x, const uint16_t *dy, int64
  *                  updated in place.  base may be y; it must not overlap it
  *                  in another way.  The outputs must not overlap each other,
  *                  x or the workspace.
- * Numerics: products accumulate in fp32; A_i x is kept in fp32, or beyond
- *   LB_ADAPTERS_SMALL_TOKENS tokens as the sum of two bf16 (16 bits and the
- *   sign); base is added in fp32 and y rounded to bf16 once.  Every sum runs
- *   in a fixed order: results are deterministic.  A token's result does not
- *   depend on the other tokens' values (an infinity or NaN stays in its row).
+ * Numerics: products accumulate in fp32; A_i x is kept in fp32, or in larger
+ *   batches (always beyond LB_ADAPTERS_SMALL_TOKENS tokens, and from 177 on
+ *   where few adapters are in the pool) as the sum of two bf16 (16 bits and
+ *   the sign); base is added in fp32 and y rounded to bf16 once.  Every sum
+ *   runs in a fixed order: results are deterministic.  A token's result does
+ *   not depend on the other tokens' values (an infinity or NaN stays in its
+ *   row).
  * lb_adapters_backward: for one projection, given dy = dL/dy,
  *     dA_i = s_i sum_m (B_i^T dy[m]) x[m]^T,   dB_i = s_i sum_m dy[m] (A_i x[m])^T,
  *     dx[m] = dx_base[m] + s_i A_i^T (B_i^T dy[m]),
@@ -379,16 +381,21 @@ LB_API lb_status lb_linear_backward(const uint16_t *x, const uint16_t *dy, int64
  *        no token uses.
  *   dx_base, lddxbase : as base above (the layer's own dx; NULL: dx itself).
  *   dx : bf16 [tokens x n_in], or NULL for none.
- *   Numerics: B_i^T dy and A_i x travel as the sum of two bf16 each; fp32
- *   accumulation in a fixed order.  tokens == 0 sets da and db to zero.
+ *   Numerics: B_i^T dy and A_i x travel as the sum of three bf16 each (24
+ *   bits) to da and db, of the first two to dx; fp32 accumulation in a fixed
+ *   order.  tokens == 0 sets da and db to zero.
  * Shapes, alignment and strides as lb_linear_forward, at most 2^20 tokens; a,
  *   b, da and db 16-byte aligned, ids, scale and ranks 4-byte aligned.  No token is a no-op for
  *   the forward call.  The workspace as there: its contents on entry do not
  *   matter, and calls that share it must be ordered on one stream.
+ *   ids and the pool (a, b, scale, ranks) may be read before the work ahead on
+ *   the stream has finished, where that work lets a launch behind it start
+ *   early (programmatic dependent launch): a kernel that writes them must not
+ *   do so.  None of this library's does both.
  * Errors as lb_linear_forward. */
 #define LB_MAX_ADAPTERS 1024
 #define LB_MAX_ADAPTER_RANK 128
-#define LB_ADAPTERS_SMALL_TOKENS 256
+#define LB_ADAPTERS_SMALL_TOKENS 512
 typedef struct {
     const uint16_t *a;
     const uint16_t *b;
@@ -448,6 +455,8 @@ LB_API lb_status lb_adapters_backward(const uint16_t *x, const uint16_t *dy, int
  * Shapes: head_dim a multiple of 8 up to 256, rotary_dim a multiple of 8 from 0
  *   to head_dim, heads >= 1 and at most 4096 in all, eps >= 0 and finite.  ld multiples of
  *   8 up to 2^30, bf16 tensors and the workspace 16-byte aligned, the rest 4-byte.
+ *   positions, inv_freq and weight may be read before the work ahead on the
+ *   stream has finished, as ids and the pool are above.
  * Errors as lb_linear_forward. */
 typedef enum { LB_ROTATE_HALVES = 0, LB_ROTATE_PAIRS = 1 } lb_rotation;
 typedef struct {

@@ -21,6 +21,12 @@ FORWARD = [  # tokens, n_in, outputs, ranks of the pools, count, ids, ranks of t
     (256, 16384, [64], [16], 5, "mixed", [16, 0, 7, 8, 9]),
     (257, 512, [256, 96, 32, 800], [64, 8, 72, 16], 128, "mixed", None),
     (300, 96, [64], [8], 1024, "mixed", None),
+    (416, 160, [96], [24], 6, "some", [24, 0, 1, 8, 23, 9]),
+    (417, 160, [96], [24], 6, "some", [24, 0, 1, 8, 23, 9]),
+    (511, 288, [64, 160], [32, 8], 16, "mixed", None),
+    (512, 64, [288], [128], 64, "runs", None),
+    (512, 1056, [32], [8], 8, "one", None),
+    (513, 1056, [32], [8], 8, "one", None),
     (385, 544, [160, 96], [128, 24], 3, "none", None),
     (600, 128, [96], [16], 4, "mixed", [0, 16, 0, 3]),
     (4096, 256, [160], [128], 5, "mixed", None),
