@@ -27,7 +27,7 @@ std::atomic<int> g_prefill_pairs{1};  // lb_set_prefill_pairs
 std::array<lb::DeviceInfo, kMaxDevices> g_dev;
 std::array<bool, kMaxDevices> g_ready{};
 
-constexpr int64_t kMaxAdapterTokens = int64_t(1) << 20;
+constexpr int64_t kMaxAdapterTokens = int64_t(1) << 20, kMaxAdapterLd = int64_t(1) << 30;
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -67,7 +67,8 @@ lb_status device_info(lb::DeviceInfo *out)
         return LB_ERR_CUDA;
     }
     if (lb::decode_prepare_device(info) != cudaSuccess || lb::prefill_prepare_device(info) != cudaSuccess ||
-        lb::wgrad_prepare_device(info) != cudaSuccess || lb::adapters_prepare_device(info) != cudaSuccess || lb::heads_prepare_device(info) != cudaSuccess) {
+        lb::wgrad_prepare_device(info) != cudaSuccess || lb::adapters_prepare_device(info) != cudaSuccess ||
+        lb::heads_prepare_device(info) != cudaSuccess) {
         cudaGetLastError();
         return LB_ERR_CUDA;
     }
@@ -588,6 +589,7 @@ static lb_status build_adapters(const uint16_t *x, int64_t tokens, int64_t n_in,
     if (n_in % 32 != 0 || n_in > kMaxDim || tokens > kMaxAdapterTokens) return LB_ERR_UNSUPPORTED_SHAPE;
     if (!sizes_only) {
         if (!x || !ids || ldx < n_in) return LB_ERR_INVALID_ARGUMENT;
+        if (ldx > kMaxAdapterLd) return LB_ERR_UNSUPPORTED_SHAPE;
         if (ldx % 8 != 0 || !aligned16(x) || !aligned4(ids)) return LB_ERR_MISALIGNED;
     }
     *a = lb::AdaptersArgs{};
@@ -609,6 +611,7 @@ static lb_status build_adapters(const uint16_t *x, int64_t tokens, int64_t n_in,
         if (sizes_only) continue;
         if (!pj.y || pj.ldy < pj.n_out || (pj.base && pj.ldbase < pj.n_out)) return LB_ERR_INVALID_ARGUMENT;
         if (pj.base == pj.y && pj.ldbase != pj.ldy) return LB_ERR_INVALID_ARGUMENT;
+        if (pj.ldy > kMaxAdapterLd || (pj.base && pj.ldbase > kMaxAdapterLd)) return LB_ERR_UNSUPPORTED_SHAPE;
         if (pj.ldy % 8 != 0 || !aligned16(pj.y) || (pj.base && (pj.ldbase % 8 != 0 || !aligned16(pj.base))))
             return LB_ERR_MISALIGNED;
         d.a = pj.adapters->a;
@@ -687,6 +690,8 @@ lb_status lb_adapters_backward(const uint16_t *x, const uint16_t *dy, int64_t to
         return LB_ERR_INVALID_ARGUMENT;
     if (dx && dx_base == dx && lddxbase != lddx) return LB_ERR_INVALID_ARGUMENT;
     if (!adapters_backward_sizes(tokens, n_in, n_out)) return LB_ERR_UNSUPPORTED_SHAPE;
+    if (ldx > kMaxAdapterLd || lddy > kMaxAdapterLd || (dx && (lddx > kMaxAdapterLd || (dx_base && lddxbase > kMaxAdapterLd))))
+        return LB_ERR_UNSUPPORTED_SHAPE;
     lb_status st = check_pool(adapters, false);
     if (st != LB_OK) return st;
     if (ldx % 8 != 0 || lddy % 8 != 0 || !aligned16(x) || !aligned16(dy) || !aligned4(ids)) return LB_ERR_MISALIGNED;

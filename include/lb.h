@@ -380,13 +380,14 @@ LB_API lb_status lb_linear_backward(const uint16_t *x, const uint16_t *dy, int64
  *        both is written: zeros past an adapter's rank and for adapters that
  *        no token uses.
  *   dx_base, lddxbase : as base above (the layer's own dx; NULL: dx itself).
- *   dx : bf16 [tokens x n_in], or NULL for none.
+ *   dx : bf16 [tokens x n_in], or NULL for none.  It must not overlap x or
+ *        dy, which are read while it is written.
  *   Numerics: B_i^T dy and A_i x travel as the sum of three bf16 each (24
  *   bits) to da and db, of the first two to dx; fp32 accumulation in a fixed
  *   order.  tokens == 0 sets da and db to zero.
- * Shapes, alignment and strides as lb_linear_forward, at most 2^20 tokens; a,
- *   b, da and db 16-byte aligned, ids, scale and ranks 4-byte aligned.  No token is a no-op for
- *   the forward call.  The workspace as there: its contents on entry do not
+ * Shapes, alignment and strides as lb_linear_forward, at most 2^20 tokens and
+ *   strides of at most 2^30; a, b, da and db 16-byte aligned, ids, scale and
+ *   ranks 4-byte aligned.  No token is a no-op for the forward call.  The workspace as there: its contents on entry do not
  *   matter, and calls that share it must be ordered on one stream.
  *   ids and the pool (a, b, scale, ranks) may be read before the work ahead on
  *   the stream has finished, where that work lets a launch behind it start

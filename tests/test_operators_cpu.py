@@ -176,3 +176,34 @@ def test_heads_form_against_differences(rotation, rd):
     y, _ = ref.heads(x, pos, freq, rotation, None, 1e-6, d)
     (back, _), _ = ref.heads_backward(None, y, pos, freq, rotation, None, 1e-6, d)
     assert float((back - x).abs().max()) < 1e-12
+
+
+FAR = (1 << 30) + 8
+
+
+@pytest.mark.parametrize("kw", [dict(ldx=FAR), dict(base=0, ldy=FAR), dict(ldy=FAR, ldbase=FAR), dict(base=2 * FAKE, ldbase=FAR)])
+def test_forward_refuses_rows_too_far_apart(L, kw):
+    assert forward(L, **kw) == SHAPE
+
+
+@pytest.mark.parametrize("name", ["ldx", "lddy", "lddx", "ldbase"])
+def test_backward_refuses_rows_too_far_apart(L, name):
+    ld = dict(ldx=64, lddy=96, lddx=64, ldbase=64)
+    ld[name] = FAR
+    p = pool()
+    assert L.lb_adapters_backward(FAKE, FAKE, 5, 64, 96, ld["ldx"], ld["lddy"], FAKE, ctypes.byref(p), 2 * FAKE, ld["ldbase"],
+                                  FAKE, ld["lddx"], FAKE, FAKE, FAKE, 1 << 24, None) == SHAPE
+
+
+@pytest.mark.parametrize("kw", [dict(ld_in=FAR), dict(ld_out=FAR)])
+def test_heads_refuse_rows_too_far_apart(L, kw):
+    assert heads(L, **kw) == SHAPE
+
+
+def test_workspace_follows_the_kernels(L):
+    """Small batches need partial sums alone, more tokens than the pool allows
+    for them the plan and tiles too; the query knows both sides of the border."""
+    for count in (1, 6, 1000):
+        border = min(512, 128 + 48 * count)
+        sizes = [lb.adapters_workspace_bytes(t, 64, count, (16,)) for t in (1, border, border + 1)]
+        assert 0 < sizes[0] <= sizes[1] < sizes[2]
