@@ -577,11 +577,19 @@ def _require_vector(t, name: str, n: int, dtype, device) -> None:
 def _current(t, name: str):
     """The device of `t`, which must be the current one: the library launches there."""
     device = t.device
-    if device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be in device memory")
     if device.index != _torch().cuda.current_device():
         raise ValueError(f"{name} is on {device}, which is not the current device")
     return device
+
+
+def _stream_of(stream, device):
+    """_stream_handle for a call whose tensors are on `device`, the current one."""
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    if stream is None and raw is not None:
+        return raw(device.index)
+    return _stream_handle(stream)
 
 
 def _held(t, stream):
@@ -700,7 +708,7 @@ def adapters_forward(x, ids, pools, bases=None, ys=None, workspace=None, stream=
         e.adapters = pool._p
         if bases is not None:
             base = bases[j]
-            e.ldbase = _rows_ld(base, f"bases[{j}]", tokens, n_out, bf16, device)
+            e.ldbase = _rows_ld(base, "bases", tokens, n_out, bf16, device)
             e.base = base.data_ptr()
         if ys is None:
             y = torch.empty_strided((tokens, n_out), (n_out, 1), dtype=bf16, device=device)
@@ -710,7 +718,7 @@ def adapters_forward(x, ids, pools, bases=None, ys=None, workspace=None, stream=
             e.ldy = n_out
         else:
             y = ys[j]
-            e.ldy = _rows_ld(y, f"ys[{j}]", tokens, n_out, bf16, device)
+            e.ldy = _rows_ld(y, "ys", tokens, n_out, bf16, device)
         e.y = y.data_ptr()
     if workspace is None:
         workspace = _new_workspace(x, adapters_workspace_bytes(tokens, n_in, c.count, tuple(ranks)), stream)
@@ -718,7 +726,7 @@ def adapters_forward(x, ids, pools, bases=None, ys=None, workspace=None, stream=
         _require_workspace(workspace)
     _check(lib().lb_adapters_forward(
         x.data_ptr(), tokens, n_in, x.stride(0) if tokens > 1 else n_in, ids_ptr, n, arr, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream_handle(stream)), "lb_adapters_forward")
+        workspace.numel() * workspace.element_size(), _stream_of(stream, device)), "lb_adapters_forward")
     return made if ys is None else ys
 
 
@@ -755,15 +763,16 @@ def adapters_backward(x, dy, ids, pool: AdapterPool, dx_base=None, dx=None, want
     lddx = _rows_ld(dx, "dx", tokens, n_in, bf16, device) if dx is not None else n_in
     with_base = dx is not None and dx_base is not None
     ldbase = _rows_ld(dx_base, "dx_base", tokens, n_in, bf16, device) if with_base else n_in
-    for name, t, shape in (("da", da, (c.count, c.rank, n_in)), ("db", db, (c.count, n_out, c.rank))):
+    count, rank = c.count, c.rank
+    for name, t, shape in (("da", da, (count, rank, n_in)), ("db", db, (count, n_out, rank))):
         if t is not None and (t.dtype != f32 or t.shape != shape or not t.is_contiguous() or t.device != device):
             raise ValueError(f"{name} must be a contiguous {shape} float32 tensor on {device}")
     if da is None:
-        da = _held(torch.empty((c.count, c.rank, n_in), dtype=f32, device=device), stream)
+        da = _held(torch.empty_strided((count, rank, n_in), (rank * n_in, n_in, 1), dtype=f32, device=device), stream)
     if db is None:
-        db = _held(torch.empty((c.count, n_out, c.rank), dtype=f32, device=device), stream)
+        db = _held(torch.empty_strided((count, n_out, rank), (n_out * rank, rank, 1), dtype=f32, device=device), stream)
     if workspace is None:
-        need = adapters_backward_workspace_bytes(tokens, n_in, n_out, c.count, c.rank)
+        need = adapters_backward_workspace_bytes(tokens, n_in, n_out, count, rank)
         workspace = _new_workspace(x, need, stream)
     else:
         _require_workspace(workspace)
@@ -771,7 +780,7 @@ def adapters_backward(x, dy, ids, pool: AdapterPool, dx_base=None, dx=None, want
         x.data_ptr(), dy.data_ptr(), tokens, n_in, n_out, x.stride(0) if tokens > 1 else n_in, lddy, ids_ptr,
         pool._p, dx_base.data_ptr() if with_base else None, ldbase, dx.data_ptr() if dx is not None else None, lddx,
         da.data_ptr(), db.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _stream_handle(stream)), "lb_adapters_backward")
+        _stream_of(stream, device)), "lb_adapters_backward")
     return {"dx": dx, "da": da, "db": db}
 
 
@@ -808,7 +817,7 @@ def _heads_call(tensors, positions, rotation: HeadRotation, weights, name: str):
         raise ValueError(f"1 to {MAX_SIBLINGS} tensors, got {n}")
     if weights is not None and len(weights) != n:
         raise ValueError(f"weights must have one entry for each of the {n} tensors")
-    device = _current(tensors[0], f"{name}[0]")
+    device = _current(tensors[0], name)
     tokens = tensors[0].shape[0]
     if rotation.rotary_dim == 0:
         return device, tokens, None, None
@@ -818,10 +827,12 @@ def _heads_call(tensors, positions, rotation: HeadRotation, weights, name: str):
     return device, tokens, pos, rotation.inv_freq.data_ptr()
 
 
-def _heads_of(t, name: str, head_dim: int) -> int:
-    if t.dim() != 2 or head_dim < 1 or t.shape[1] % head_dim:
-        raise ValueError(f"{name} must be [tokens, heads * {head_dim}], got {tuple(t.shape)}")
-    return t.shape[1] // head_dim
+def _heads_of(t, name: str, head_dim: int) -> tuple:
+    """The heads and columns of `t`."""
+    shape = t.shape
+    if len(shape) != 2 or head_dim < 1 or shape[1] % head_dim:
+        raise ValueError(f"{name} must be [tokens, heads * {head_dim}], got {tuple(shape)}")
+    return shape[1] // head_dim, shape[1]
 
 
 def heads_norm_rotate(tensors, positions, rotation: HeadRotation, weights=None, outs=None, stream=None):
@@ -839,9 +850,8 @@ def heads_norm_rotate(tensors, positions, rotation: HeadRotation, weights=None, 
     made = []
     for j, t in enumerate(tensors):
         e = arr[j]
-        e.heads = _heads_of(t, f"tensors[{j}]", d)
-        cols = t.shape[1]
-        e.ld_in = _rows_ld(t, f"tensors[{j}]", tokens, cols, bf16, device)
+        e.heads, cols = _heads_of(t, "tensors", d)
+        e.ld_in = _rows_ld(t, "tensors", tokens, cols, bf16, device)
         e.in_ = t.data_ptr()
         if outs is None:
             o = _held(torch.empty_strided((tokens, cols), (cols, 1), dtype=bf16, device=device), stream)
@@ -849,12 +859,12 @@ def heads_norm_rotate(tensors, positions, rotation: HeadRotation, weights=None, 
             e.ld_out = cols
         else:
             o = outs[j]
-            e.ld_out = _rows_ld(o, f"outs[{j}]", tokens, cols, bf16, device)
+            e.ld_out = _rows_ld(o, "outs", tokens, cols, bf16, device)
         e.out = o.data_ptr()
         if weights is not None and weights[j] is not None:
-            e.weight = _vector_ptr(weights[j], f"weights[{j}]", d, bf16, device)
+            e.weight = _vector_ptr(weights[j], "weights", d, bf16, device)
     _check(lib().lb_heads_norm_rotate(tokens, d, rotation.rotary_dim, rotation.code, pos, freq, rotation.eps,
-                                      len(tensors), arr, _stream_handle(stream)), "lb_heads_norm_rotate")
+                                      len(tensors), arr, _stream_of(stream, device)), "lb_heads_norm_rotate")
     return made if outs is None else outs
 
 
@@ -882,22 +892,21 @@ def heads_norm_rotate_backward(tensors, douts, positions, rotation: HeadRotation
     sums = False
     for j, t in enumerate(tensors):
         e = arr[j]
-        e.heads = _heads_of(t, f"tensors[{j}]", d)
-        cols = t.shape[1]
-        e.ld_in = _rows_ld(t, f"tensors[{j}]", tokens, cols, bf16, device)
+        e.heads, cols = _heads_of(t, "tensors", d)
+        e.ld_in = _rows_ld(t, "tensors", tokens, cols, bf16, device)
         e.in_ = t.data_ptr()
-        e.ld_dout = _rows_ld(douts[j], f"douts[{j}]", tokens, cols, bf16, device)
+        e.ld_dout = _rows_ld(douts[j], "douts", tokens, cols, bf16, device)
         e.dout = douts[j].data_ptr()
         if dins is None:
             din = _held(torch.empty_strided((tokens, cols), (cols, 1), dtype=bf16, device=device), stream)
             e.ld_din = cols
         else:
             din = dins[j]
-            e.ld_din = _rows_ld(din, f"dins[{j}]", tokens, cols, bf16, device)
+            e.ld_din = _rows_ld(din, "dins", tokens, cols, bf16, device)
         e.din = din.data_ptr()
         out.append({"din": din})
         if weights is not None and weights[j] is not None:
-            e.weight = _vector_ptr(weights[j], f"weights[{j}]", d, bf16, device)
+            e.weight = _vector_ptr(weights[j], "weights", d, bf16, device)
             if want_dweight:
                 dw = _held(torch.empty_strided((d,), (1,), dtype=torch.float32, device=device), stream)
                 e.dweight = dw.data_ptr()
@@ -909,7 +918,7 @@ def heads_norm_rotate_backward(tensors, douts, positions, rotation: HeadRotation
         _require_workspace(workspace)
     _check(lib().lb_heads_norm_rotate_backward(tokens, d, rotation.rotary_dim, rotation.code, pos, freq, rotation.eps, n,
                                                arr, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                               _stream_handle(stream)), "lb_heads_norm_rotate_backward")
+                                               _stream_of(stream, device)), "lb_heads_norm_rotate_backward")
     return out
 
 
