@@ -19,24 +19,25 @@
 // (programmatic dependent launch).  Tokens that share an adapter read its weights
 // once per kGroup of them, wherever they stand in the batch.  Each CTA finds the
 // groups for itself, once, and takes its units one after the other, the next one's
-// weights asked for before the last is written.
+// weights asked for before the last is written; in expand a CTA's units are a run,
+// so that v is put together once for many of them.
 // Measured, both launches, operands not in L2: 1 token and three projections of
-// 4096 x 4096, rank 16, 3.7 us; 100 tokens, 16 adapters of rank 32, 5120 to 2 x
-// 17408 columns, 20.6 us, 3.0 TB/s (60 us with fp32 FMAs, a thread a row of B: most
+// 4096 x 4096, rank 16, 3.9 us; 100 tokens, 16 adapters of rank 32, 5120 to 2 x
+// 17408 columns, 19.1 us, 3.2 TB/s (60 us with fp32 FMAs, a thread a row of B: most
 // of it spent unpacking and on 16-byte pieces of 32 rows at a time; 36 us with the
 // products but a CTA a unit: most of it spent finding groups, one wave of CTAs
-// after the other); 128 tokens, 32 adapters of rank 128, 4096 x 4096, 19 us, 3.6
-// TB/s.  What is left is the chain of each unit: partials, split, product, store.
+// after the other; 20.5 us with the units dealt out in turn); 128 tokens, 32
+// adapters of rank 128, 4096 x 4096, 19 us, 3.6 TB/s.  What is left is the chain of each unit: partials, split, product, store.
 //
 // For up to 128 + 48 x adapters of the pool tokens, at most kAdapterSmallTokens
 // (512); beyond, and for the backward pass, the tcgen05 kernels of
 // lb_adapters_mma.cu, whose tiles hold 128 tokens of one adapter: they pay where
 // an adapter has many tokens, and how many it has is bounded by the pool.  Here
-// and there: 8 adapters of rank 16, 4096 x 4096, 256 tokens 7.6 and 17.0 us, 512
-// tokens 10.5 and 17.3; 64 of rank 16, 5120 to 7168 columns, 512 tokens 28 and 90;
-// 16 of rank 32, 5120 to 34816, 512 tokens 51 and 66; 4 of rank 64, 4096 to 11008,
-// 320 tokens 17.8 and 19.8, 512 tokens 26 and 23; 1 of rank 64, 4096 to 28672, 128
-// tokens 16.1 and 15.6, 192 tokens 23 and 19.
+// and there: 8 adapters of rank 16, 4096 x 4096, 256 tokens 7.8 and 17.0 us, 512
+// tokens 10.0 and 17.3; 64 of rank 16, 5120 to 7168 columns, 512 tokens 27 and 90;
+// 16 of rank 32, 5120 to 34816, 512 tokens 45 and 66; 4 of rank 64, 4096 to 11008,
+// 320 tokens 16.1 and 19.8, 512 tokens 26 and 23; 1 of rank 64, 4096 to 28672, 128
+// tokens 14.1 and 15.6, 192 tokens 23 and 19.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -288,8 +289,10 @@ __global__ void __launch_bounds__(kThreads, kShrinkCtas) small_shrink_kernel(con
     }
 }
 
-// Units (group, kOutputs outputs of a projection), one after the other.  KS: 32
-// columns of B are a step, and `rank` has at most KS of them.
+// Units (group, kOutputs outputs of a projection); a CTA takes a run of them, so
+// that v is put together once for many units and the next unit's weights and base
+// are under way while this one is added.  KS: 32 columns of B are a step, and
+// `rank` has at most KS of them.
 template <int KS>
 __global__ void __launch_bounds__(kThreads, expand_ctas(KS)) small_expand_kernel(const __grid_constant__ SmallParams p)
 {
@@ -297,65 +300,74 @@ __global__ void __launch_bounds__(kThreads, expand_ctas(KS)) small_expand_kernel
     // s_i v in three bf16 parts, 24 bits: nothing of the fp32 value is lost
     constexpr int kPitch = 32 * KS + 8;  // 16-byte reads of 8 rows fall into 8 different bank groups
     __shared__ alignas(16) uint16_t vs[2][3][kGroup][kPitch];
+    constexpr int kAtOnce = 8;  // partials a thread asks for at once
     const int groups = find_groups(p, grp);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane >> 2, q = lane & 3;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    constexpr int kAtOnce = 8;  // partials a thread asks for at once
     const int chunks = p.chunk0[p.nproj], units = groups * chunks;
-    int g, j, out0, rank;
-    auto find = [&](int unit) {
-        for (; unit < units; unit += gridDim.x) {
-            g = unit / chunks;
-            const int c = unit - g * chunks;
-            j = 0;
-            while (j + 1 < p.nproj && c >= p.chunk0[j + 1]) ++j;
-            out0 = (c - p.chunk0[j]) * kOutputs + warp * kWarpOuts;
-            rank = grp.rank[j][g];
-            if (rank > 0 || p.proj[j].base != p.proj[j].y) break;
+    const int share = units / (int)gridDim.x, longer = units - share * (int)gridDim.x, cta = blockIdx.x;
+    const int begin = cta * share + min(cta, longer), end = begin + share + (cta < longer ? 1 : 0);
+    struct Unit {
+        int g, j, out0, rank;
+    };
+    Unit at;
+    auto find = [&](int unit) {  // the next unit with something to do
+        for (; unit < end; ++unit) {
+            at.g = unit / chunks;
+            const int c = unit - at.g * chunks;
+            at.j = 0;
+            while (at.j + 1 < p.nproj && c >= p.chunk0[at.j + 1]) ++at.j;
+            at.out0 = (c - p.chunk0[at.j]) * kOutputs + warp * kWarpOuts;
+            at.rank = grp.rank[at.j][at.g];
+            if (at.rank > 0 || p.proj[at.j].base != p.proj[at.j].y) break;
         }
         return unit;
     };
     // Column `row` of product b is output 8 (row / 2) + 2 b + row % 2 of the warp's,
     // so that a lane's columns of the four products are 8 outputs in a row, from 8 q on.
-    uint4 w[KS][4];
-    float scale;
-    auto load = [&]() {
-        const AdapterProj &P = p.proj[j];
-        const int id = max((int)grp.ids[g], 0);
+    uint4 w[KS][4], y[2];
+    float scale = 1.0f;
+    auto load_weights = [&]() {
+        const AdapterProj &P = p.proj[at.j];
+        const int id = max((int)grp.ids[at.g], 0);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int o = out0 + 8 * (row >> 1) + 2 * b + (row & 1);
+            const int o = at.out0 + 8 * (row >> 1) + 2 * b + (row & 1);
             const uint16_t *B = P.b + ((int64_t)id * P.n_out + o) * P.rank + 8 * q;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) w[k][b] = o < P.n_out && 32 * k + 8 * q < rank ? ldg_early_v4(B + 32 * k) : zero;
+            for (int k = 0; k < KS; ++k) w[k][b] = o < P.n_out && 32 * k + 8 * q < at.rank ? ldg_early_v4(B + 32 * k) : zero;
         }
         scale = P.scale != nullptr ? __ldg(P.scale + id) : 1.0f;
     };
-    int unit = find(blockIdx.x);
-    if (unit < units) load();
+    auto load_base = [&]() {
+        const AdapterProj &P = p.proj[at.j];
+        const int o = at.out0 + 8 * q;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            y[h] = o < P.n_out && row + 8 * h < grp.size[at.g]
+                       ? *reinterpret_cast<const uint4 *>(P.base + (int64_t)grp.tok[at.g][row + 8 * h] * P.ldbase + o)
+                       : zero;
+    };
+    int unit = find(begin);
+    if (unit < end) load_weights();
     pdl_wait();
     pdl_launch_dependents();
-    for (int turn = 0; unit < units;) {
-        const AdapterProj &P = p.proj[j];
-        const int n = grp.size[g], o = out0 + 8 * q;
-        uint4 y[2] = {zero, zero};
-        uint16_t *to[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            to[h] = nullptr;
-            if (o < P.n_out && row + 8 * h < n) {
-                const int64_t t = grp.tok[g][row + 8 * h];
-                to[h] = P.y + t * P.ldy + o;
-                y[h] = *reinterpret_cast<const uint4 *>(P.base + t * P.ldbase + o);
-            }
-        }
-        if (rank > 0) {
+    if (unit < end) load_base();
+    int turn = 0, vg = -1, vj = -1;  // whose v is in vs[turn]
+    while (unit < end) {
+        const Unit u = at;
+        const AdapterProj &P = p.proj[u.j];
+        const int n = grp.size[u.g], o = u.out0 + 8 * q;
+        if (u.rank > 0 && (u.g != vg || u.j != vj)) {
+            turn ^= 1;  // some threads may still read the other half
+            vg = u.g;
+            vj = u.j;
             const int64_t next = (int64_t)p.tokens * P.rank;
             for (int i = threadIdx.x; i < n * 16 * KS; i += kThreads) {
                 const int t = i / (16 * KS), r = i % (16 * KS) * 2;  // and r + 1
                 float2 v = make_float2(0.0f, 0.0f);
-                if (r < rank) {
-                    const float *part = p.part[j] + (int64_t)grp.tok[g][t] * P.rank + r;
+                if (r < u.rank) {
+                    const float *part = p.part[u.j] + (int64_t)grp.tok[u.g][t] * P.rank + r;
                     for (int s0 = 0; s0 < p.slices; s0 += kAtOnce) {
                         float2 e[kAtOnce];
 #pragma unroll
@@ -366,44 +378,45 @@ __global__ void __launch_bounds__(kThreads, expand_ctas(KS)) small_expand_kernel
                     }
                 }
                 v.x *= scale;
-                v.y = r + 1 < rank ? v.y * scale : 0.0f;  // nothing was written past the rank
+                v.y = r + 1 < u.rank ? v.y * scale : 0.0f;  // nothing was written past the rank
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {  // truncated, so that no part can overflow
-                    const uint32_t x = __float_as_uint(v.x) & 0xffff0000u, y = __float_as_uint(v.y) & 0xffff0000u;
-                    *reinterpret_cast<uint32_t *>(&vs[turn][k][t][r]) = x >> 16 | y;
+                    const uint32_t x = __float_as_uint(v.x) & 0xffff0000u, z = __float_as_uint(v.y) & 0xffff0000u;
+                    *reinterpret_cast<uint32_t *>(&vs[turn][k][t][r]) = x >> 16 | z;
                     v.x = isfinite(v.x) ? v.x - __uint_as_float(x) : 0.0f;
-                    v.y = isfinite(v.y) ? v.y - __uint_as_float(y) : 0.0f;
+                    v.y = isfinite(v.y) ? v.y - __uint_as_float(z) : 0.0f;
                 }
             }
-            __syncthreads();  // the next unit writes the other half of `vs`
-            float d[4][4] = {};
+            __syncthreads();
+        }
+        float d[4][4] = {};
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                if (32 * k < rank) {
+        for (int k = 0; k < KS; ++k) {
+            if (32 * k < u.rank) {
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        const uint4 lo = row < n ? *reinterpret_cast<const uint4 *>(&vs[turn][i][row][32 * k + 8 * q]) : zero;
-                        const uint4 hi = row + 8 < n ? *reinterpret_cast<const uint4 *>(&vs[turn][i][row + 8][32 * k + 8 * q]) : zero;
+                for (int i = 0; i < 3; ++i) {
+                    const uint4 lo = row < n ? *reinterpret_cast<const uint4 *>(&vs[turn][i][row][32 * k + 8 * q]) : zero;
+                    const uint4 hi = row + 8 < n ? *reinterpret_cast<const uint4 *>(&vs[turn][i][row + 8][32 * k + 8 * q]) : zero;
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) mma32(d[b], lo, hi, w[k][b]);
-                    }
+                    for (int b = 0; b < 4; ++b) mma32(d[b], lo, hi, w[k][b]);
                 }
             }
+        }
+        unit = find(unit + 1);
+        if (unit < end) load_weights();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h) {
+            if (u.rank > 0) {
                 uint32_t e[4] = {y[h].x, y[h].y, y[h].z, y[h].w};
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
                     e[b] = pack_bf162(__uint_as_float(e[b] << 16) + d[b][2 * h], __uint_as_float(e[b] & 0xffff0000u) + d[b][2 * h + 1]);
                 y[h] = make_uint4(e[0], e[1], e[2], e[3]);
             }
-            turn ^= 1;  // only where the barrier above was passed
+            if (o < P.n_out && row + 8 * h < n)
+                *reinterpret_cast<uint4 *>(P.y + (int64_t)grp.tok[u.g][row + 8 * h] * P.ldy + o) = y[h];
         }
-        unit = find(unit + gridDim.x);
-        if (unit < units) load();
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (to[h] != nullptr) *reinterpret_cast<uint4 *>(to[h]) = y[h];
+        if (unit < end) load_base();
     }
 }
 
