@@ -349,38 +349,67 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint16_t *src, bool t
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-// This thread's part of ROWS rows x 64 columns: every 16th row from tid / 8 on,
-// 16 bytes at chunk tid % 8, in the layout of a TMA box.  `row` holds the rows
-// (negative: not read; `strict`: as zeros).
+// This thread's part of ROWS rows x 64 columns: every kStep-th row from tid / 8
+// on, 16 bytes at chunk tid % 8, in the layout of a TMA box.  The rows' addresses
+// are found once, so that a copy is an addition and the copy itself: with a
+// multiplication in each, four warps could not keep up with a weight gradient
+// (the backward pass of 8192 tokens in any order, 276 us; 235 us so).  Rows that are not `there` are not read
+// (`strict`: zeros).
 template <int ROWS>
 struct Copier {
-    static constexpr int kN = ROWS / (kLoadThreads / 8);
-    int row[kN];
+    static constexpr int kStep = kLoadThreads / 8, kN = ROWS / kStep;
+    const uint16_t *src[kN];
+    uint32_t there;
     int r0, chunk;
-    __device__ __forceinline__ void rows(const int *perm, int used, int tid)
+    template <typename F>
+    __device__ __forceinline__ void set(const uint16_t *p, int64_t ld, int used, int tid, F row)
     {
         r0 = tid >> 3;
         chunk = tid & 7;
+        there = 0;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) row[i] = r0 + 16 * i < used ? perm[r0 + 16 * i] : -1;
+        for (int i = 0; i < kN; ++i) {
+            const int r = r0 + kStep * i;
+            src[i] = p;
+            if (r < used) {
+                src[i] = p + row(r) * ld;
+                there |= 1u << i;
+            }
+        }
     }
-    __device__ __forceinline__ void run(int first, int used, int tid)
+    __device__ __forceinline__ void rows(const uint16_t *p, int64_t ld, const int *perm, int used, int tid)
     {
-        r0 = tid >> 3;
-        chunk = tid & 7;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) row[i] = r0 + 16 * i < used ? first + r0 + 16 * i : -1;
+        set(p, ld, used, tid, [&](int r) { return perm[r]; });
     }
-    __device__ __forceinline__ void copy(uint32_t dst, const uint16_t *p, int64_t ld, int cols, int col, bool strict) const
+    __device__ __forceinline__ void run(const uint16_t *p, int64_t ld, int first, int used, int tid)
+    {
+        set(p, ld, used, tid, [&](int r) { return first + r; });
+    }
+    // BOXES of 64 columns from `col` on
+    template <int BOXES>
+    __device__ __forceinline__ void copy(uint32_t dst, uint32_t box, int cols, int col, bool strict) const
     {
         const int c = col + 8 * chunk;
-        const uint32_t at = dst + r0 * 128u + (uint32_t)((chunk ^ (r0 & 7)) << 4);  // rows 16 apart: the same swizzle
+        const uint32_t at = dst + r0 * 128u + (uint32_t)((chunk ^ (r0 & 7)) << 4);  // rows kStep apart: the same swizzle
+        if (c + 64 * (BOXES - 1) < cols) {
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-            if (row[i] >= 0)
-                copy16(at + 2048u * i, c < cols ? p + row[i] * ld + c : p, c < cols);
-            else if (strict)
-                copy16(at + 2048u * i, p, false);
+            for (int i = 0; i < kN; ++i) {
+                const bool in = there >> i & 1u;
+                const uint16_t *from = src[i] + c;
+#pragma unroll
+                for (int b = 0; b < BOXES; ++b)
+                    if (strict || in) copy16(at + 128u * kStep * i + b * box, from + 64 * b, in);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+#pragma unroll
+                for (int b = 0; b < BOXES; ++b) {
+                    const bool in = (there >> i & 1u) && c + 64 * b < cols;
+                    copy16(at + 128u * kStep * i + b * box, src[i] + (in ? c + 64 * b : 0), in);
+                }
+            }
+        }
     }
 };
 
@@ -581,7 +610,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
                 const int64_t ld = J.x.ld;
                 const int cols = J.x.cols;
                 Copier<TM> mine;
-                mine.rows(p.plan.perm + q.tile * TM, T.rows, 32 * loader + lane);
+                mine.rows(x, ld, p.plan.perm + q.tile * TM, T.rows, 32 * loader + lane);
                 loaders_meet();  // the first is here, so nobody is ahead of the ring
                 for (int kb = q.kb; kb < q.kb + q.n; ++kb) {
                     const bool ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
@@ -594,7 +623,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
                         load_w(kb);
                     }
                     __syncwarp();
-                    mine.copy(base + s * S::kStage, x, ld, cols, 64 * kb, false);
+                    mine.copy<1>(base + s * S::kStage, 0, cols, 64 * kb, false);
                     mbar_arrive_after_copies(full0 + 8 * s);
                     if (++s == S::kStages) s = 0, ph ^= 1;
                 }
@@ -918,8 +947,6 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
         uint32_t ph = 1;
         bool mn = false, run = false;
         const CUtensorMap *mb = nullptr, *mw = nullptr;
-        const uint16_t *x = nullptr;
-        int64_t ld = 0;
         int cols = 0;
         Copier<TM> mine;
         Walk q = start();
@@ -929,12 +956,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
                 mn = J.mn != 0;
                 mb = &J.base.box;
                 mw = &J.w;
-                x = J.base.p;
-                ld = J.base.ld;
                 cols = J.base.cols;
                 run = q.t.run();
                 if (!run) {
-                    mine.rows(p.plan.perm + q.tile * TM, q.t.rows, 32 * loader + lane);
+                    mine.rows(J.base.p, J.base.ld, p.plan.perm + q.tile * TM, q.t.rows, 32 * loader + lane);
                     loaders_meet();  // the first is here, so nobody is ahead of the ring
                 }
             }
@@ -969,8 +994,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
                 }
                 __syncwarp();
                 if (ok && !run) {
-                    mine.copy(dst + S::kW, x, ld, cols, c0, false);
-                    mine.copy(dst + S::kW + kBaseBytes / 2, x, ld, cols, c0 + 64, false);
+                    mine.copy<2>(dst + S::kW, kBaseBytes / 2, cols, c0, false);
                     mbar_arrive_after_copies(bar);
                 }
                 if (++s == S::kStages) s = 0, ph ^= 1;
@@ -1320,7 +1344,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
         uint32_t ph = 1;
         Product<NK> q(p, w0, w0 < w1);
         bool waited = false;
-        for (int w = w0; w < w1;) {  // to the end in every loader, whatever happens: they meet
+        for (int w = w0; w < w1;) {  // to the end in every loader, whatever happens
             const int n = min(q.nkb - q.kb, w1 - w);
             const WgradJob &J = p.job[q.job];
             const CUtensorMap *mx = &J.x.box, *mv = J.v;
@@ -1330,22 +1354,26 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
             Tile T = q.first;
             if (q.kb >= 2) T = p.plan.tiles[tile0 + q.kb / 2];
             Tile next = T;
+            Copier<64> mine, ahead;
+            auto find = [&](Copier<64> &c, const Tile &t, int kb) {  // the rows of a K-block that is no box
+                const int left = t.rows - 64 * (kb & 1);
+                if (t.run() && left < 64) c.run(x, ld, t.first + 64 * (kb & 1), left, 32 * loader + lane);
+                if (!t.run()) c.rows(x, ld, p.plan.perm + tile0 * TM + 64 * kb, left, 32 * loader + lane);
+            };
+            find(mine, T, q.kb);
             for (int kb = q.kb; kb < end; ++kb) {
                 const int half = kb & 1;
                 if (half == 0) T = next;
                 if (half == 0 || kb == q.kb) {  // ahead of use
                     if ((kb | 1) + 1 < end) next = p.plan.tiles[tile0 + kb / 2 + 1];
                 }
+                if (kb + 1 < end) find(ahead, half == 0 ? T : next, kb + 1);
                 const uint32_t dst = base + s * S::kStage, bar = full0 + 8 * s;
                 const int slot = tile0 * TM + 64 * kb;
                 const bool run = T.run() && T.rows >= 64 * half + 64;
-                if (!run) loaders_meet();  // the first is here, so nobody is ahead of the ring
-                bool ok = true;
-                if (loader <= 1 || !run) {
-                    ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) abort_flag = 1;
-                }
+                bool ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);  // all loaders: nobody is ahead of the ring
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) abort_flag = 1;
                 if (ok && loader == 0 && elect_one()) {
                     mbar_arrive_expect_tx(bar, S::kStage - (run ? 0u : S::kX));
                     if (run) {
@@ -1357,13 +1385,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
                 }
                 __syncwarp();
                 if (ok && !run) {  // zeros past the adapter's tokens: the slots are what is summed over
-                    Copier<64> mine;
-                    if (T.run())
-                        mine.run(T.first + 64 * half, T.rows - 64 * half, 32 * loader + lane);
-                    else
-                        mine.rows(p.plan.perm + slot, T.rows - 64 * half, 32 * loader + lane);
-#pragma unroll
-                    for (int c = 0; c < 2 * S::kTiles; ++c) mine.copy(dst + c * kBox, x, ld, J.x.cols, q.n0 + 64 * c, true);
+                    mine.copy<2 * S::kTiles>(dst, kBox, J.x.cols, q.n0, true);
                     mbar_arrive_after_copies(bar);
                 }
                 if (loader == 1) {
@@ -1381,6 +1403,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
                     }
                     __syncwarp();
                 }
+                mine = ahead;
                 if (++s == S::kStages) s = 0, ph ^= 1;
             }
             w += n;
