@@ -1090,8 +1090,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
         // the stage is given back a unit later.
         int s = 0, na = 0, tok = 0, n = 0, held = -1;
         uint32_t ph = 0;
-        uint16_t *y = nullptr;  // this lane's columns of the job
-        int64_t ldy = 0;
+        uint16_t *to[8];  // where this lane's columns of the job go
         bool run = false;
         int row0 = 0;
         const CUtensorMap *my = nullptr;
@@ -1104,8 +1103,14 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
                 run = __all_sync(0xffffffffu, tok < tokens && tok == row0 + lane);
                 my = &J.y;
                 n = J.n;
-                y = J.y_rows + 64 * half + 8 * (lane & 7);
-                ldy = J.ldy;
+                if (!run) {
+                    uint16_t *y = J.y_rows + 64 * half + 8 * (lane & 7);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int t = __shfl_sync(0xffffffffu, tok, 4 * i + (lane >> 3));
+                        to[i] = t < tokens ? y + t * J.ldy : nullptr;
+                    }
+                }
             }
             if (q.kind == 0) {
                 if (u + 1 < u1) advance(q);
@@ -1178,10 +1183,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
                     mbar_arrive(empty0 + 8 * s);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int t = __shfl_sync(0xffffffffu, tok, 4 * i + (lane >> 3));
-                    if (t < tokens && in) *reinterpret_cast<uint4 *>(y + (int64_t)t * ldy + c0) = o[i];
-                }
+                for (int i = 0; i < 8; ++i)
+                    if (to[i] != nullptr && in) *reinterpret_cast<uint4 *>(to[i] + c0) = o[i];
             }
             if (++s == S::kStages) s = 0, ph ^= 1;
             if (u + 1 < u1) advance(q);
