@@ -87,7 +87,11 @@ struct PlanParams {
 };
 
 constexpr int kPlanThreads = 1024, kPlanWarps = 32;
-constexpr int kHeld = 8192;  // tokens whose bins stay in shared memory between the two passes
+constexpr int kHeld = 8192;  // tokens that stay in shared memory between the two passes
+constexpr int kBinBits = 11;
+static_assert(LB_MAX_ADAPTERS < 1 << kBinBits, "a bin, and above it a place");
+constexpr int kPlanTokens = 1 << 20;  // the most; the sums over adapters of tiles and blocks share 32 bits
+static_assert(kPlanTokens / TM + LB_MAX_ADAPTERS < 1 << 14 && kPlanTokens / 64 + LB_MAX_ADAPTERS < 1 << 18, "tiles, blocks");
 
 // Each warp takes a run of tokens in order, so that an adapter's tokens keep
 // their order and sums over them do not depend on timing.  One CTA runs this
@@ -97,12 +101,12 @@ constexpr int kHeld = 8192;  // tokens whose bins stay in shared memory between 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
 {
     extern __shared__ int hist[];  // [warp][bin]; bin `count`: no adapter
-    __shared__ unsigned long long sums[kPlanWarps];
+    __shared__ uint32_t sums[kPlanWarps];
     __shared__ int first_tile[LB_MAX_ADAPTERS + 1], total[LB_MAX_ADAPTERS + 1];
-    __shared__ int held[kHeld];  // bins, then slots
+    __shared__ int held[kHeld];  // bins, with places among a warp's tokens of a bin, then slots
     const int bins = p.count + 1, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int rounds = (p.tokens + kPlanThreads - 1) / kPlanThreads;
-    const int t0 = w * rounds * 32 + lane, bits = 32 - __clz(p.count);
+    const int t0 = w * rounds * 32 + lane;
     int *mine = hist + w * bins;
     const bool hold = p.tokens <= kHeld;
     auto bin_of = [&](int id) {
@@ -137,7 +141,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         waited = true;
     };
     int all_tiles = 0, tile0 = 0, n = 0, block0 = 0, all_blocks = 0;
-    // pass 0 counts each warp's tokens of each bin, pass 1 gives them their slots
+    // pass 0 counts each warp's tokens of each bin, pass 1 gives them their slots:
+    // from the places that pass 0 kept, or by counting again
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
@@ -145,28 +150,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
             const int t = t0 + 32 * i;
             int b = -1;
             if (t < p.tokens) b = hold ? held[t] : bin_of(__ldg(p.ids + t));
-            // the lanes with the same bin, by a vote on each of its bits
-            uint32_t same = __ballot_sync(0xffffffffu, b >= 0);
-#pragma unroll 1
-            for (int k = 0; k < bits; ++k) {
-                const bool set = (b >> k) & 1;
-                const uint32_t vote = __ballot_sync(0xffffffffu, set);
-                same &= set ? vote : ~vote;
-            }
+            const uint32_t same = __match_any_sync(0xffffffffu, b);  // the lanes with the same bin
             const int had = b >= 0 ? mine[b] : 0;
             __syncwarp();
             if (b >= 0) {
                 const int rank = __popc(same & ((1u << lane) - 1u));
-                if (pass == 1) {
-                    const int at = had + rank;
-                    if (hold) {  // written with the others, after the wait
-                        held[t] = first_tile[b] * TM + at;
-                        if (at % TM == 0) held[t] |= kFirst;
-                        if (at % TM == TM - 1 || at == total[b] - 1) held[t] |= kLast;
-                    } else {
-                        put(t, first_tile[b] * TM + at, at % TM == 0, at % TM == TM - 1 || at == total[b] - 1);
-                    }
-                }
+                const int at = had + rank;
+                if (pass == 1)
+                    put(t, first_tile[b] * TM + at, at % TM == 0, at % TM == TM - 1 || at == total[b] - 1);
+                else if (hold)
+                    held[t] = b | at << kBinBits;  // its place among the warp's
                 if (rank == 0) mine[b] = had + __popc(same);
             }
             __syncwarp();
@@ -187,41 +180,55 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
             if (lane == 31) total[b] = inc;
         }
         __syncthreads();
-        // one sum over the adapters of two 32-bit counts: tiles and blocks
+        // one sum over the adapters of two counts: tiles, and above them blocks
         n = tid < p.count ? total[tid] : 0;
         const int tiles = (n + TM - 1) / TM;
-        const unsigned long long v = (unsigned long long)tiles | (unsigned long long)((n + 63) / 64) << 32;
-        unsigned long long inc = v;
+        constexpr int kTileBits = 14;
+        const uint32_t v = (uint32_t)tiles | (uint32_t)((n + 63) / 64) << kTileBits;
+        uint32_t inc = v;
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
+            const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += u;
         }
         if (lane == 31) sums[w] = inc;
         __syncthreads();
-        unsigned long long all = sums[lane];
+        uint32_t all = sums[lane];
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long u = __shfl_up_sync(0xffffffffu, all, o);
+            const uint32_t u = __shfl_up_sync(0xffffffffu, all, o);
             if (lane >= o) all += u;
         }
-        const unsigned long long below = __shfl_sync(0xffffffffu, all, max(w - 1, 0));
+        const uint32_t below = __shfl_sync(0xffffffffu, all, max(w - 1, 0));
         all = __shfl_sync(0xffffffffu, all, 31);
-        const unsigned long long before = inc - v + (w > 0 ? below : 0);
-        all_tiles = (int)all;
-        tile0 = (int)before;
-        all_blocks = (int)(all >> 32);
-        block0 = (int)(before >> 32);
+        const uint32_t before = inc - v + (w > 0 ? below : 0);
+        all_tiles = (int)(all & ((1u << kTileBits) - 1));
+        tile0 = (int)(before & ((1u << kTileBits) - 1));
+        all_blocks = (int)(all >> kTileBits);
+        block0 = (int)(before >> kTileBits);
         if (tid < p.count) first_tile[tid] = tile0;
         if (tid == 0) first_tile[p.count] = all_tiles;
         if (!hold) wait_once();
         __syncthreads();
+        if (hold) break;
     }
-    __syncthreads();
+    if (hold) {  // written after the wait
+#pragma unroll 2
+        for (int i = 0; i < rounds; ++i) {
+            const int t = t0 + 32 * i;
+            if (t >= p.tokens) break;
+            const int v = held[t], b = v & ((1 << kBinBits) - 1);
+            const int at = mine[b] + (v >> kBinBits);
+            held[t] = first_tile[b] * TM + at | (at % TM == 0 ? kFirst : 0) |
+                      (at % TM == TM - 1 || at == total[b] - 1 ? kLast : 0);
+        }
+    }
     wait_once();
     if (hold) {
 #pragma unroll 2
-        for (int t = tid; t < p.tokens; t += kPlanThreads) {
+        for (int i = 0; i < rounds; ++i) {
+            const int t = t0 + 32 * i;
+            if (t >= p.tokens) break;
             const int v = held[t];
             put(t, v & (kLast - 1), (v & kFirst) != 0, (v & kLast) != 0);
         }

@@ -32,6 +32,7 @@ FORWARD = [  # tokens, n_in, outputs, ranks of the pools, count, ids, ranks of t
     (4096, 256, [160], [128], 5, "mixed", None),
     (9000, 64, [96, 32], [8, 72], 3, "mixed", [8, 5, 3]),  # more than the plan holds in shared memory
     (20001, 32, [32], [8], 700, "some", None),
+    (1 << 20, 32, [32], [8], 1024, "some", None),  # the most tokens and adapters
 ]
 
 
