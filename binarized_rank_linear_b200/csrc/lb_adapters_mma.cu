@@ -40,11 +40,12 @@
 // the backward pass wgrad goes before expand, and expand, which needs nothing of
 // it, begins on the SMs that wgrad leaves.  Measured on the device, alone and at
 // full clocks, 8192 tokens of 5120 columns, 8 adapters of rank 64: forward to 5120
-// columns 66 us (shrink 23 us, 3.7 TB/s; finish 3; expand 33, 5.1 TB/s over the
-// base read and y written), backward from 17408 columns, 4 adapters, 198 us (shrink 73 us, 5.1
-// TB/s; wgrad 78, 4.7 TB/s; expand 33; finish 3 and 10).  333 tokens, 3 adapters
-// of rank 8, 4096 x 4096, backward 26 us: six launches of 3 to 6 us, each a chain
-// of reads that depend on one another.
+// columns 60 us (plan 4 us past the launch before; shrink 23, 3.7 TB/s; finish 3;
+// expand 30, 5.6 TB/s over the base read and y written), backward from 17408
+// columns, 4 adapters, 192 us (shrink 72 us, 5.1 TB/s; wgrad 74, 5.0 TB/s; expand
+// 30; finish 3 and 10).  333 tokens, 3 adapters of rank 8, 4096 x 4096, backward
+// 25 us: six launches of 3 to 6 us, each a chain of reads that depend on one
+// another.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
