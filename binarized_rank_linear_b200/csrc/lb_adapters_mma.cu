@@ -77,7 +77,6 @@ struct Plan {
     int *perm;     // [tiles][TM]: the token of each slot, `tokens` for none
     int *block0;   // [count + 1]: blocks of the adapters before; each has ceil(its tokens / 64)
     int *tile0;    // [count]: tiles of the adapters before
-    int *tokens;   // [count]: tokens of each adapter
 };
 
 struct PlanParams {
@@ -141,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         }
         waited = true;
     };
-    int all_tiles = 0, tile0 = 0, n = 0, block0 = 0, all_blocks = 0;
+    int all_tiles = 0, tile0 = 0, block0 = 0, all_blocks = 0;
     // pass 0 counts each warp's tokens of each bin, pass 1 gives them their slots:
     // from the places that pass 0 kept, or by counting again
 #pragma unroll 1
@@ -182,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         }
         __syncthreads();
         // one sum over the adapters of two counts: tiles, and above them blocks
-        n = tid < p.count ? total[tid] : 0;
+        const int n = tid < p.count ? total[tid] : 0;
         const int tiles = (n + TM - 1) / TM;
         constexpr int kTileBits = 14;
         const uint32_t v = (uint32_t)tiles | (uint32_t)((n + 63) / 64) << kTileBits;
@@ -236,7 +235,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     }
     if (tid < p.count) {
         p.plan.tile0[tid] = tile0;
-        p.plan.tokens[tid] = n;
         p.plan.block0[tid] = block0;
     }
     if (tid == 0) {
@@ -1626,7 +1624,7 @@ constexpr int kMostCtas = 148;  // of shrink and wgrad, whatever the device has:
 int most_tiles(int tokens, int count) { return tokens / TM + std::min(count + 1, tokens); }
 
 struct Layout {
-    size_t counts, tiles, perm, block0, tile0, tokens, v[kMaxSiblings][kParts], sums, grads, total;
+    size_t counts, tiles, perm, block0, tile0, v[kMaxSiblings][kParts], sums, grads, total;
 };
 // nv: products v per tile, of `parts` bf16 each; grad_floats: of the shared sums of wgrad
 Layout layout_of(int tokens, int count, int nv, const int *ranks, int parts, size_t grad_floats)
@@ -1644,7 +1642,6 @@ Layout layout_of(int tokens, int count, int nv, const int *ranks, int parts, siz
     L.perm = take(tiles * TM * sizeof(int));
     L.block0 = take((size_t)(count + 1) * sizeof(int));
     L.tile0 = take((size_t)count * sizeof(int));
-    L.tokens = take((size_t)count * sizeof(int));
     int widest = 0;
     for (int j = 0; j < nv; ++j) widest = std::max(widest, ranks[j]);
     L.sums = take((size_t)2 * kMostCtas * TM * (size_t)widest * sizeof(float));
@@ -1663,7 +1660,6 @@ Plan plan_at(const Layout &L, uint8_t *ws)
     p.perm = reinterpret_cast<int *>(ws + L.perm);
     p.block0 = reinterpret_cast<int *>(ws + L.block0);
     p.tile0 = reinterpret_cast<int *>(ws + L.tile0);
-    p.tokens = reinterpret_cast<int *>(ws + L.tokens);
     return p;
 }
 

@@ -20,7 +20,8 @@
 // lane where the sizes allow it, else 8.  For 8192 tokens of 40 + 8 heads of
 // 128: 35 us forward (5.7 TB/s), 61 us backward (4.9 TB/s).  (A CTA a token: 63 us
 // forward; CTAs that stay, with the next tokens in registers, 41 us forward and 86
-// us backward.)
+// us backward; 8 elements a lane on twice the threads, 67 us backward, 16 on twice
+// the threads 74.)
 // An angle is p f / pi in 64 bits, reduced to [-1, 1] before sincospi in 32: a
 // 32-bit product would be wrong in the second digit at positions near 10^6.
 // All arithmetic on values is fp32; each output is rounded to bf16 once.
