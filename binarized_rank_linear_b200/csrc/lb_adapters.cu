@@ -29,15 +29,17 @@
 // after the other; 20.5 us with the units dealt out in turn); 128 tokens, 32
 // adapters of rank 128, 4096 x 4096, 19 us, 3.6 TB/s.  What is left is the chain of each unit: partials, split, product, store.
 //
-// For up to 128 + 48 x adapters of the pool tokens, at most kAdapterSmallTokens
-// (512); beyond, and for the backward pass, the tcgen05 kernels of
-// lb_adapters_mma.cu, whose tiles hold 128 tokens of one adapter: they pay where
-// an adapter has many tokens, and how many it has is bounded by the pool.  Here
-// and there: 8 adapters of rank 16, 4096 x 4096, 256 tokens 7.8 and 17.0 us, 512
-// tokens 10.0 and 17.3; 64 of rank 16, 5120 to 7168 columns, 512 tokens 27 and 90;
-// 16 of rank 32, 5120 to 34816, 512 tokens 45 and 66; 4 of rank 64, 4096 to 11008,
-// 320 tokens 16.1 and 19.8, 512 tokens 26 and 23; 1 of rank 64, 4096 to 28672, 128
-// tokens 14.1 and 15.6, 192 tokens 23 and 19.
+// For up to 128 + 48 tokens for each adapter of the pool, at most 512, or 24 for
+// each, at most kAdapterSmallTokens (2048); beyond, and for the backward pass, the
+// tcgen05 kernels of lb_adapters_mma.cu, whose tiles hold 128 tokens of one
+// adapter: they pay where an adapter has many tokens, and how many it has is
+// bounded by the pool.  Here and there, tokens spread over the pool: 8 adapters of
+// rank 16, 4096 x 4096, 513 tokens 9.9 and 16.6 us, 1024 tokens 14.6 and 19.7; 64
+// of rank 16, 5120 to 7168 columns, 1024 tokens 34 and 82, 2048 tokens 57 and 83;
+// 32 of rank 128, 4096 x 4096, 768 tokens 38 and 39, 1024 tokens 46 and 40; 16 of
+// rank 32, 5120 to 34816, 513 tokens 44 and 55, 768 tokens 59 and 56; 4 of rank 64,
+// 4096 to 11008, 400 tokens 19.1 and 19.3, 513 tokens 24 and 21; 1 of rank 64, 4096
+// to 28672, 128 tokens 14.1 and 15.6, 200 tokens 20 and 19.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -58,10 +60,11 @@ constexpr int kWarpOuts = 32;          // outputs of an expand warp
 constexpr int kOutputs = kWarps * kWarpOuts;
 constexpr int kShrinkCtas = 3;          // CTAs an SM: what their registers leave room for
 constexpr int expand_ctas(int ks) { return ks < 2 ? 3 : 2; }
-constexpr int kRounds = kAdapterSmallTokens / kThreads;  // tokens of a thread that looks for their groups
-constexpr int kRuns = kRounds * kWarps;                  // of 32 tokens
-static_assert(kAdapterSmallTokens % kThreads == 0 && kRuns == 16 && LB_MAX_ADAPTER_RANK < 256 && LB_MAX_ADAPTERS < 32768,
-              "two words of bytes hold an adapter's tokens in each run, a byte a rank, 16 bits an adapter");
+constexpr int kMostGroups = kAdapterSmallTokens / kGroup + LB_MAX_ADAPTERS + 1;
+constexpr int kGroupBits = 12;         // of the sums over adapters: groups, and above them tokens
+static_assert(kAdapterSmallTokens / kThreads * 32 <= 256 && LB_MAX_ADAPTER_RANK < 256 && LB_MAX_ADAPTERS < 32768 &&
+                  kMostGroups < 1 << kGroupBits && kAdapterSmallTokens < 1 << 16,
+              "8 bits hold a place among a warp's tokens and a rank, 16 an adapter and a token");
 static_assert(kGroup * kRows == kThreads, "one thread for each partial of a shrink CTA");
 
 struct SmallParams {
@@ -77,25 +80,29 @@ struct SmallParams {
     int *status;
 };
 
-// The groups of a call: each adapter's tokens in order, cut every kGroup; an
-// adapter's groups stand where its first token does.  A thread takes a token, or
-// two: those of a run of 32 with the same adapter find each other (match), and a
-// table by adapter holds their number in each run.
+// The groups of a call: each adapter's tokens in order, cut every kGroup, adapter
+// by adapter (those without one first).
 struct Groups {
-    int16_t ids[kAdapterSmallTokens];            // of each group (-1: no adapter)
-    uint8_t size[kAdapterSmallTokens];
-    uint8_t rank[kMaxSiblings][kAdapterSmallTokens];
-    int starts[kRuns];                           // groups that begin in each run
-    uint16_t first[LB_MAX_ADAPTERS + 1];         // by id + 1: its first group
-    union {                                      // the table is read before the first token is written
-        ulonglong2 in_run[LB_MAX_ADAPTERS + 1];  // by id + 1: tokens in each run, a byte each
-        uint16_t tok[kAdapterSmallTokens][kGroup];
-    };
+    uint16_t order[kAdapterSmallTokens];  // the tokens
+    uint16_t start[kMostGroups];          // of each group in `order`
+    int16_t ids[kMostGroups];             // -1: no adapter
+    uint8_t size[kMostGroups];
+    uint8_t rank[kMaxSiblings][kMostGroups];
 };
-__device__ __forceinline__ int find_groups(const SmallParams &p, Groups &g)
+// What finding them takes besides; a bin is an adapter's id + 1.
+struct Finding {
+    uint16_t count[LB_MAX_ADAPTERS + 1][kWarps];  // a warp's tokens of a bin, then where they begin in `order`
+    uint16_t order0[LB_MAX_ADAPTERS + 2];         // of each bin
+    uint16_t group0[LB_MAX_ADAPTERS + 1];
+    uint16_t bin[kAdapterSmallTokens];            // of each token
+    uint8_t place[kAdapterSmallTokens];           // among its warp's tokens of the bin
+    uint32_t sums[kWarps];
+};
+// Each warp takes a run of tokens, 32 at a time: those of one bin find each other
+// (match), the table has how many came before them.
+__device__ __forceinline__ int find_groups(const SmallParams &p, Groups &g, Finding &f)
 {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int rounds = p.tokens > kThreads ? kRounds : 1;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, bins = p.count + 1;
     auto id_of = [&](int t) {
         int id = __ldg(p.ids + t);
         if (id >= p.count) {
@@ -109,82 +116,94 @@ __device__ __forceinline__ int find_groups(const SmallParams &p, Groups &g)
     };
     if (p.tokens == 1) {  // every thread has its id
         const int id = id_of(0);
-        if (threadIdx.x < p.nproj) g.rank[threadIdx.x][0] = rank_of(p.proj[threadIdx.x], id);
-        if (threadIdx.x == 0) {
+        if (tid < p.nproj) g.rank[tid][0] = rank_of(p.proj[tid], id);
+        if (tid == 0) {
+            g.order[0] = g.start[0] = 0;
             g.ids[0] = (int16_t)id;
             g.size[0] = 1;
-            g.tok[0][0] = 0;
         }
         __syncthreads();
         return 1;
     }
-    int mine[kRounds], before[kRounds], all[kRounds], led[kRounds];
-    uint32_t peers[kRounds];
-    const uint32_t lower = (1u << lane) - 1u;
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        const int t = i * kThreads + threadIdx.x;
-        mine[i] = t < p.tokens ? id_of(t) : -2;
-        if (i < rounds) peers[i] = __match_any_sync(0xffffffffu, mine[i]);
-        if (mine[i] > -2) g.in_run[mine[i] + 1] = make_ulonglong2(0, 0);
-    }
+    const int rounds = (p.tokens + kThreads - 1) / kThreads, t0 = w * rounds * 32 + lane;
+#pragma unroll 1
+    for (int b = tid; b < bins; b += kThreads) *reinterpret_cast<uint4 *>(f.count[b]) = make_uint4(0, 0, 0, 0);
+    int bin = t0 < p.tokens ? id_of(t0) + 1 : -1;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i)
-        if (mine[i] > -2 && (peers[i] & lower) == 0)
-            reinterpret_cast<uint8_t *>(&g.in_run[mine[i] + 1])[i * kWarps + w] = (uint8_t)__popc(peers[i]);
-    __syncthreads();
-    int begin[kRounds];
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        before[i] = all[i] = 0;  // tokens of the same adapter: earlier ones; all
-        if (mine[i] > -2) {
-            const ulonglong2 c = g.in_run[mine[i] + 1];
-            before[i] = __popc(peers[i] & lower);
-#pragma unroll
-            for (int k = 0; k < kRuns; ++k) {
-                const int n = (int)((k < 8 ? c.x : c.y) >> (8 * (k & 7))) & 0xff;
-                before[i] += k < i * kWarps + w ? n : 0;
-                all[i] += n;
-            }
+#pragma unroll 1
+    for (int i = 0; i < rounds; ++i) {
+        const int t = t0 + 32 * i, next = t + 32 < p.tokens && i + 1 < rounds ? id_of(t + 32) + 1 : -1;
+        const uint32_t peers = __match_any_sync(0xffffffffu, bin), earlier = peers & ((1u << lane) - 1u);
+        const int had = bin >= 0 ? f.count[bin][w] : 0;
+        __syncwarp();
+        if (bin >= 0) {
+            f.bin[t] = (uint16_t)bin;
+            f.place[t] = (uint8_t)(had + __popc(earlier));
+            if (earlier == 0) f.count[bin][w] = (uint16_t)(had + __popc(peers));
         }
-        led[i] = mine[i] > -2 && before[i] == 0 ? (all[i] + kGroup - 1) / kGroup : 0;
-        begin[i] = led[i];
-        if (i < rounds) {
+        __syncwarp();
+        bin = next;
+    }
+    __syncthreads();
+    // a thread's bins, one after the other: their groups and tokens, summed over all
+    const int per = (bins + kThreads - 1) / kThreads, b0 = min(tid * per, bins), b1 = min(b0 + per, bins);
+    auto both = [&](int b) {
+        const uint4 c = *reinterpret_cast<const uint4 *>(f.count[b]);
+        const uint32_t h = (c.x & 0xffffu) + (c.x >> 16) + (c.y & 0xffffu) + (c.y >> 16) + (c.z & 0xffffu) + (c.z >> 16) +
+                           (c.w & 0xffffu) + (c.w >> 16);
+        return (h + kGroup - 1) / kGroup | h << kGroupBits;
+    };
+    uint32_t mine = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) mine += both(b);
+    uint32_t at = mine;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int k = __shfl_up_sync(0xffffffffu, begin[i], o);
-                begin[i] += lane >= o ? k : 0;
-            }
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t k = __shfl_up_sync(0xffffffffu, at, o);
+        at += lane >= o ? k : 0;
+    }
+    if (lane == 31) f.sums[w] = at;
+    __syncthreads();
+    at -= mine;
+    uint32_t all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        at += i < w ? f.sums[i] : 0;
+        all += f.sums[i];
+    }
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        const uint32_t n = both(b);
+        f.group0[b] = (uint16_t)(at & ((1u << kGroupBits) - 1));
+        uint32_t first = at >> kGroupBits;
+        f.order0[b] = (uint16_t)first;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            const uint32_t c = f.count[b][i];
+            f.count[b][i] = (uint16_t)first;
+            first += c;
         }
-        if (lane == 31) g.starts[i * kWarps + w] = begin[i];
-        begin[i] -= led[i];
+        at += n;
     }
+    if (tid == 0) f.order0[bins] = (uint16_t)p.tokens;
     __syncthreads();
-    int n = 0;
-#pragma unroll
-    for (int k = 0; k < kRuns; ++k) {
-#pragma unroll
-        for (int i = 0; i < kRounds; ++i) begin[i] += k < i * kWarps + w ? g.starts[k] : 0;
-        n += g.starts[k];
-    }
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i)
-        if (led[i] > 0) g.first[mine[i] + 1] = (uint16_t)begin[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        if (mine[i] > -2) {
-            const int k = g.first[mine[i] + 1] + before[i] / kGroup;
-            g.tok[k][before[i] % kGroup] = (uint16_t)(i * kThreads + threadIdx.x);
-            if (before[i] % kGroup == 0) {
-                g.ids[k] = (int16_t)mine[i];
-                g.size[k] = (uint8_t)min(kGroup, all[i] - before[i]);
-            }
+#pragma unroll 1
+    for (int i = 0; i < rounds; ++i) {
+        const int t = t0 + 32 * i;
+        if (t >= p.tokens) break;
+        const int b = f.bin[t], to = f.count[b][w] + f.place[t], before = to - f.order0[b];
+        g.order[to] = (uint16_t)t;
+        if (before % kGroup == 0) {
+            const int k = f.group0[b] + before / kGroup;
+            g.start[k] = (uint16_t)to;
+            g.ids[k] = (int16_t)(b - 1);
+            g.size[k] = (uint8_t)min(kGroup, f.order0[b + 1] - to);
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n * p.nproj; i += kThreads) {
+    const int n = (int)(all & ((1u << kGroupBits) - 1));
+#pragma unroll 1
+    for (int i = tid; i < n * p.nproj; i += kThreads) {
         const int j = i / n, k = i - j * n;
         g.rank[j][k] = rank_of(p.proj[j], g.ids[k]);
     }
@@ -211,9 +230,13 @@ __device__ __forceinline__ void mma32(float (&d)[4], const uint4 &lo, const uint
 // Units (group, kRows rows of a projection's A, slice), one after the other
 __global__ void __launch_bounds__(kThreads, kShrinkCtas) small_shrink_kernel(const __grid_constant__ SmallParams p)
 {
-    __shared__ alignas(16) Groups grp;
-    __shared__ float red[2][kWarps][kGroup][kRows + 2];
-    const int groups = find_groups(p, grp);
+    __shared__ Groups grp;
+    __shared__ union {
+        alignas(16) Finding f;
+        float red[2][kWarps][kGroup][kRows + 2];
+    } scratch;
+    auto &red = scratch.red;
+    const int groups = find_groups(p, grp, scratch.f);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int kw = warp * kWarpCols + 8 * (lane & 3);
     const int t0 = lane >> 2, t1 = t0 + 8;
@@ -253,8 +276,9 @@ __global__ void __launch_bounds__(kThreads, kShrinkCtas) small_shrink_kernel(con
     pdl_launch_dependents();
     for (int turn = 0; unit < units; turn ^= 1) {
         const int n = grp.size[g], k0 = slice * kSlice + kw;
-        const uint16_t *x0 = p.x + (int64_t)grp.tok[g][t0 < n ? t0 : 0] * p.ldx + k0;
-        const uint16_t *x1 = p.x + (int64_t)grp.tok[g][t1 < n ? t1 : 0] * p.ldx + k0;
+        const uint16_t *tok = grp.order + grp.start[g];
+        const uint16_t *x0 = p.x + (int64_t)tok[t0 < n ? t0 : 0] * p.ldx + k0;
+        const uint16_t *x1 = p.x + (int64_t)tok[t1 < n ? t1 : 0] * p.ldx + k0;
         uint4 lo[kSteps], hi[kSteps];
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
@@ -271,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, kShrinkCtas) small_shrink_kernel(con
         // where the partial of this thread goes: token threadIdx.x / kRows, row r0 + threadIdx.x % kRows
         const int t = threadIdx.x / kRows, r = threadIdx.x % kRows;
         float *to = t < n && r0 + r < rank
-                        ? p.part[j] + ((int64_t)slice * p.tokens + grp.tok[g][t]) * p.proj[j].rank + r0 + r
+                        ? p.part[j] + ((int64_t)slice * p.tokens + tok[t]) * p.proj[j].rank + r0 + r
                         : nullptr;
         unit = find(unit + gridDim.x);
         if (unit < units) load();
@@ -296,12 +320,16 @@ __global__ void __launch_bounds__(kThreads, kShrinkCtas) small_shrink_kernel(con
 template <int KS>
 __global__ void __launch_bounds__(kThreads, expand_ctas(KS)) small_expand_kernel(const __grid_constant__ SmallParams p)
 {
-    __shared__ alignas(16) Groups grp;
+    __shared__ Groups grp;
     // s_i v in three bf16 parts, 24 bits: nothing of the fp32 value is lost
     constexpr int kPitch = 32 * KS + 8;  // 16-byte reads of 8 rows fall into 8 different bank groups
-    __shared__ alignas(16) uint16_t vs[2][3][kGroup][kPitch];
+    __shared__ union {
+        alignas(16) Finding f;
+        alignas(16) uint16_t vs[2][3][kGroup][kPitch];
+    } scratch;
+    auto &vs = scratch.vs;
     constexpr int kAtOnce = 8;  // partials a thread asks for at once
-    const int groups = find_groups(p, grp);
+    const int groups = find_groups(p, grp, scratch.f);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane >> 2, q = lane & 3;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     const int chunks = p.chunk0[p.nproj], units = groups * chunks;
@@ -345,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, expand_ctas(KS)) small_expand_kernel
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             y[h] = o < P.n_out && row + 8 * h < grp.size[at.g]
-                       ? *reinterpret_cast<const uint4 *>(P.base + (int64_t)grp.tok[at.g][row + 8 * h] * P.ldbase + o)
+                       ? *reinterpret_cast<const uint4 *>(P.base + (int64_t)grp.order[grp.start[at.g] + row + 8 * h] * P.ldbase + o)
                        : zero;
     };
     int unit = find(begin);
@@ -358,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, expand_ctas(KS)) small_expand_kernel
         const Unit u = at;
         const AdapterProj &P = p.proj[u.j];
         const int n = grp.size[u.g], o = u.out0 + 8 * q;
+        const uint16_t *tok = grp.order + grp.start[u.g];
         if (u.rank > 0 && (u.g != vg || u.j != vj)) {
             turn ^= 1;  // some threads may still read the other half
             vg = u.g;
@@ -367,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, expand_ctas(KS)) small_expand_kernel
                 const int t = i / (16 * KS), r = i % (16 * KS) * 2;  // and r + 1
                 float2 v = make_float2(0.0f, 0.0f);
                 if (r < u.rank) {
-                    const float *part = p.part[u.j] + (int64_t)grp.tok[u.g][t] * P.rank + r;
+                    const float *part = p.part[u.j] + (int64_t)tok[t] * P.rank + r;
                     for (int s0 = 0; s0 < p.slices; s0 += kAtOnce) {
                         float2 e[kAtOnce];
 #pragma unroll
@@ -414,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, expand_ctas(KS)) small_expand_kernel
                 y[h] = make_uint4(e[0], e[1], e[2], e[3]);
             }
             if (o < P.n_out && row + 8 * h < n)
-                *reinterpret_cast<uint4 *>(P.y + (int64_t)grp.tok[u.g][row + 8 * h] * P.ldy + o) = y[h];
+                *reinterpret_cast<uint4 *>(P.y + (int64_t)tok[row + 8 * h] * P.ldy + o) = y[h];
         }
         if (unit < end) load_base();
     }
@@ -485,7 +514,10 @@ size_t small_workspace(int M, int n_in, int nproj, const int *ranks)
 }  // namespace
 
 // Whether a call runs here: see the top of this file.
-static bool small_batch(int tokens, int count) { return tokens <= std::min(kAdapterSmallTokens, 128 + 48 * count); }
+static bool small_batch(int tokens, int count)
+{
+    return tokens <= std::max(std::min(512, 128 + 48 * count), std::min(kAdapterSmallTokens, 24 * count));
+}
 
 size_t adapters_workspace_bytes(int tokens, int n_in, int count, int nproj, const int *ranks)
 {

@@ -366,9 +366,8 @@ LB_API lb_status lb_linear_backward(const uint16_t *x, const uint16_t *dy, int64
  *                  in another way.  The outputs must not overlap each other,
  *                  x or the workspace.
  * Numerics: products accumulate in fp32; A_i x is kept in fp32, or in larger
- *   batches (always beyond LB_ADAPTERS_SMALL_TOKENS tokens, and from 177 on
- *   where few adapters are in the pool) as the sum of two bf16 (16 bits and
- *   the sign); base is added in fp32 and y rounded to bf16 once.  Every sum
+ *   batches (always beyond LB_ADAPTERS_SMALL_TOKENS tokens, with few adapters
+ *   in the pool from 177 on) as the sum of two bf16 (16 bits and the sign); base is added in fp32 and y rounded to bf16 once.  Every sum
  *   runs in a fixed order: results are deterministic.  A token's result does
  *   not depend on the other tokens' values (an infinity or NaN stays in its
  *   row).
@@ -396,7 +395,7 @@ LB_API lb_status lb_linear_backward(const uint16_t *x, const uint16_t *dy, int64
  * Errors as lb_linear_forward. */
 #define LB_MAX_ADAPTERS 1024
 #define LB_MAX_ADAPTER_RANK 128
-#define LB_ADAPTERS_SMALL_TOKENS 512
+#define LB_ADAPTERS_SMALL_TOKENS 2048
 typedef struct {
     const uint16_t *a;
     const uint16_t *b;

@@ -27,6 +27,12 @@ FORWARD = [  # tokens, n_in, outputs, ranks of the pools, count, ids, ranks of t
     (512, 64, [288], [128], 64, "runs", None),
     (512, 1056, [32], [8], 8, "one", None),
     (513, 1056, [32], [8], 8, "one", None),
+    (768, 96, [64, 32], [16, 128], 32, "mixed", [16] * 16 + [3] * 16),
+    (769, 96, [64, 32], [16, 128], 32, "mixed", [16] * 16 + [3] * 16),
+    (2047, 64, [288], [24], 1024, "some", None),
+    (2048, 1056, [32], [8], 86, "one", None),           # a warp's tokens all of one adapter
+    (2048, 64, [32, 64, 96, 32], [8, 16, 72, 128], 900, "runs", None),
+    (2049, 64, [32], [8], 1000, "mixed", None),
     (385, 544, [160, 96], [128, 24], 3, "none", None),
     (600, 128, [96], [16], 4, "mixed", [0, 16, 0, 3]),
     (4096, 256, [160], [128], 5, "mixed", None),

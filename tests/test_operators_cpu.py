@@ -203,7 +203,6 @@ def test_heads_refuse_rows_too_far_apart(L, kw):
 def test_workspace_follows_the_kernels(L):
     """Small batches need partial sums alone, more tokens than the pool allows
     for them the plan and tiles too; the query knows both sides of the border."""
-    for count in (1, 6, 1000):
-        border = min(512, 128 + 48 * count)
+    for count, border in ((1, 176), (6, 416), (16, 512), (64, 1536), (1000, 2048)):
         sizes = [lb.adapters_workspace_bytes(t, 64, count, (16,)) for t in (1, border, border + 1)]
         assert 0 < sizes[0] <= sizes[1] < sizes[2]
