@@ -636,7 +636,8 @@ class AdapterPool:
 
     def as_c(self) -> LbAdapters:
         """The lb_adapters struct of this pool, built once (the fields are
-        frozen and a tensor's storage does not move)."""
+        frozen and a tensor's storage does not move).  ``_c`` is set last: a
+        thread that finds it finds the rest too."""
         c = self.__dict__.get("_c")
         if c is None:
             torch = _torch()
@@ -658,11 +659,11 @@ class AdapterPool:
             c = LbAdapters(self.a.data_ptr(), self.b.data_ptr(),
                            self.scale.data_ptr() if self.scale is not None else None,
                            self.ranks.data_ptr() if self.ranks is not None else None, count, rank)
-            object.__setattr__(self, "_c", c)
             object.__setattr__(self, "_p", ctypes.pointer(c))
             object.__setattr__(self, "n_in", n_in)
             object.__setattr__(self, "n_out", self.b.shape[1])
             object.__setattr__(self, "device", self.a.device)
+            object.__setattr__(self, "_c", c)
         return c
 
 
