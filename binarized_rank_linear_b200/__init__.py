@@ -9,6 +9,10 @@ this module only marshals arguments through the C ABI declared in
 CPU fallback: if ``liblb.so`` is missing or the device is not an sm_100 part,
 the calls raise.
 
+A call runs on the current stream, or on the ``stream`` it is given, which then
+has to be ordered behind whatever wrote its inputs; memory that the call makes
+for itself comes from that stream.
+
 Build the library with ``python -m binarized_rank_linear_b200.build``.
 """
 from __future__ import annotations
@@ -260,18 +264,41 @@ def _require_workspace(ws) -> None:
         raise ValueError("workspace must be a contiguous device tensor")
 
 
+# Memory that a call makes for itself.  On a stream of the caller's it comes from
+# that stream's part of torch's pool: a block of the current stream's may still be
+# read by kernels queued there, which the call's stream knows nothing of.
+
+def _new(shape, dtype, device, stream):
+    """A dense tensor that a call on `stream` writes and returns.  It may be read
+    on the current stream afterwards, so its memory waits for that one too."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _new_workspace(like, need: int, stream):
+    """Scratch of `need` bytes on the device of the tensor `like`, of two-byte elements."""
+    if stream is None:
+        return like.new_empty(max(need, 16) + 1 >> 1)
+    with _torch().cuda.stream(stream):
+        return like.new_empty(max(need, 16) + 1 >> 1)
+
+
 def pack_signs(src, kind: str, ld_words: int | None = None, stream=None):
     """Pack a device factor (f32 / f16 / bf16 / int8, 2-D, unit column stride)
     with ``lb_pack_signs``.  ``kind`` is ``"U"`` (src = U [n_out, r]) or
     ``"V"`` (src = V [n_in, r], packed as V^T).  Returns an int32 tensor of
     packed words (bit patterns)."""
-    torch = _torch()
     if src.dim() != 2 or src.stride(1) != 1 or not src.is_cuda:
         raise ValueError("src must be a 2-D CUDA tensor with unit column stride")
     rows, cols = src.shape
     packed_rows, packed_cols = (rows, cols) if kind == "U" else (cols, rows)
     ld = packed_ld_words(packed_cols) if ld_words is None else int(ld_words)
-    dst = torch.empty((packed_rows, ld), dtype=torch.int32, device=src.device)
+    dst = _new((packed_rows, ld), _torch().int32, src.device, stream)
     code = LB_FACTOR_U if kind == "U" else LB_FACTOR_V
     _check(lib().lb_pack_signs(src.data_ptr(), _dtype_code(src), code, rows, cols, src.stride(0),
                                dst.data_ptr(), ld, _stream_handle(stream)), "lb_pack_signs")
@@ -331,11 +358,11 @@ def linear_forward(x, main: PackedPath, residual: PackedPath | None = None, y=No
     tokens, n_in = x.shape
     n_out = main.h.shape[0]
     if y is None:
-        y = torch.empty((tokens, n_out), dtype=torch.bfloat16, device=x.device)
+        y = _new((tokens, n_out), torch.bfloat16, x.device, stream)
     _require(y, "y", torch.bfloat16)
     if workspace is None:  # a caller's workspace size is checked by the library itself
         need = forward_workspace_bytes(tokens, n_in, n_out, main.rank, residual.rank if residual else 0)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        workspace = _new_workspace(x, need, stream)
     _require_workspace(workspace)
     cm = main.as_c()
     cr = residual.as_c() if residual is not None else None
@@ -385,7 +412,7 @@ def linear_forward_siblings(x, layers, ys=None, workspace=None, stream=None, ada
     _require(x, "x", torch.bfloat16)
     tokens, n_in = x.shape
     if ys is None:
-        ys = [torch.empty((tokens, main.h.shape[0]), dtype=torch.bfloat16, device=x.device) for main, _ in layers]
+        ys = [_new((tokens, main.h.shape[0]), torch.bfloat16, x.device, stream) for main, _ in layers]
     for j, y in enumerate(ys):
         _require(y, f"ys[{j}]", torch.bfloat16)
     if adapters is not None and (len(adapters) != len(layers) or ids is None):
@@ -395,7 +422,7 @@ def linear_forward_siblings(x, layers, ys=None, workspace=None, stream=None, ada
     arr, _keep = _projections(layers, ys)
     need = int(lib().lb_siblings_workspace_bytes(tokens, n_in, len(layers), arr))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        workspace = _new_workspace(x, need, stream)
     _require_workspace(workspace)
     _check(lib().lb_linear_forward_siblings(
         x.data_ptr(), tokens, n_in, x.stride(0), len(layers), arr, workspace.data_ptr(),
@@ -448,7 +475,7 @@ def latent_forward(x, main: PackedPath, residual: PackedPath | None = None, z=No
     tokens, n_in = x.shape
     R = main.rank + (residual.rank if residual is not None else 0)
     if z is None:
-        z = torch.empty((tokens, R), dtype=torch.float16, device=x.device)
+        z = _new((tokens, R), torch.float16, x.device, stream)
     _require(z, "z", torch.float16)
     cm = main.as_c()
     cr = residual.as_c() if residual is not None else None
@@ -466,7 +493,7 @@ def expand_forward(z, main: PackedPath, residual: PackedPath | None = None, y=No
     tokens = z.shape[0]
     n_out = main.h.shape[0]
     if y is None:
-        y = torch.empty((tokens, n_out), dtype=torch.bfloat16, device=z.device)
+        y = _new((tokens, n_out), torch.bfloat16, z.device, stream)
     _require(y, "y", torch.bfloat16)
     cm = main.as_c()
     cr = residual.as_c() if residual is not None else None
@@ -487,7 +514,7 @@ def linear_forward_fixed_scratch(x, main: PackedPath, residual: PackedPath | Non
     tokens, n_in = x.shape
     n_out = main.h.shape[0]
     if y is None:
-        y = torch.empty((tokens, n_out), dtype=torch.bfloat16, device=x.device)
+        y = _new((tokens, n_out), torch.bfloat16, x.device, stream)
     _require(y, "y", torch.bfloat16)
     cm = main.as_c()
     cr = residual.as_c() if residual is not None else None
@@ -522,16 +549,15 @@ def linear_backward(x, dy, main: PackedPath, residual: PackedPath | None = None,
         raise ValueError(f"dy must be [{tokens}, {n_out}], got {tuple(dy.shape)}")
     npaths = 2 if residual is not None else 1
     if dx is None and want_dx:
-        dx = torch.empty((tokens, n_in), dtype=torch.bfloat16, device=x.device)
+        dx = _new((tokens, n_in), torch.bfloat16, x.device, stream)
     if dx is not None:
         _require(dx, "dx", torch.bfloat16)
-    dh = torch.empty((npaths, n_out), dtype=torch.float32, device=x.device)
-    dg = torch.empty((npaths, n_in), dtype=torch.float32, device=x.device)
-    dl = torch.empty((main.rank + (residual.rank if residual is not None else 0),), dtype=torch.float32,
-                     device=x.device)
+    dh = _new((npaths, n_out), torch.float32, x.device, stream)
+    dg = _new((npaths, n_in), torch.float32, x.device, stream)
+    dl = _new((main.rank + (residual.rank if residual is not None else 0),), torch.float32, x.device, stream)
     if workspace is None:
         need = backward_workspace_bytes(tokens, n_in, n_out, main.rank, residual.rank if residual else 0)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        workspace = _new_workspace(x, need, stream)
     _require_workspace(workspace)
     cm = main.as_c()
     cr = residual.as_c() if residual is not None else None
@@ -592,17 +618,16 @@ def _stream_of(stream, device):
     return _stream_handle(stream)
 
 
-def _held(t, stream):
-    """Keeps memory that torch gave on the current stream from being handed out
-    again before `stream` is done with it."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 # A decode step calls these for microseconds of work on the device, so the calls
 # check all of a tensor in one expression and only go through the checks that
 # name the fault when it fails, and allocate by the cheapest of torch's calls.
+
+def _new_dense(shape: tuple, strides: tuple, dtype, device, stream):
+    """_new, given the strides of a dense tensor too."""
+    if stream is None:
+        return _torch().empty_strided(shape, strides, dtype=dtype, device=device)
+    return _new(shape, dtype, device, stream)
+
 
 def _rows_ld(t, name: str, rows: int, cols: int, dtype, device) -> int:
     """_require_rows, at once where nothing is wrong."""
@@ -617,11 +642,6 @@ def _vector_ptr(t, name: str, n: int, dtype, device) -> int:
     if t.dtype is not dtype or t.shape != (n,) or t.device != device or not t.is_contiguous():
         _require_vector(t, name, n, dtype, device)
     return t.data_ptr()
-
-
-def _new_workspace(like, need: int, stream):
-    """Scratch of `need` bytes on the device of the bf16 tensor `like`."""
-    return _held(like.new_empty(max(need, 16) + 1 >> 1), stream)
 
 
 @dataclass(frozen=True)
@@ -712,9 +732,7 @@ def adapters_forward(x, ids, pools, bases=None, ys=None, workspace=None, stream=
             e.ldbase = _rows_ld(base, "bases", tokens, n_out, bf16, device)
             e.base = base.data_ptr()
         if ys is None:
-            y = torch.empty_strided((tokens, n_out), (n_out, 1), dtype=bf16, device=device)
-            if stream is not None:
-                y.record_stream(stream)
+            y = _new_dense((tokens, n_out), (n_out, 1), bf16, device, stream)
             made.append(y)
             e.ldy = n_out
         else:
@@ -758,7 +776,7 @@ def adapters_backward(x, dy, ids, pool: AdapterPool, dx_base=None, dx=None, want
     if want_dx and dx is None:
         if dx_base is None:
             raise ValueError("give dx_base, or dx to update in place, or want_dx=False")
-        dx = _held(torch.empty_strided((tokens, n_in), (n_in, 1), dtype=bf16, device=device), stream)
+        dx = _new_dense((tokens, n_in), (n_in, 1), bf16, device, stream)
     if not want_dx:
         dx = None
     lddx = _rows_ld(dx, "dx", tokens, n_in, bf16, device) if dx is not None else n_in
@@ -769,9 +787,9 @@ def adapters_backward(x, dy, ids, pool: AdapterPool, dx_base=None, dx=None, want
         if t is not None and (t.dtype != f32 or t.shape != shape or not t.is_contiguous() or t.device != device):
             raise ValueError(f"{name} must be a contiguous {shape} float32 tensor on {device}")
     if da is None:
-        da = _held(torch.empty_strided((count, rank, n_in), (rank * n_in, n_in, 1), dtype=f32, device=device), stream)
+        da = _new_dense((count, rank, n_in), (rank * n_in, n_in, 1), f32, device, stream)
     if db is None:
-        db = _held(torch.empty_strided((count, n_out, rank), (n_out * rank, rank, 1), dtype=f32, device=device), stream)
+        db = _new_dense((count, n_out, rank), (n_out * rank, rank, 1), f32, device, stream)
     if workspace is None:
         need = adapters_backward_workspace_bytes(tokens, n_in, n_out, count, rank)
         workspace = _new_workspace(x, need, stream)
@@ -855,7 +873,7 @@ def heads_norm_rotate(tensors, positions, rotation: HeadRotation, weights=None, 
         e.ld_in = _rows_ld(t, "tensors", tokens, cols, bf16, device)
         e.in_ = t.data_ptr()
         if outs is None:
-            o = _held(torch.empty_strided((tokens, cols), (cols, 1), dtype=bf16, device=device), stream)
+            o = _new_dense((tokens, cols), (cols, 1), bf16, device, stream)
             made.append(o)
             e.ld_out = cols
         else:
@@ -899,7 +917,7 @@ def heads_norm_rotate_backward(tensors, douts, positions, rotation: HeadRotation
         e.ld_dout = _rows_ld(douts[j], "douts", tokens, cols, bf16, device)
         e.dout = douts[j].data_ptr()
         if dins is None:
-            din = _held(torch.empty_strided((tokens, cols), (cols, 1), dtype=bf16, device=device), stream)
+            din = _new_dense((tokens, cols), (cols, 1), bf16, device, stream)
             e.ld_din = cols
         else:
             din = dins[j]
@@ -909,7 +927,7 @@ def heads_norm_rotate_backward(tensors, douts, positions, rotation: HeadRotation
         if weights is not None and weights[j] is not None:
             e.weight = _vector_ptr(weights[j], "weights", d, bf16, device)
             if want_dweight:
-                dw = _held(torch.empty_strided((d,), (1,), dtype=torch.float32, device=device), stream)
+                dw = _new_dense((d,), (1,), torch.float32, device, stream)
                 e.dweight = dw.data_ptr()
                 out[j]["dweight"] = dw
                 sums = True
@@ -980,8 +998,9 @@ class LittleBitLinear:
     def __call__(self, x, y=None, stream=None, adapters: AdapterPool | None = None, ids=None):
         if adapters is not None and ids is None:
             raise ValueError("adapters need ids, each token's adapter")
-        y = linear_forward(x, self.main, self.residual, y=y,
-                           workspace=self.workspace(x.shape[0], x.device), stream=stream)
+        # the kept workspace belongs to the current stream
+        y = linear_forward(x, self.main, self.residual, y=y, stream=stream,
+                           workspace=self.workspace(x.shape[0], x.device) if stream is None else None)
         if adapters is not None:
             adapters_forward(x, ids, [adapters], ys=[y], stream=stream)
         return y

@@ -10,7 +10,7 @@ import torch
 
 import binarized_rank_linear_b200 as lb
 from binarized_rank_linear_b200 import build as lb_build
-from tests.binding_stub import World
+from tests.binding_stub import Stream, World
 
 
 @pytest.fixture
@@ -65,3 +65,54 @@ def test_fresh_pools_in_three_threads(world):
     finally:
         sys.setswitchinterval(interval)
     assert not faults, faults[0]
+
+
+def calls_of(world, stream, kept=None):
+    """Every call that makes memory for itself, and what it returned."""
+    x, dy, ids = world.tensor(5, 64), world.tensor(5, 96), world.tensor(5, dtype=torch.int32)
+    path, pool = world.path(64, 96, 32), world.pool(3, 8, 64, 96)
+    rot = lb.HeadRotation(32, world.tensor(16, dtype=torch.float32))
+    w = world.tensor(32)
+    z = world.tensor(5, 32, dtype=torch.float16)
+    layer = lb.LittleBitLinear(path)
+    if kept is not None:
+        layer._ws = kept
+    calls = [
+        lambda: [lb.linear_forward(x, path, stream=stream)],
+        lambda: lb.linear_forward_siblings(x, [(path, None)] * 2, adapters=[pool, None], ids=ids, rotation=rot, positions=ids,
+                                           rotate={0: w}, stream=stream),
+        lambda: [lb.latent_forward(x, path, stream=stream)],
+        lambda: [lb.expand_forward(z, path, stream=stream)],
+        lambda: [lb.linear_forward_fixed_scratch(x, path, stream=stream)],
+        lambda: [v for v in lb.linear_backward(x, dy, path, adapters=pool, ids=ids, stream=stream).values()],
+        lambda: lb.adapters_forward(x, ids, [pool], bases=[dy], stream=stream),
+        lambda: [*lb.adapters_backward(x, dy, ids, pool, dx_base=x, stream=stream).values()],
+        lambda: lb.heads_norm_rotate([dy], ids, rot, weights=[w], stream=stream),
+        lambda: [*lb.heads_norm_rotate_backward([dy], [dy], ids, rot, weights=[w], stream=stream)[0].values()],
+        lambda: [layer(x, adapters=pool, ids=ids, stream=stream)],
+        lambda: [lb.pack_signs(world.tensor(96, 32), "U", stream=stream)],
+    ]
+    for call in calls:
+        world.calls.clear()
+        world.allocations.clear()
+        yield call(), world.allocations, world.calls
+
+
+def test_memory_for_a_stream_comes_from_it(world):
+    """A block of the current stream's may still be read by kernels queued
+    there; the call's stream is not ordered behind them."""
+    side = Stream(77)
+    scratch = world.tensor(1 << 16, dtype=torch.uint8)  # a layer's, from calls on the current stream
+    kept = scratch.address
+    for returned, made, calls in calls_of(world, side, scratch):
+        assert made and calls
+        for t in made:
+            assert t.stream is side
+        for t in returned:  # read on the current stream after the caller has waited there
+            assert t in made and t.recorded == [world.default]
+        assert not any(kept in args for _, args in calls)
+
+
+def test_memory_without_a_stream_comes_from_the_current_one(world):
+    for returned, made, _ in calls_of(world, None):
+        assert all(t.stream is world.default and not t.recorded for t in made)
