@@ -101,6 +101,7 @@ class LbHeadsGrad(ctypes.Structure):
 MAX_SIBLINGS = 4
 MAX_ADAPTERS = 1024
 MAX_ADAPTER_RANK = 128
+MAX_HEADS = 4096  # of a heads call's tensors together
 ROTATE_HALVES, ROTATE_PAIRS = 0, 1
 
 
@@ -419,6 +420,16 @@ def linear_forward_siblings(x, layers, ys=None, workspace=None, stream=None, ada
         raise ValueError("adapters must name a pool or None for each layer, and ids each token's adapter")
     if rotation is not None and (positions is None or not rotate or not all(0 <= j < len(layers) for j in rotate)):
         raise ValueError("rotation needs positions and, in rotate, the layers whose outputs are rotated")
+    # what follows the projections is checked before they are launched
+    some = [j for j, pool in enumerate(adapters or ()) if pool is not None]
+    if some:
+        beside = _adapters_call(x, ids, [adapters[j] for j in some], None, [ys[j] for j in some], stream)
+        _adapters_checked(lib().lb_adapters_forward, "lb_adapters_forward", tokens, beside[0])
+    if rotation is not None:
+        which = sorted(rotate)
+        turned = [ys[j] for j in which]
+        heads = _heads_forward_call(turned, positions, rotation, [rotate[j] for j in which], turned, stream)
+        _heads_checked(heads[0])
     arr, _keep = _projections(layers, ys)
     need = int(lib().lb_siblings_workspace_bytes(tokens, n_in, len(layers), arr))
     if workspace is None:
@@ -427,14 +438,10 @@ def linear_forward_siblings(x, layers, ys=None, workspace=None, stream=None, ada
     _check(lib().lb_linear_forward_siblings(
         x.data_ptr(), tokens, n_in, x.stride(0), len(layers), arr, workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream_handle(stream)), "lb_linear_forward_siblings")
-    if adapters is not None:
-        some = [j for j, pool in enumerate(adapters) if pool is not None]
-        if some:
-            adapters_forward(x, ids, [adapters[j] for j in some], ys=[ys[j] for j in some], stream=stream)
+    if some:
+        _adapters_launch(beside, x, None, stream)
     if rotation is not None:
-        which = sorted(rotate)
-        heads_norm_rotate([ys[j] for j in which], positions, rotation, weights=[rotate[j] for j in which],
-                          outs=[ys[j] for j in which], stream=stream)
+        _check(lib().lb_heads_norm_rotate(*heads[0], _stream_of(stream, heads[1])), "lb_heads_norm_rotate")
     return ys
 
 
@@ -548,10 +555,15 @@ def linear_backward(x, dy, main: PackedPath, residual: PackedPath | None = None,
     if tuple(dy.shape) != (tokens, n_out):
         raise ValueError(f"dy must be [{tokens}, {n_out}], got {tuple(dy.shape)}")
     npaths = 2 if residual is not None else 1
+    if adapters is not None and ids is None:
+        raise ValueError("adapters need ids, each token's adapter")
     if dx is None and want_dx:
         dx = _new((tokens, n_in), torch.bfloat16, x.device, stream)
     if dx is not None:
         _require(dx, "dx", torch.bfloat16)
+    if adapters is not None:  # checked before the layer's own pass is launched
+        beside = _adapters_backward_call(x, dy, ids, adapters, None, dx, dx is not None, None, None, stream)
+        _adapters_checked(lib().lb_adapters_backward, "lb_adapters_backward", tokens, beside[0])
     dh = _new((npaths, n_out), torch.float32, x.device, stream)
     dg = _new((npaths, n_in), torch.float32, x.device, stream)
     dl = _new((main.rank + (residual.rank if residual is not None else 0),), torch.float32, x.device, stream)
@@ -569,7 +581,7 @@ def linear_backward(x, dy, main: PackedPath, residual: PackedPath | None = None,
         "lb_linear_backward")
     out = {"dx": dx, "dh": dh, "dg": dg, "dl": dl}
     if adapters is not None:
-        more = adapters_backward(x, dy, ids, adapters, dx=dx, want_dx=dx is not None, stream=stream)
+        more = _adapters_backward_launch(beside, x, None, stream)
         out["da"], out["db"] = more["da"], more["db"]
     return out
 
@@ -704,6 +716,12 @@ def adapters_forward(x, ids, pools, bases=None, ys=None, workspace=None, stream=
     and ``ys`` are lists of bf16 [tokens, n_out_j]: without ``bases`` the
     ``ys`` are updated in place, without ``ys`` they are allocated.  Returns
     ``ys``."""
+    call = _adapters_call(x, ids, pools, bases, ys, stream)
+    return _adapters_launch(call, x, workspace, stream)
+
+
+def _adapters_call(x, ids, pools, bases, ys, stream) -> tuple:
+    """What the binding checks of an adapters_forward call, and the arguments of the library's."""
     torch = _torch()
     bf16 = torch.bfloat16
     device = _current(x, "x")
@@ -739,14 +757,28 @@ def adapters_forward(x, ids, pools, bases=None, ys=None, workspace=None, stream=
             y = ys[j]
             e.ldy = _rows_ld(y, "ys", tokens, n_out, bf16, device)
         e.y = y.data_ptr()
+    args = (x.data_ptr(), tokens, n_in, x.stride(0) if tokens > 1 else n_in, ids_ptr, n, arr)
+    return args, c.count, ranks, device, made if ys is None else ys
+
+
+def _adapters_launch(call: tuple, x, workspace, stream):
+    args, count, ranks, device, ys = call
     if workspace is None:
-        workspace = _new_workspace(x, adapters_workspace_bytes(tokens, n_in, c.count, tuple(ranks)), stream)
+        workspace = _new_workspace(x, adapters_workspace_bytes(args[1], args[2], count, tuple(ranks)), stream)
     else:
         _require_workspace(workspace)
-    _check(lib().lb_adapters_forward(
-        x.data_ptr(), tokens, n_in, x.stride(0) if tokens > 1 else n_in, ids_ptr, n, arr, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream_of(stream, device)), "lb_adapters_forward")
-    return made if ys is None else ys
+    _check(lib().lb_adapters_forward(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                     _stream_of(stream, device)), "lb_adapters_forward")
+    return ys
+
+
+def _adapters_checked(function, name: str, tokens: int, args: tuple) -> None:
+    """Raises what the library refuses of an adapters call that follows another
+    launch, before that launch.  A workspace without bytes is the last thing that
+    the library finds wrong with a call, before it touches the device."""
+    status = function(*args, args[0], 0, None) if tokens else LB_OK
+    if status != LB_ERR_WORKSPACE_TOO_SMALL:
+        _check(status, name)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -762,6 +794,12 @@ def adapters_backward(x, dy, ids, pool: AdapterPool, dx_base=None, dx=None, want
     adapters' part is added; without it ``dx`` is updated in place.  Returns
     ``{"dx": bf16 [tokens, n_in] or None, "da": fp32 [count, rank, n_in],
     "db": fp32 [count, n_out, rank]}``, allocated with torch when not given."""
+    call = _adapters_backward_call(x, dy, ids, pool, dx_base, dx, want_dx, da, db, stream)
+    return _adapters_backward_launch(call, x, workspace, stream)
+
+
+def _adapters_backward_call(x, dy, ids, pool, dx_base, dx, want_dx, da, db, stream) -> tuple:
+    """_adapters_call for the backward pass."""
     torch = _torch()
     bf16, f32 = torch.bfloat16, torch.float32
     device = _current(x, "x")
@@ -790,17 +828,21 @@ def adapters_backward(x, dy, ids, pool: AdapterPool, dx_base=None, dx=None, want
         da = _new_dense((count, rank, n_in), (rank * n_in, n_in, 1), f32, device, stream)
     if db is None:
         db = _new_dense((count, n_out, rank), (n_out * rank, rank, 1), f32, device, stream)
+    args = (x.data_ptr(), dy.data_ptr(), tokens, n_in, n_out, x.stride(0) if tokens > 1 else n_in, lddy, ids_ptr,
+            pool._p, dx_base.data_ptr() if with_base else None, ldbase, dx.data_ptr() if dx is not None else None, lddx,
+            da.data_ptr(), db.data_ptr())
+    return args, (tokens, n_in, n_out, count, rank), device, {"dx": dx, "da": da, "db": db}
+
+
+def _adapters_backward_launch(call: tuple, x, workspace, stream) -> dict:
+    args, sizes, device, out = call
     if workspace is None:
-        need = adapters_backward_workspace_bytes(tokens, n_in, n_out, count, rank)
-        workspace = _new_workspace(x, need, stream)
+        workspace = _new_workspace(x, adapters_backward_workspace_bytes(*sizes), stream)
     else:
         _require_workspace(workspace)
-    _check(lib().lb_adapters_backward(
-        x.data_ptr(), dy.data_ptr(), tokens, n_in, n_out, x.stride(0) if tokens > 1 else n_in, lddy, ids_ptr,
-        pool._p, dx_base.data_ptr() if with_base else None, ldbase, dx.data_ptr() if dx is not None else None, lddx,
-        da.data_ptr(), db.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _stream_of(stream, device)), "lb_adapters_backward")
-    return {"dx": dx, "da": da, "db": db}
+    _check(lib().lb_adapters_backward(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                      _stream_of(stream, device)), "lb_adapters_backward")
+    return out
 
 
 # ------------------------------------------------------------------ heads
@@ -860,6 +902,13 @@ def heads_norm_rotate(tensors, positions, rotation: HeadRotation, weights=None, 
     ``positions`` (int32 [tokens] on the device), for up to 4 tensors bf16
     [tokens, heads * head_dim].  ``outs`` may be the tensors themselves; they
     are allocated when not given.  Returns them."""
+    args, device, outs = _heads_forward_call(tensors, positions, rotation, weights, outs, stream)
+    _check(lib().lb_heads_norm_rotate(*args, _stream_of(stream, device)), "lb_heads_norm_rotate")
+    return outs
+
+
+def _heads_forward_call(tensors, positions, rotation: HeadRotation, weights, outs, stream) -> tuple:
+    """What the binding checks of a heads_norm_rotate call, and the arguments of the library's."""
     torch = _torch()
     bf16, d = torch.bfloat16, rotation.head_dim
     device, tokens, pos, freq = _heads_call(tensors, positions, rotation, weights, "tensors")
@@ -882,9 +931,23 @@ def heads_norm_rotate(tensors, positions, rotation: HeadRotation, weights=None, 
         e.out = o.data_ptr()
         if weights is not None and weights[j] is not None:
             e.weight = _vector_ptr(weights[j], "weights", d, bf16, device)
-    _check(lib().lb_heads_norm_rotate(tokens, d, rotation.rotary_dim, rotation.code, pos, freq, rotation.eps,
-                                      len(tensors), arr, _stream_of(stream, device)), "lb_heads_norm_rotate")
-    return made if outs is None else outs
+    args = (tokens, d, rotation.rotary_dim, rotation.code, pos, freq, rotation.eps, len(tensors), arr)
+    return args, device, made if outs is None else outs
+
+
+def _heads_checked(args: tuple) -> None:
+    """Raises what the library refuses of a heads call that follows another
+    launch, before that launch: what it checks of the sizes also where there are
+    no tokens, then the limits of its tensors."""
+    name = "lb_heads_norm_rotate"
+    _check(lib().lb_heads_norm_rotate(0, *args[1:], None), name)
+    arr = args[-1]
+    if sum(e.heads for e in arr) > MAX_HEADS or any(max(e.ld_in, e.ld_out) > 1 << 30 for e in arr):
+        raise LbError(LB_ERR_UNSUPPORTED_SHAPE, name)
+    if any(e.heads < 1 or e.ld_in < e.heads * args[1] or e.ld_out < e.heads * args[1] for e in arr):
+        raise LbError(LB_ERR_INVALID_ARGUMENT, name)
+    if any(v % 16 for e in arr for v in (e.in_ or 0, e.out or 0, e.weight or 0, 2 * e.ld_in, 2 * e.ld_out)):
+        raise LbError(LB_ERR_MISALIGNED, name)
 
 
 @functools.lru_cache(maxsize=256)
@@ -998,9 +1061,14 @@ class LittleBitLinear:
     def __call__(self, x, y=None, stream=None, adapters: AdapterPool | None = None, ids=None):
         if adapters is not None and ids is None:
             raise ValueError("adapters need ids, each token's adapter")
+        if adapters is not None:  # checked before the layer is launched
+            if y is None:
+                y = _new((x.shape[0], self.n_out), _torch().bfloat16, x.device, stream)
+            beside = _adapters_call(x, ids, [adapters], None, [y], stream)
+            _adapters_checked(lib().lb_adapters_forward, "lb_adapters_forward", x.shape[0], beside[0])
         # the kept workspace belongs to the current stream
         y = linear_forward(x, self.main, self.residual, y=y, stream=stream,
                            workspace=self.workspace(x.shape[0], x.device) if stream is None else None)
         if adapters is not None:
-            adapters_forward(x, ids, [adapters], ys=[y], stream=stream)
+            _adapters_launch(beside, x, None, stream)
         return y

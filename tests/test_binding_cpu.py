@@ -116,3 +116,85 @@ def test_memory_for_a_stream_comes_from_it(world):
 def test_memory_without_a_stream_comes_from_the_current_one(world):
     for returned, made, _ in calls_of(world, None):
         assert all(t.stream is world.default and not t.recorded for t in made)
+
+
+def group(world):
+    """A sibling group with everything behind it, and the layer's other calls, as keyword arguments."""
+    i32 = torch.int32
+    return dict(x=world.tensor(5, 64), ids=world.tensor(5, dtype=i32), positions=world.tensor(5, dtype=i32),
+                pools=[world.pool(3, 8, 64, 96), None], rot=lb.HeadRotation(32, world.tensor(16, dtype=torch.float32)),
+                weight=world.tensor(32), path=world.path(64, 96, 32))
+
+
+def siblings(world, g):
+    return lb.linear_forward_siblings(g["x"], [(g["path"], None)] * 2, adapters=g["pools"], ids=g["ids"], rotation=g["rot"],
+                                      positions=g["positions"], rotate={0: g["weight"]})
+
+
+def layer(world, g):
+    return lb.LittleBitLinear(g["path"])(g["x"], adapters=g["pools"][0], ids=g["ids"])
+
+
+def backward(world, g):
+    return lb.linear_backward(g["x"], world.tensor(5, 96), g["path"], adapters=g["pools"][0], ids=g["ids"], dx=g.get("dx"))
+
+
+SOME = [siblings, layer, backward]
+BAD_GROUPS = [  # what is wrong, the calls that see it, the error
+    ("ids of another type", SOME, TypeError, lambda w, g: g.update(ids=w.tensor(5, dtype=torch.float32))),
+    ("too few ids", SOME, ValueError, lambda w, g: g.update(ids=w.tensor(4, dtype=torch.int32))),
+    ("no ids", SOME, ValueError, lambda w, g: g.update(ids=None)),
+    ("ids on the host", SOME, ValueError, lambda w, g: g.update(ids=torch.zeros(5, dtype=torch.int32))),
+    ("a pool for another x", SOME, ValueError, lambda w, g: g.update(pools=[w.pool(3, 8, 32, 96), None])),
+    ("a pool for another y", SOME, ValueError, lambda w, g: g.update(pools=[w.pool(3, 8, 64, 64), None])),
+    ("an odd rank", SOME, lb.LbError, lambda w, g: g.update(pools=[w.pool(3, 12, 64, 96), None])),
+    ("too many adapters", SOME, lb.LbError, lambda w, g: g.update(pools=[w.pool(1025, 8, 64, 96), None])),
+    ("a pool at an odd address", SOME, lb.LbError, lambda w, g: g.update(pools=[
+        lb.AdapterPool(w.tensor(3, 8, 64, address=1 << 30 | 2), w.tensor(3, 96, 8)), None])),
+    ("pools of unlike counts", [siblings], lb.LbError, lambda w, g: g.update(pools=[w.pool(3, 8, 64, 96), w.pool(4, 8, 64, 96)])),
+    ("a dx of another shape", [backward], ValueError, lambda w, g: g.update(dx=w.tensor(5, 96))),
+    ("positions of another type", [siblings], TypeError, lambda w, g: g.update(positions=w.tensor(5, dtype=torch.float32))),
+    ("too few positions", [siblings], ValueError, lambda w, g: g.update(positions=w.tensor(4, dtype=torch.int32))),
+    ("no positions", [siblings], ValueError, lambda w, g: g.update(positions=None)),
+    ("a weight of another size", [siblings], ValueError, lambda w, g: g.update(weight=w.tensor(64))),
+    ("a weight at an odd address", [siblings], lb.LbError, lambda w, g: g.update(weight=w.tensor(32, address=1 << 30 | 2))),
+    ("heads that do not divide", [siblings], ValueError, lambda w, g: g.update(
+        rot=lb.HeadRotation(40, w.tensor(16, dtype=torch.float32)))),
+    ("more turned than a head has", [siblings], lb.LbError, lambda w, g: g.update(
+        rot=lb.HeadRotation(32, w.tensor(24, dtype=torch.float32)))),
+    ("a negative eps", [siblings], lb.LbError, lambda w, g: g.update(
+        rot=lb.HeadRotation(32, w.tensor(16, dtype=torch.float32), eps=-1.0))),
+]
+
+
+@pytest.mark.parametrize("call,error,change", [pytest.param(c, e, f, id=f"{c.__name__}: {what}")
+                                               for what, calls, e, f in BAD_GROUPS for c in calls])
+def test_a_refused_call_launches_nothing(world, call, error, change):
+    g = group(world)
+    change(world, g)
+    with pytest.raises(error):
+        call(world, g)
+    assert not world.calls
+
+
+def test_a_group_that_is_right_launches_in_order(world):
+    siblings(world, group(world))
+    layer(world, group(world))
+    backward(world, group(world))
+    assert world.names() == ["lb_linear_forward_siblings", "lb_adapters_forward", "lb_heads_norm_rotate", "lb_linear_forward",
+                             "lb_adapters_forward", "lb_linear_backward", "lb_adapters_backward"]
+
+
+def test_wide_heads_are_refused_before_the_projections(world):
+    x, path = world.tensor(5, 64), world.path(64, 4097 * 32, 32)
+    with pytest.raises(lb.LbError) as e:
+        lb.linear_forward_siblings(x, [(path, None)], rotation=lb.HeadRotation(32), positions=world.tensor(5, dtype=torch.int32),
+                                   rotate={0: None})
+    assert e.value.status == lb.LB_ERR_UNSUPPORTED_SHAPE and not world.calls
+
+
+def test_no_tokens_launch_no_check(world):
+    g = group(world)
+    g.update(x=world.tensor(0, 64), ids=world.tensor(0, dtype=torch.int32))
+    lb.linear_backward(g["x"], world.tensor(0, 96), g["path"], adapters=g["pools"][0], ids=g["ids"])
+    assert world.names() == ["lb_linear_backward", "lb_adapters_backward"]
