@@ -405,8 +405,8 @@ def linear_forward_siblings(x, layers, ys=None, workspace=None, stream=None, ada
 
     With ``adapters`` (one :class:`AdapterPool` or None per layer) and ``ids``
     each token's adapter is added to the outputs (:func:`adapters_forward`).
-    With ``rotation`` (a :class:`HeadRotation`) and ``positions`` the outputs
-    named by ``rotate``, a dict from the layer's index to its norm weight (or
+    With ``rotation`` (a :class:`HeadRotation`) and ``positions`` (not needed
+    for a norm alone) the outputs named by ``rotate``, a dict from the layer's index to its norm weight (or
     None for no norm), then get their heads normed and rotated
     (:func:`heads_norm_rotate`): an attention block's queries and keys."""
     torch = _torch()
@@ -418,8 +418,10 @@ def linear_forward_siblings(x, layers, ys=None, workspace=None, stream=None, ada
         _require(y, f"ys[{j}]", torch.bfloat16)
     if adapters is not None and (len(adapters) != len(layers) or ids is None):
         raise ValueError("adapters must name a pool or None for each layer, and ids each token's adapter")
-    if rotation is not None and (positions is None or not rotate or not all(0 <= j < len(layers) for j in rotate)):
-        raise ValueError("rotation needs positions and, in rotate, the layers whose outputs are rotated")
+    if rotation is not None and (not rotate or not all(0 <= j < len(layers) for j in rotate)):
+        raise ValueError("rotation needs, in rotate, the layers whose outputs are normed and rotated")
+    if rotation is not None and positions is None and rotation.rotary_dim:
+        raise ValueError("rotation needs positions")
     # what follows the projections is checked before they are launched
     some = [j for j, pool in enumerate(adapters or ()) if pool is not None]
     if some:
@@ -899,7 +901,8 @@ def _heads_of(t, name: str, head_dim: int) -> tuple:
 def heads_norm_rotate(tensors, positions, rotation: HeadRotation, weights=None, outs=None, stream=None):
     """``lb_heads_norm_rotate``: the RMS norm of each head (where ``weights``
     has a bf16 [head_dim] weight for the tensor) and the rotation by
-    ``positions`` (int32 [tokens] on the device), for up to 4 tensors bf16
+    ``positions`` (int32 [tokens] on the device; not read where nothing is
+    rotated), for up to 4 tensors bf16
     [tokens, heads * head_dim].  ``outs`` may be the tensors themselves; they
     are allocated when not given.  Returns them."""
     args, device, outs = _heads_forward_call(tensors, positions, rotation, weights, outs, stream)

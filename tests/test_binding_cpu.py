@@ -198,3 +198,11 @@ def test_no_tokens_launch_no_check(world):
     g.update(x=world.tensor(0, 64), ids=world.tensor(0, dtype=torch.int32))
     lb.linear_backward(g["x"], world.tensor(0, 96), g["path"], adapters=g["pools"][0], ids=g["ids"])
     assert world.names() == ["lb_linear_backward", "lb_adapters_backward"]
+
+
+def test_a_norm_alone_needs_no_positions(world):
+    """As heads_norm_rotate itself."""
+    g = group(world)
+    lb.linear_forward_siblings(g["x"], [(g["path"], None)], rotation=lb.HeadRotation(32), rotate={0: g["weight"]})
+    lb.heads_norm_rotate([world.tensor(5, 96)], None, lb.HeadRotation(32), weights=[g["weight"]])
+    assert world.names() == ["lb_linear_forward_siblings", "lb_heads_norm_rotate", "lb_heads_norm_rotate"]
