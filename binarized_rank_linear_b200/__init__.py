@@ -260,9 +260,11 @@ def _require(t, name: str, dtype, device: str = "cuda", contiguous: bool = False
         raise ValueError(f"{name} must be in {'device' if device == 'cuda' else 'host'} memory")
 
 
-def _require_workspace(ws) -> None:
+def _require_workspace(ws, device=None) -> None:
     if not ws.is_cuda or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous device tensor")
+    if device is not None and ws.device != device:
+        raise ValueError(f"workspace must be on {device}, got {ws.device}")
 
 
 # Memory that a call makes for itself.  On a stream of the caller's it comes from
@@ -768,7 +770,7 @@ def _adapters_launch(call: tuple, x, workspace, stream):
     if workspace is None:
         workspace = _new_workspace(x, adapters_workspace_bytes(args[1], args[2], count, tuple(ranks)), stream)
     else:
-        _require_workspace(workspace)
+        _require_workspace(workspace, device)
     _check(lib().lb_adapters_forward(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                      _stream_of(stream, device)), "lb_adapters_forward")
     return ys
@@ -841,7 +843,7 @@ def _adapters_backward_launch(call: tuple, x, workspace, stream) -> dict:
     if workspace is None:
         workspace = _new_workspace(x, adapters_backward_workspace_bytes(*sizes), stream)
     else:
-        _require_workspace(workspace)
+        _require_workspace(workspace, device)
     _check(lib().lb_adapters_backward(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                       _stream_of(stream, device)), "lb_adapters_backward")
     return out
@@ -1000,7 +1002,7 @@ def heads_norm_rotate_backward(tensors, douts, positions, rotation: HeadRotation
     if workspace is None:
         workspace = _new_workspace(tensors[0], heads_backward_workspace_bytes(d) if sums else 0, stream)
     else:
-        _require_workspace(workspace)
+        _require_workspace(workspace, device)
     _check(lib().lb_heads_norm_rotate_backward(tokens, d, rotation.rotary_dim, rotation.code, pos, freq, rotation.eps, n,
                                                arr, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                                _stream_of(stream, device)), "lb_heads_norm_rotate_backward")

@@ -206,3 +206,15 @@ def test_a_norm_alone_needs_no_positions(world):
     lb.linear_forward_siblings(g["x"], [(g["path"], None)], rotation=lb.HeadRotation(32), rotate={0: g["weight"]})
     lb.heads_norm_rotate([world.tensor(5, 96)], None, lb.HeadRotation(32), weights=[g["weight"]])
     assert world.names() == ["lb_linear_forward_siblings", "lb_heads_norm_rotate", "lb_heads_norm_rotate"]
+
+
+def test_a_workspace_on_another_device_is_refused(world):
+    g = group(world)
+    far = world.tensor(1 << 22, dtype=torch.uint8, device=torch.device("cuda", 1))
+    y, w = world.tensor(5, 96), [g["weight"]]
+    for call in (lambda: lb.adapters_forward(g["x"], g["ids"], g["pools"][:1], ys=[y], workspace=far),
+                 lambda: lb.adapters_backward(g["x"], y, g["ids"], g["pools"][0], want_dx=False, workspace=far),
+                 lambda: lb.heads_norm_rotate_backward([y], [y], g["positions"], g["rot"], weights=w, workspace=far)):
+        with pytest.raises(ValueError, match="workspace must be on cuda:0"):
+            call()
+    assert not world.calls
