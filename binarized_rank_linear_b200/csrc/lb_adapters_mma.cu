@@ -34,9 +34,10 @@
 // to nearest.  The extra products and reads hide behind the wide operand.
 //
 // A launch begins as soon as the one before allows and waits only for what that
-// one writes: of the kernels behind plan each reads the plan, the weights and the
-// wide operand before its wait, which are older (every launch lets the next begin
-// only after its own wait, so all launches but the last one are complete).  In
+// one writes.  plan reads nothing ahead of its wait; of the kernels behind it each
+// reads the plan, the weights and the wide operand before its wait, which are
+// older: each of them, and plan, lets the next begin only after its own wait, so
+// that all launches but the last one are complete, whatever came before plan.  In
 // the backward pass wgrad goes before expand, and expand, which needs nothing of
 // it, begins on the SMs that wgrad leaves.  Measured on the device, alone and at
 // full clocks, 8192 tokens of 5120 columns, 8 adapters of rank 64: forward to 5120
@@ -96,14 +97,14 @@ static_assert(kPlanTokens / TM + LB_MAX_ADAPTERS < 1 << 14 && kPlanTokens / 64 +
 // Each warp takes a run of tokens in order, so that an adapter's tokens keep
 // their order and sums over them do not depend on timing.  One CTA runs this
 // once, so its instructions come from far away: the code is kept short (loops
-// stay rolled; unrolled it took twice as long).  The ids are read before the
-// launch ahead is done; nothing is written before that.
+// stay rolled; unrolled it took twice as long).  The ids may have been written by
+// the work ahead on the stream, so they are read after the wait for it.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
 {
     extern __shared__ int hist[];  // [warp][bin]; bin `count`: no adapter
     __shared__ uint32_t sums[kPlanWarps];
     __shared__ int first_tile[LB_MAX_ADAPTERS + 1], total[LB_MAX_ADAPTERS + 1];
-    __shared__ int held[kHeld];  // bins, with places among a warp's tokens of a bin, then slots
+    __shared__ int held[kHeld];  // bins, with places among a warp's tokens of a bin
     const int bins = p.count + 1, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int rounds = (p.tokens + kPlanThreads - 1) / kPlanThreads;
     const int t0 = w * rounds * 32 + lane;
@@ -113,32 +114,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         if (id >= p.count) set_status(p.status, LB_ERR_INVALID_ARGUMENT);
         return id < 0 || id >= p.count ? p.count : id;
     };
+#pragma unroll 1
+    for (int i = tid; i < kPlanWarps * bins; i += kPlanThreads) hist[i] = 0;
+    pdl_wait();
+    pdl_launch_dependents();
     if (hold) {
         int ids[kHeld / kPlanThreads];
 #pragma unroll
         for (int i = 0; i < kHeld / kPlanThreads; ++i) {
             const int t = i * kPlanThreads + tid;
-            ids[i] = t < p.tokens ? __ldg(p.ids + t) : -1;
+            ids[i] = t < p.tokens ? __ldcg(p.ids + t) : -1;
         }
 #pragma unroll
         for (int i = 0; i < kHeld / kPlanThreads; ++i) held[i * kPlanThreads + tid] = bin_of(ids[i]);
     }
-#pragma unroll 1
-    for (int i = tid; i < kPlanWarps * bins; i += kPlanThreads) hist[i] = 0;
     __syncthreads();
     auto put = [&](int t, int slot, bool first, bool last) {
         p.plan.perm[slot] = t;
         if (first) p.plan.tiles[slot / TM].first = t;
         if (last) p.plan.tiles[slot / TM].last = t;
-    };
-    constexpr int kFirst = 1 << 30, kLast = 1 << 29;  // of a tile; slots are below
-    bool waited = false;
-    auto wait_once = [&] {
-        if (!waited) {
-            pdl_wait();
-            pdl_launch_dependents();
-        }
-        waited = true;
     };
     int all_tiles = 0, tile0 = 0, block0 = 0, all_blocks = 0;
     // pass 0 counts each warp's tokens of each bin, pass 1 gives them their slots:
@@ -149,7 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         for (int i = 0; i < rounds; ++i) {
             const int t = t0 + 32 * i;
             int b = -1;
-            if (t < p.tokens) b = hold ? held[t] : bin_of(__ldg(p.ids + t));
+            if (t < p.tokens) b = hold ? held[t] : bin_of(__ldcg(p.ids + t));
             const uint32_t same = __match_any_sync(0xffffffffu, b);  // the lanes with the same bin
             const int had = b >= 0 ? mine[b] : 0;
             __syncwarp();
@@ -208,29 +202,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         block0 = (int)(before >> kTileBits);
         if (tid < p.count) first_tile[tid] = tile0;
         if (tid == 0) first_tile[p.count] = all_tiles;
-        if (!hold) wait_once();
         __syncthreads();
         if (hold) break;
     }
-    if (hold) {  // written after the wait
+    if (hold) {
 #pragma unroll 2
         for (int i = 0; i < rounds; ++i) {
             const int t = t0 + 32 * i;
             if (t >= p.tokens) break;
             const int v = held[t], b = v & ((1 << kBinBits) - 1);
             const int at = mine[b] + (v >> kBinBits);
-            held[t] = first_tile[b] * TM + at | (at % TM == 0 ? kFirst : 0) |
-                      (at % TM == TM - 1 || at == total[b] - 1 ? kLast : 0);
-        }
-    }
-    wait_once();
-    if (hold) {
-#pragma unroll 2
-        for (int i = 0; i < rounds; ++i) {
-            const int t = t0 + 32 * i;
-            if (t >= p.tokens) break;
-            const int v = held[t];
-            put(t, v & (kLast - 1), (v & kFirst) != 0, (v & kLast) != 0);
+            put(t, first_tile[b] * TM + at, at % TM == 0, at % TM == TM - 1 || at == total[b] - 1);
         }
     }
     if (tid < p.count) {

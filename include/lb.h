@@ -388,10 +388,8 @@ LB_API lb_status lb_linear_backward(const uint16_t *x, const uint16_t *dy, int64
  *   strides of at most 2^30; a, b, da and db 16-byte aligned, ids, scale and
  *   ranks 4-byte aligned.  No token is a no-op for the forward call.  The workspace as there: its contents on entry do not
  *   matter, and calls that share it must be ordered on one stream.
- *   ids and the pool (a, b, scale, ranks) may be read before the work ahead on
- *   the stream has finished, where that work lets a launch behind it start
- *   early (programmatic dependent launch): a kernel that writes them must not
- *   do so.  None of this library's does both.
+ *   The call's inputs may be written by the work directly ahead on the stream,
+ *   also by a kernel that lets the launch behind it start early.
  * Errors as lb_linear_forward. */
 #define LB_MAX_ADAPTERS 1024
 #define LB_MAX_ADAPTER_RANK 128

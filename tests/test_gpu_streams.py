@@ -1,8 +1,13 @@
 """Calls on a stream of the caller's, and behind kernels that let the next
 launch start early, on the GPU."""
+import ctypes
+import os
+import subprocess
+
 import pytest
 
 import binarized_rank_linear_b200 as lb
+from binarized_rank_linear_b200 import build as lb_build
 from tests.test_gpu_adapters import gen, make_ids, make_pool, normal, torch_
 from tests.test_gpu_heads import make
 
@@ -49,3 +54,62 @@ def test_memory_that_the_current_stream_still_reads(tokens):
         t.cuda.synchronize()
         assert all(bool((k == 7).all()) for k in kept)
         assert all(t.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.fixture(scope="module")
+def early_copy(tmp_path_factory):
+    """copy(dst, src, seconds): dst = src by a kernel that lets the launch behind
+    it start at once and writes only when `seconds` have passed."""
+    so = str(tmp_path_factory.mktemp("early") / "early_writer.so")
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "early_writer.cu")
+    subprocess.run([lb_build.NVCC, *lb_build.ARCH, "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", "-o", so, src], check=True)
+    launch = ctypes.CDLL(so).early_copy_launch
+    launch.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p]
+
+    def copy(dst, src, seconds=1e-3):
+        t = torch_()
+        words = dst.numel() * dst.element_size() // 4
+        assert words == src.numel() * src.element_size() // 4 and dst.is_contiguous() and src.is_contiguous()
+        assert launch(dst.data_ptr(), src.data_ptr(), words, int(seconds * 1e9), t.cuda.current_stream().cuda_stream) == 0
+
+    return copy
+
+
+def behind(copy, fields, call, what):
+    """`call()` with each of `fields` written directly ahead of it gives what it gives with them in place."""
+    t = torch_()
+    new = {k: v.clone() for k, v in fields.items()}
+    t.cuda.synchronize()
+    want = [v.clone() for v in call()]
+    for name, field in fields.items():
+        field.copy_(new[name].flatten().roll(1).view_as(field))
+        t.cuda.synchronize()
+        copy(field, new[name])
+        got = call()
+        t.cuda.synchronize()
+        assert all(t.equal(a, b) for a, b in zip(got, want)), f"{what}: {name} was read before it was written"
+    assert lb.device_status() == lb.LB_OK
+
+
+@pytest.mark.parametrize("tokens", [1, 30, 400, 9001])
+def test_adapters_behind_an_early_writer(early_copy, tokens):
+    t = torch_()
+    g = gen(63)
+    n_in, n_out = 512, 1024
+    pool = make_pool(g, 5, 16, n_in, n_out, [16, 3, 8, 12, 15])
+    x, dy, base = normal(g, tokens, n_in), normal(g, tokens, n_out), normal(g, tokens, n_out)
+    ids = t.arange(tokens, device="cuda", dtype=t.int32) * 2 % 5
+    y, dx = t.empty_like(base), t.empty_like(x)
+    fields = dict(ids=ids, a=pool.a, b=pool.b, scale=pool.scale, ranks=pool.ranks, x=x)
+    if tokens == 1:  # rolled by one it would be what it was
+        stale = t.tensor([3], dtype=t.int32, device="cuda")
+        fields.pop("ids")
+        want = lb.adapters_forward(x, ids, [pool], bases=[base])[0].clone()
+        new = ids.clone()
+        ids.copy_(stale)
+        t.cuda.synchronize()
+        early_copy(ids, new)
+        assert t.equal(lb.adapters_forward(x, ids, [pool], bases=[base])[0], want)
+    behind(early_copy, dict(fields, base=base), lambda: lb.adapters_forward(x, ids, [pool], bases=[base], ys=[y]), "forward")
+    behind(early_copy, dict(fields, dy=dy), lambda: [*lb.adapters_backward(x, dy, ids, pool, dx_base=x, dx=dx).values()],
+           "backward")
