@@ -453,8 +453,7 @@ LB_API lb_status lb_adapters_backward(const uint16_t *x, const uint16_t *dy, int
  * Shapes: head_dim a multiple of 8 up to 256, rotary_dim a multiple of 8 from 0
  *   to head_dim, heads >= 1 and at most 4096 in all, eps >= 0 and finite.  ld multiples of
  *   8 up to 2^30, bf16 tensors and the workspace 16-byte aligned, the rest 4-byte.
- *   positions, inv_freq and weight may be read before the work ahead on the
- *   stream has finished, as ids and the pool are above.
+ *   The inputs may be written by the work directly ahead, as above.
  * Errors as lb_linear_forward. */
 typedef enum { LB_ROTATE_HALVES = 0, LB_ROTATE_PAIRS = 1 } lb_rotation;
 typedef struct {

@@ -113,3 +113,31 @@ def test_adapters_behind_an_early_writer(early_copy, tokens):
     behind(early_copy, dict(fields, base=base), lambda: lb.adapters_forward(x, ids, [pool], bases=[base], ys=[y]), "forward")
     behind(early_copy, dict(fields, dy=dy), lambda: [*lb.adapters_backward(x, dy, ids, pool, dx_base=x, dx=dx).values()],
            "backward")
+
+
+@pytest.mark.parametrize("tokens,rotation", [(2, "halves"), (300, "pairs"), (2000, "halves")])
+def test_heads_behind_an_early_writer(early_copy, tokens, rotation):
+    t = torch_()
+    g, rot, pos, (x,), (w,) = make(tokens, [3], 128, 64, rotation, [True], 1000, 64)
+    dout = normal(g, *x.shape)
+    out = t.empty_like(x)
+    fields = dict(positions=pos, inv_freq=rot.inv_freq, weight=w, x=x)
+    behind(early_copy, fields, lambda: lb.heads_norm_rotate([x], pos, rot, weights=[w], outs=[out]), "forward")
+    behind(early_copy, dict(fields, dout=dout), lambda: [*lb.heads_norm_rotate_backward([x], [dout], pos, rot, weights=[w],
+                                                                                      dins=[out])[0].values()], "backward")
+
+
+def test_heads_behind_a_launch_that_takes_longer_than_their_waits(early_copy):
+    """The kernels' own waits give up after 2 s; the time until the launch ahead
+    has finished is not theirs."""
+    t = torch_()
+    g, rot, pos, (x,), (w,) = make(40, [3], 128, 128, "halves", [True], 7, 65)
+    out = t.empty_like(x)
+    want = lb.heads_norm_rotate([x], pos, rot, weights=[w])[0].clone()
+    late = x.clone()
+    x.zero_()
+    t.cuda.synchronize()
+    early_copy(x, late, seconds=2.6)
+    lb.heads_norm_rotate([x], pos, rot, weights=[w], outs=[out])
+    assert lb.device_status() == lb.LB_OK
+    assert t.equal(out, want)
