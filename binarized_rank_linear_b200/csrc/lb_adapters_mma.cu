@@ -1335,7 +1335,12 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
         uint32_t ph = 1;
         Product<NK> q(p, w0, w0 < w1);
         bool waited = false;
-        for (int w = w0; w < w1;) {  // to the end in every loader, whatever happens
+        // Loaders 2 and 3 take no part in a box, so the ring turns without them
+        // there and the parity they would wait for may come round again: they leave
+        // such K-blocks alone, and all loaders meet at the next one of copies, so
+        // that nobody is a turn ahead of the ring or behind it.
+        bool boxes = false;  // since they last met
+        for (int w = w0; w < w1;) {  // to the end in every loader, whatever happens: they meet
             const int n = min(q.nkb - q.kb, w1 - w);
             const WgradJob &J = p.job[q.job];
             const CUtensorMap *mx = &J.x.box, *mv = J.v;
@@ -1362,9 +1367,14 @@ __global__ void __launch_bounds__(kWgradThreads, 1) adapter_wgrad_kernel(const _
                 const uint32_t dst = base + s * S::kStage, bar = full0 + 8 * s;
                 const int slot = tile0 * TM + 64 * kb;
                 const bool run = T.run() && T.rows >= 64 * half + 64;
-                bool ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);  // all loaders: nobody is ahead of the ring
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) abort_flag = 1;
+                if (!run && boxes) loaders_meet();
+                boxes = run;
+                bool ok = true;
+                if (!run || loader < 2) {
+                    ok = !abort_flag && mbar_wait(empty0 + 8 * s, ph);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) abort_flag = 1;
+                }
                 if (ok && loader == 0 && elect_one()) {
                     mbar_arrive_expect_tx(bar, S::kStage - (run ? 0u : S::kX));
                     if (run) {

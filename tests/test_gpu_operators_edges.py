@@ -223,3 +223,37 @@ def test_heads_at_their_borders(tokens, heads, d, rd, rotation, norms, first):
         ref.within(o["din"], din, tx, f"tensor {j} din")
         if w is not None:
             ref.within(o["dweight"], dw, tw, f"tensor {j} dweight")
+
+
+def tiles_in_turn(segments, count):
+    """ids whose tiles and K-blocks come now as consecutive tokens, now not:
+    segments of 128 tokens of adapter 0, of 256 of 0 and 1 by turns, of 128 of
+    the last adapter, and of 64 of adapter 0 with a token without one inside."""
+    ids = []
+    for k in segments:
+        ids += {"run": [0] * 128, "turns": [0, 1] * 128, "last": [count - 1] * 128, "broken": [0] * 40 + [-1] + [0] * 23}[k]
+    return torch_().tensor(ids, dtype=torch_().int32, device="cuda")
+
+
+@pytest.mark.parametrize("rank", [16, 64, 128])
+@pytest.mark.parametrize("segments", [
+    ["run", "turns"] * 5, ["run"] * 9 + ["turns"] + ["run"] * 6, ["turns", "last"] * 4 + ["broken"],
+    ["run", "broken", "broken", "turns", "run", "last", "last"] * 2, ["last"] * 8 + ["turns"] + ["last"] * 8,
+])
+def test_boxes_and_copies_in_turn(segments, rank):
+    """The loaders of copied rows leave boxes alone and come back behind them:
+    every gradient, and the same bits each time."""
+    g = gen(41)
+    n_in, n_out, count = 544, 160, 3
+    ids = tiles_in_turn(segments, count)
+    tokens = len(ids)
+    x, dy, base = normal(g, tokens, n_in), normal(g, tokens, n_out), normal(g, tokens, n_in)
+    pool = make_pool(g, count, rank, n_in, n_out)
+    out = lb.adapters_backward(x, dy, ids, pool, dx_base=base)
+    exact, tol = ref.adapters_backward(x, dy, ids, pool.a, pool.b, pool.scale, pool.ranks, base)
+    for name, e, w in zip(("dx", "da", "db"), exact, tol):
+        ref.within(out[name], e, w, name)
+    for _ in range(30):
+        again = lb.adapters_backward(x, dy, ids, pool, dx_base=base)
+        assert all(torch_().equal(again[k], out[k]) for k in out)
+    assert lb.device_status() == lb.LB_OK
