@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
         if (lane == 0) {
             for (int s = 0; s < S::kStages; ++s) {
                 mbar_init(full0 + 8 * s, kFull);
-                mbar_init(empty0 + 8 * s, kExpandWarps);
+                mbar_init(empty0 + 8 * s, kExpandWarps + 1);  // and the MMA thread
             }
             for (int b = 0; b < 2; ++b) {
                 mbar_init(accf0 + 8 * b, 1);
@@ -1040,7 +1040,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
                     v0 = (uint32_t)smem_desc(sV + b * S::kV);
                     ++nv;
                 }
-                if (q.kind != 0) {  // a stage's phases are all waited for, with a product or without
+                // A stage's phases are all waited for, with a product or without, and the
+                // stage is given back by this thread too: where base is only copied nothing
+                // else keeps the ring from turning past it.
+                if (q.kind != 0) {
                     const int ab = na & 1;
                     if ((q.kind == 2 && !mbar_wait(acce0 + 8 * ab, ((uint32_t)(na >> 1) & 1u) ^ 1u)) ||
                         !mbar_wait(full0 + 8 * s, ph) || abort_flag) {
@@ -1062,6 +1065,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_kernel(const __grid_
                         umma_commit(accf0 + 8 * ab);
                         ++na;
                     }
+                    mbar_arrive(empty0 + 8 * s);  // the epilogue's arrivals come after the products
                     if (++s == S::kStages) s = 0, ph ^= 1;
                 }
                 if (u + 1 < u1) advance(q);

@@ -257,3 +257,30 @@ def test_boxes_and_copies_in_turn(segments, rank):
         again = lb.adapters_backward(x, dy, ids, pool, dx_base=base)
         assert all(torch_().equal(again[k], out[k]) for k in out)
     assert lb.device_status() == lb.LB_OK
+
+
+@pytest.mark.parametrize("rank", [16, 64, 128])
+@pytest.mark.parametrize("segments", [
+    ["last"] * 8 + ["run"] + ["last"] * 8, ["turns", "last"] * 4 + ["broken"], ["last", "run"] * 5, ["last"] * 9,
+    ["broken", "last", "broken", "turns", "last", "last"] * 2,
+])
+def test_copied_and_added_tiles_in_turn(segments, rank):
+    """Where base is only copied (the last adapter has rank 0), tile after tile
+    and between tiles with products: every row, and the same bits each time."""
+    g = gen(42)
+    n_in, outs, count = 160, [1056, 544], 3
+    ids = tiles_in_turn(segments, count)
+    tokens = len(ids)
+    x, dy = normal(g, tokens, n_in), normal(g, tokens, outs[0])
+    bases = [normal(g, tokens, o) for o in outs]
+    pools = [make_pool(g, count, rank, n_in, o, [rank, rank - 3, 0]) for o in outs]
+    ys = lb.adapters_forward(x, ids, pools, bases=bases)
+    check_forward(x, ids, pools, bases, ys, "copied and added")
+    out = lb.adapters_backward(x, dy, ids, pools[0], dx_base=x)
+    exact, tol = ref.adapters_backward(x, dy, ids, pools[0].a, pools[0].b, pools[0].scale, pools[0].ranks, x)
+    for name, e, w in zip(("dx", "da", "db"), exact, tol):
+        ref.within(out[name], e, w, name)
+    for _ in range(30):
+        again = lb.adapters_forward(x, ids, pools, bases=bases)
+        assert all(torch_().equal(a, b) for a, b in zip(again, ys))
+    assert lb.device_status() == lb.LB_OK
