@@ -141,3 +141,28 @@ def test_heads_behind_a_launch_that_takes_longer_than_their_waits(early_copy):
     lb.heads_norm_rotate([x], pos, rot, weights=[w], outs=[out])
     assert lb.device_status() == lb.LB_OK
     assert t.equal(out, want)
+
+
+@pytest.mark.parametrize("tokens", [5, 700, 8192, 9001])
+def test_ids_past_the_pool_that_are_written_over_in_time(early_copy, tokens):
+    """What ids held before their writer has finished is not reported, what it
+    writes is."""
+    t = torch_()
+    g = gen(66)
+    pool = make_pool(g, 3, 8, 64, 96)
+    x, base = normal(g, tokens, 64), normal(g, tokens, 96)
+    good = make_ids(g, tokens, 3, "mixed")
+    bad = good.clone()
+    bad[tokens // 2] = 3
+    ids = t.full_like(good, 99)
+    want = lb.adapters_forward(x, good, [pool], bases=[base])[0]
+    assert lb.device_status() == lb.LB_OK
+    early_copy(ids, good)
+    y = lb.adapters_forward(x, ids, [pool], bases=[base])[0]
+    assert lb.device_status() == lb.LB_OK and t.equal(y, want)
+    early_copy(ids, bad)
+    y = lb.adapters_forward(x, ids, [pool], bases=[base])[0]
+    assert lb.device_status() == lb.LB_ERR_INVALID_ARGUMENT
+    assert t.equal(y[tokens // 2], base[tokens // 2])
+    y[tokens // 2] = want[tokens // 2]
+    assert t.equal(y, want)
