@@ -528,16 +528,19 @@ size_t small_workspace(int M, int n_in, int nproj, const int *ranks)
 
 }  // namespace
 
-// Whether a call runs here: see the top of this file.
-static bool small_batch(int tokens, int count)
+// The most tokens of a call that runs here: see the top of this file.
+static int most_small_tokens(int count)
 {
-    return tokens <= std::max(std::min(512, 128 + 48 * count), std::min(kAdapterSmallTokens, 24 * count));
+    return std::max(std::min(512, 128 + 48 * count), std::min(kAdapterSmallTokens, 24 * count));
 }
+static bool small_batch(int tokens, int count) { return tokens <= most_small_tokens(count); }
 
+// Enough for every smaller number of tokens too: the partial sums of a small batch,
+// which grow with n_in, can be more than a larger one's plan and tiles.
 size_t adapters_workspace_bytes(int tokens, int n_in, int count, int nproj, const int *ranks)
 {
-    return small_batch(tokens, count) ? small_workspace(tokens, n_in, nproj, ranks)
-                                      : adapters_mma_workspace_bytes(tokens, count, nproj, ranks);
+    const size_t small = small_workspace(std::min(tokens, most_small_tokens(count)), n_in, nproj, ranks);
+    return small_batch(tokens, count) ? small : std::max(small, adapters_mma_workspace_bytes(tokens, count, nproj, ranks));
 }
 
 cudaError_t adapters_prepare_device(const DeviceInfo &dev) { return adapters_mma_prepare_device(dev); }

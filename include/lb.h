@@ -412,7 +412,8 @@ typedef struct {
 } lb_adapter_projection;
 
 /* Workspace of lb_adapters_forward (the pools' count and rank and n_out are
- * read, no pointer); 0 on a bad argument. */
+ * read, no pointer), enough for every smaller number of tokens too; 0 on a bad
+ * argument. */
 LB_API size_t lb_adapters_workspace_bytes(int64_t tokens, int64_t n_in, int nproj, const lb_adapter_projection *proj);
 LB_API lb_status lb_adapters_forward(const uint16_t *x, int64_t tokens, int64_t n_in, int64_t ldx, const int32_t *ids,
                                      int nproj, const lb_adapter_projection *proj, void *workspace,

@@ -206,3 +206,13 @@ def test_workspace_follows_the_kernels(L):
     for count, border in ((1, 176), (6, 416), (16, 512), (64, 1536), (1000, 2048)):
         sizes = [lb.adapters_workspace_bytes(t, 64, count, (16,)) for t in (1, border, border + 1)]
         assert 0 < sizes[0] <= sizes[1] < sizes[2]
+
+
+@pytest.mark.parametrize("n_in,count,ranks", [(16384, 64, (64,) * 4), (28672, 86, (16,)), (64, 3, (8,)), (1 << 20, 1, (128,) * 4),
+                                              (5120, 1024, (16, 8, 128)), (4096, 8, (16,) * 3)])
+def test_a_workspace_serves_every_smaller_batch(L, n_in, count, ranks):
+    tokens = sorted({*range(1, 200, 13), *range(160, 2200, 61), 512, 513, 1536, 1537, 1736, 2048, 2049, 4096, 1 << 20})
+    sizes = [lb.adapters_workspace_bytes(t, n_in, count, ranks) for t in tokens]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
+    back = [lb.adapters_backward_workspace_bytes(t, n_in, 64, count, ranks[0]) for t in tokens]
+    assert back[0] > 0 and back == sorted(back)
