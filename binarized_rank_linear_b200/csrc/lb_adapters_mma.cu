@@ -471,7 +471,8 @@ struct Shrink {
 
 // Four elements of v from their sums: scaled, zero past the adapter's rank, and
 // split into bf16 parts, each what the ones before leave (exactly; an infinity
-// or NaN is all in the first).
+// or NaN is all in the first, and a finite value that would round to one leaves
+// the largest bf16 there).
 __device__ __forceinline__ void store_v(const ShrinkJob &J, int64_t at, int c, int rank, float scale, const float4 &s)
 {
     float f[4] = {s.x, s.y, s.z, s.w};
@@ -480,7 +481,14 @@ __device__ __forceinline__ void store_v(const ShrinkJob &J, int64_t at, int c, i
 #pragma unroll
     for (int k = 0; k < kParts; ++k) {
         if (J.v[k] == nullptr) break;
-        const uint2 o = make_uint2(pack_bf162(f[0], f[1]), pack_bf162(f[2], f[3]));
+        float g[4] = {f[0], f[1], f[2], f[3]};
+        if (k == 0) {
+            const float most = __int_as_float(0x7f7f0000);  // of bf16
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (fabsf(g[e]) < __int_as_float(0x7f800000)) g[e] = fminf(fmaxf(g[e], -most), most);
+        }
+        const uint2 o = make_uint2(pack_bf162(g[0], g[1]), pack_bf162(g[2], g[3]));
         *reinterpret_cast<uint2 *>(J.v[k] + at) = o;
         const float h[4] = {__uint_as_float(o.x << 16), __uint_as_float(o.x & 0xffff0000u), __uint_as_float(o.y << 16),
                             __uint_as_float(o.y & 0xffff0000u)};

@@ -284,3 +284,36 @@ def test_copied_and_added_tiles_in_turn(segments, rank):
         again = lb.adapters_forward(x, ids, pools, bases=bases)
         assert all(torch_().equal(a, b) for a, b in zip(again, ys))
     assert lb.device_status() == lb.LB_OK
+
+
+@pytest.mark.parametrize("tokens", [10, 300])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_latents_between_the_largest_bf16_and_the_largest_fp32(tokens, sign):
+    """A_i x (and B_i^T dy) of (255/128)^2 2^126 + 3 2^119 = 3.99224853515625
+    2^126: finite in fp32 (24 bits hold it), but past the middle between the
+    largest bf16, 3.984375 2^126, and 2^128."""
+    t = torch_()
+    n, rank = 32, 8
+    big, latent = 255 / 128 * 2.0 ** 63, 3.99224853515625 * 2.0 ** 126
+    bf16 = lambda *shape: t.zeros(shape, dtype=t.bfloat16, device="cuda")
+    x, a, b, base = bf16(tokens, n), bf16(1, rank, n), bf16(1, n, rank), bf16(tokens, n)
+    x[:, 0], x[:, 1] = big, 2.0 ** 60
+    a[0, 0, 0], a[0, 0, 1] = sign * big, sign * 3 * 2.0 ** 59
+    b[0, :, 0] = 2.0 ** -100
+    ids = t.zeros(tokens, dtype=t.int32, device="cuda")
+    pool = lb.AdapterPool(a, b)
+    y = lb.adapters_forward(x, ids, [pool], bases=[base])[0]
+    assert bool((y.double() == sign * 4.0 * 2.0 ** 26).all())  # 3.99224853515625 in bf16
+    # db = dy v of one token with dy = 2^-100: exactly the latent over 2^100; the others' dy is zero
+    dy = bf16(tokens, n)
+    dy[0] = 2.0 ** -100
+    db = lb.adapters_backward(x, dy, ids, pool, want_dx=False)["db"]
+    assert bool((db[0, :, 0].double() == sign * latent * 2.0 ** -100).all())
+    # u = B^T dy of the same size: da = u x and dx = A^T u
+    pool = lb.AdapterPool(b.transpose(1, 2).contiguous(), a.transpose(1, 2).contiguous())
+    small = bf16(tokens, n)
+    small[0, 0] = 2.0 ** -100
+    out = lb.adapters_backward(small, x, ids, pool, dx_base=base)
+    assert bool((out["da"][0, 0, 0].double() == sign * latent * 2.0 ** -100).all())
+    assert bool((out["dx"].double() == sign * 4.0 * 2.0 ** 26).all())
+    assert lb.device_status() == lb.LB_OK
