@@ -32,8 +32,10 @@
 // For up to 128 + 48 tokens for each adapter of the pool, at most 512, or 24 for
 // each, at most kAdapterSmallTokens (2048); beyond, and for the backward pass, the
 // tcgen05 kernels of lb_adapters_mma.cu, whose tiles hold 128 tokens of one
-// adapter: they pay where an adapter has many tokens, and how many it has is
-// bounded by the pool.  Here and there, tokens spread over the pool: 8 adapters of
+// adapter: they pay where an adapter has many tokens.  The rule knows the tokens
+// and the pool's size, which the host has; where the forms cross depends on rank
+// and width too, and on how the tokens are spread, so that it is off by up to 1.7
+// times on either side of its border.  Here and there, tokens spread over the pool: 8 adapters of
 // rank 16, 4096 x 4096, 513 tokens 9.9 and 16.6 us, 1024 tokens 14.6 and 19.7; 64
 // of rank 16, 5120 to 7168 columns, 1024 tokens 34 and 82, 2048 tokens 57 and 83;
 // 32 of rank 128, 4096 x 4096, 768 tokens 38 and 39, 1024 tokens 46 and 40; 16 of

@@ -764,7 +764,7 @@ static lb_status check_heads(int64_t tokens, int64_t head_dim, int64_t rotary_di
     return LB_OK;
 }
 
-constexpr int64_t kMaxHeads = 4096, kMaxHeadsLd = int64_t(1) << 30;
+constexpr int64_t kMaxHeadsLd = int64_t(1) << 30;
 
 lb_status lb_heads_norm_rotate(int64_t tokens, int64_t head_dim, int64_t rotary_dim, lb_rotation rotation,
                                const int32_t *positions, const float *inv_freq, float eps, int ntensors,
@@ -782,7 +782,7 @@ lb_status lb_heads_norm_rotate(int64_t tokens, int64_t head_dim, int64_t rotary_
         const lb_heads &t = tensors[g];
         if (t.heads < 1 || !t.in || !t.out) return LB_ERR_INVALID_ARGUMENT;
         total += t.heads;
-        if (t.heads > kMaxHeads || total > kMaxHeads) return LB_ERR_UNSUPPORTED_SHAPE;
+        if (t.heads > lb::kMaxHeads || total > lb::kMaxHeads) return LB_ERR_UNSUPPORTED_SHAPE;
         if (t.ld_in > kMaxHeadsLd || t.ld_out > kMaxHeadsLd) return LB_ERR_UNSUPPORTED_SHAPE;
         if (t.ld_in < t.heads * head_dim || t.ld_out < t.heads * head_dim) return LB_ERR_INVALID_ARGUMENT;
         if (t.in == t.out && t.ld_in != t.ld_out) return LB_ERR_INVALID_ARGUMENT;
@@ -830,7 +830,7 @@ lb_status lb_heads_norm_rotate_backward(int64_t tokens, int64_t head_dim, int64_
         // `in` is read for the norm alone
         if (t.heads < 1 || (t.dweight && !t.weight)) return LB_ERR_INVALID_ARGUMENT;
         total += t.heads;
-        if (t.heads > kMaxHeads || total > kMaxHeads) return LB_ERR_UNSUPPORTED_SHAPE;
+        if (t.heads > lb::kMaxHeads || total > lb::kMaxHeads) return LB_ERR_UNSUPPORTED_SHAPE;
         sums = sums || t.dweight != nullptr;
         lb::HeadGroup &d = a.group[g];
         d.heads = (int)t.heads;

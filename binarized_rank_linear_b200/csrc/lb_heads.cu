@@ -520,7 +520,9 @@ cudaError_t dispatch_heads(const HeadsArgs &a, HeadsParams &p, const DeviceInfo 
 
 }  // namespace
 
-// A row of dw partials for each tensor of every CTA (there are at most 256 chunks of heads).
+// A row of dw partials for each tensor of every CTA.  A chunk has room for
+// kMaxCompute / 32 heads at least, so the CTAs' rows do not run out of it.
+static_assert((kMaxHeads + kMaxCompute / 32 - 1) / (kMaxCompute / 32) <= kMaxHeadCtas, "a CTA for each chunk of heads");
 size_t heads_backward_workspace_bytes(int head_dim)
 {
     return sizeof(float) * (size_t)kMaxHeadCtas * (size_t)kMaxHeadGroups * (size_t)head_dim;

@@ -259,7 +259,8 @@ cudaError_t adapters_forward(const AdaptersArgs &a, const DeviceInfo &dev, cudaS
 size_t adapters_backward_workspace_bytes(int tokens, int count, int rank);
 cudaError_t adapters_backward(const AdaptersBwdArgs &a, const DeviceInfo &dev, cudaStream_t stream);
 cudaError_t adapters_prepare_device(const DeviceInfo &dev);
-// More than kAdapterSmallTokens tokens, and the backward pass (lb_adapters_mma.cu).
+// Past the small batches (from 177 tokens on, where the pool has one adapter;
+// always past kAdapterSmallTokens), and the backward pass (lb_adapters_mma.cu).
 size_t adapters_mma_workspace_bytes(int tokens, int count, int nproj, const int *ranks);
 cudaError_t adapters_mma_forward(const AdaptersArgs &a, const DeviceInfo &dev, cudaStream_t stream);
 size_t adapters_mma_backward_workspace_bytes(int tokens, int count, int rank);
@@ -271,6 +272,7 @@ cudaError_t adapters_mma_prepare_device(const DeviceInfo &dev);
 // pass), already validated.  Forward: in -> out.  Backward: in, dout -> out
 // (the gradient of in) and dweight.
 constexpr int kMaxHeadGroups = LB_MAX_SIBLINGS;
+constexpr int kMaxHeads = 4096;     // of a call's tensors together
 constexpr int kMaxHeadCtas = 1024;  // most rows of dweight partials
 struct HeadGroup {
     const uint16_t *in, *dout, *weight;

@@ -179,3 +179,19 @@ def test_attention_inputs_together(tokens):
     for name, e, w in zip(("dx", "da", "db"), exact, tol):
         ref.within(out[name], e, w, name)
     assert lb.device_status() == lb.LB_OK
+
+
+def test_the_most_heads_in_the_narrowest_chunks():
+    """4096 heads of 136: 12 to a chunk, 342 chunks, and dweight from all of them."""
+    t = torch_()
+    tokens, d = 7, 136
+    g, rot, pos, xs, ws = make(tokens, [4000, 96], d, 64, "halves", [True, True], 3, 9)
+    douts = [normal(g, *x.shape) for x in xs]
+    outs = lb.heads_norm_rotate(xs, pos, rot, weights=ws)
+    got = lb.heads_norm_rotate_backward(xs, douts, pos, rot, weights=ws)
+    assert lb.device_status() == lb.LB_OK
+    for x, dy, w, y, o in zip(xs, douts, ws, outs, got):
+        ref.within(y, *ref.heads(x, pos, rot.inv_freq, "halves", w, rot.eps, d), "out")
+        (din, dw), (tx, tw) = ref.heads_backward(x, dy, pos, rot.inv_freq, "halves", w, rot.eps, d)
+        ref.within(o["din"], din, tx, "din")
+        ref.within(o["dweight"], dw, tw, "dweight")

@@ -317,3 +317,19 @@ def test_latents_between_the_largest_bf16_and_the_largest_fp32(tokens, sign):
     assert bool((out["da"][0, 0, 0].double() == sign * latent * 2.0 ** -100).all())
     assert bool((out["dx"].double() == sign * 4.0 * 2.0 ** 26).all())
     assert lb.device_status() == lb.LB_OK
+
+
+@pytest.mark.parametrize("tokens,n_in,n_out,rank", [(3, 1 << 20, 64, 16), (3, 64, 1 << 20, 128), (200, 1 << 20, 64, 8),
+                                                    (200, 64, 1 << 20, 8)])
+def test_the_widest_rows(tokens, n_in, n_out, rank):
+    g = gen(tokens + rank)
+    x, dy = normal(g, tokens, n_in), normal(g, tokens, n_out)
+    ids, pool = make_ids(g, tokens, 2, "some"), make_pool(g, 1, rank, n_in, n_out)
+    ids[ids == 1] = -1
+    y = lb.adapters_forward(x, ids, [pool], bases=[dy])[0]
+    check_forward(x, ids, [pool], [dy], [y], "wide")
+    out = lb.adapters_backward(x, dy, ids, pool, dx_base=x)
+    assert lb.device_status() == lb.LB_OK
+    exact, tol = ref.adapters_backward(x, dy, ids, pool.a, pool.b, pool.scale, None, x)
+    for name, e, w in zip(("dx", "da", "db"), exact, tol):
+        ref.within(out[name], e, w, name)
