@@ -47,7 +47,7 @@
 #include <cuda_runtime.h>
 
 #include "lb_common.cuh"
-#include "lb_internal.h"
+#include "lb_operators.h"
 
 namespace lb {
 namespace {

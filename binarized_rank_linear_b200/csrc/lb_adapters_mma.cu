@@ -52,7 +52,7 @@
 #include <cuda_runtime.h>
 
 #include "lb_common.cuh"
-#include "lb_internal.h"
+#include "lb_operators.h"
 #include "lb_tc.cuh"
 
 namespace lb {

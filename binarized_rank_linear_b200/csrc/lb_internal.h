@@ -23,6 +23,17 @@ struct DeviceInfo {
     int pair_slots = 0;      // CTA pairs of the prefill pair kernels resident at once
 };
 
+// DeviceInfo of the current device, set up on the first call for it.
+lb_status device_info(DeviceInfo *out);
+// The set-up of the operators beside the projection (lb_api_operators.cu).
+cudaError_t operators_prepare_device(const DeviceInfo &dev);
+
+// ----------------------------------------------------------------- arguments
+constexpr int64_t kMaxDim = int64_t(1) << 20;  // n_in, n_out
+constexpr int64_t kMaxTokens = int64_t(1) << 24;
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 // ----------------------------------------------------------------- packing
 cudaError_t pack_signs_launch(const void *src, lb_dtype dtype, lb_factor kind, int64_t rows, int64_t cols,
                               int64_t src_ld, uint32_t *dst, int64_t dst_ld, cudaStream_t stream);
@@ -215,83 +226,6 @@ struct BackwardArgs {
 };
 size_t backward_workspace_bytes(int tokens, int n_in, int n_out, const int *ranks, int npaths);
 cudaError_t backward_launch(const BackwardArgs &b, const DeviceInfo &dev, cudaStream_t stream);
-
-// ---------------------------------------------------------------- adapters (lb_adapters.cu)
-// Low-rank adapters of many requests (lb_adapters_forward, _backward),
-// already validated.
-constexpr int kMaxAdapters = LB_MAX_ADAPTERS;
-constexpr int kAdapterSmallTokens = LB_ADAPTERS_SMALL_TOKENS;
-struct AdapterProj {
-    const uint16_t *a, *b;
-    const float *scale;
-    const int32_t *ranks;
-    int rank, n_out;
-    const uint16_t *base;  // never null: y itself for an update in place
-    int64_t ldbase;
-    uint16_t *y;
-    int64_t ldy;
-};
-struct AdaptersArgs {
-    const uint16_t *x;
-    int64_t ldx;
-    const int32_t *ids;
-    int tokens, n_in, count, nproj;
-    AdapterProj proj[kMaxSiblings];
-    void *workspace;
-};
-struct AdaptersBwdArgs {
-    const uint16_t *x, *dy;
-    int64_t ldx, lddy;
-    const int32_t *ids;
-    int tokens, n_in, n_out, count, rank;
-    const uint16_t *a, *b;
-    const float *scale;
-    const int32_t *ranks;
-    const uint16_t *dx_base;  // dx itself for an update in place
-    int64_t lddxbase;
-    uint16_t *dx;  // may be null
-    int64_t lddx;
-    float *da, *db;
-    void *workspace;
-};
-size_t adapters_workspace_bytes(int tokens, int n_in, int count, int nproj, const int *ranks);
-cudaError_t adapters_forward(const AdaptersArgs &a, const DeviceInfo &dev, cudaStream_t stream);
-size_t adapters_backward_workspace_bytes(int tokens, int count, int rank);
-cudaError_t adapters_backward(const AdaptersBwdArgs &a, const DeviceInfo &dev, cudaStream_t stream);
-cudaError_t adapters_prepare_device(const DeviceInfo &dev);
-// Past the small batches (from 177 tokens on, where the pool has one adapter;
-// always past kAdapterSmallTokens), and the backward pass (lb_adapters_mma.cu).
-size_t adapters_mma_workspace_bytes(int tokens, int count, int nproj, const int *ranks);
-cudaError_t adapters_mma_forward(const AdaptersArgs &a, const DeviceInfo &dev, cudaStream_t stream);
-size_t adapters_mma_backward_workspace_bytes(int tokens, int count, int rank);
-cudaError_t adapters_mma_backward(const AdaptersBwdArgs &a, const DeviceInfo &dev, cudaStream_t stream);
-cudaError_t adapters_mma_prepare_device(const DeviceInfo &dev);
-
-// ---------------------------------------------------------------- heads (lb_heads.cu)
-// Per-head norm and position rotation (lb_heads_norm_rotate and its backward
-// pass), already validated.  Forward: in -> out.  Backward: in, dout -> out
-// (the gradient of in) and dweight.
-constexpr int kMaxHeadGroups = LB_MAX_SIBLINGS;
-constexpr int kMaxHeads = 4096;     // of a call's tensors together
-constexpr int kMaxHeadCtas = 1024;  // most rows of dweight partials
-struct HeadGroup {
-    const uint16_t *in, *dout, *weight;
-    int64_t ld_in, ld_dout, ld_out;
-    uint16_t *out;
-    float *dweight;
-    int heads;
-};
-struct HeadsArgs {
-    HeadGroup group[kMaxHeadGroups];
-    int ngroups, tokens, head_dim, rotary_dim, pairs;
-    const int32_t *positions;
-    const float *inv_freq;
-    float eps;
-};
-size_t heads_backward_workspace_bytes(int head_dim);
-cudaError_t heads_forward(const HeadsArgs &a, const DeviceInfo &dev, cudaStream_t stream);
-cudaError_t heads_backward(const HeadsArgs &a, float *workspace, const DeviceInfo &dev, cudaStream_t stream);
-cudaError_t heads_prepare_device(const DeviceInfo &dev);
 
 // Either contraction alone, the latent in caller memory: z fp16 [tokens][ldz]
 // (token-major, the paths side by side, path 0 first); any number of tokens
