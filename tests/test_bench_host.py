@@ -164,3 +164,9 @@ def test_rotation_spans_twice_l2():
             assert n * set_bytes > 2 * bench.L2_BYTES
     assert bench.rotation_size(2150400, min_sets=1024) == 1024
     assert bench.rotation_size(10 ** 9, min_sets=1024) == 4   # capped by 4 GB of weights
+
+
+@pytest.mark.parametrize("config,tokens", [("llama2_7b_q", 1), ("qwen3_14b_gate", 8192)])
+def test_the_committed_dram_figures_are_of_this_code(config, tokens):
+    """A change to the sources of these calls takes the figures anew."""
+    assert bench.load_traffic(config, tokens) > 0
