@@ -100,22 +100,22 @@ struct Finding {
     uint8_t place[kAdapterSmallTokens];           // among its warp's tokens of the bin
     uint32_t sums[kWarps];
 };
+// A token's adapter, -1 for none, and the rank of an adapter.
+__device__ __forceinline__ int adapter_of(const SmallParams &p, int t)
+{
+    const int id = __ldcg(p.ids + t);
+    return id >= p.count ? -1 : max(id, -1);
+}
+__device__ __forceinline__ uint8_t rank_of(const AdapterProj &P, int id)
+{
+    return (uint8_t)(id < 0 ? 0 : P.ranks == nullptr ? P.rank : max(0, min(P.rank, __ldcg(P.ranks + id))));
+}
 // Each warp takes a run of tokens, 32 at a time: those of one bin find each other
 // (match), the table has how many came before them.
 __device__ __forceinline__ int find_groups(const SmallParams &p, Groups &g, Finding &f)
 {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, bins = p.count + 1;
-    auto id_of = [&](int t) {
-        int id = __ldcg(p.ids + t);
-        if (id >= p.count) {
-            if (blockIdx.x == 0) set_status(p.status, LB_ERR_INVALID_ARGUMENT);
-            id = -1;
-        }
-        return max(id, -1);
-    };
-    auto rank_of = [&](const AdapterProj &P, int id) {
-        return (uint8_t)(id < 0 ? 0 : P.ranks == nullptr ? P.rank : max(0, min(P.rank, __ldcg(P.ranks + id))));
-    };
+    auto id_of = [&](int t) { return adapter_of(p, t); };
     if (p.tokens == 1) {  // every thread has its id
         const int id = id_of(0);
         if (tid < p.nproj) g.rank[tid][0] = rank_of(p.proj[tid], id);
@@ -213,6 +213,24 @@ __device__ __forceinline__ int find_groups(const SmallParams &p, Groups &g, Find
     return n;
 }
 
+// Whether ids and ranks still give what find_groups made of them.
+__device__ __forceinline__ bool still_so(const SmallParams &p, const Groups &g, const Finding &f, int groups)
+{
+    bool same = true;
+    if (p.tokens == 1) {
+        same = adapter_of(p, 0) == g.ids[0];
+    } else {
+#pragma unroll 1
+        for (int t = threadIdx.x; t < p.tokens; t += kThreads) same = same && adapter_of(p, t) + 1 == f.bin[t];
+    }
+#pragma unroll 1
+    for (int i = threadIdx.x; i < groups * p.nproj; i += kThreads) {
+        const int j = i / groups, k = i - j * groups;
+        same = same && rank_of(p.proj[j], g.ids[k]) == g.rank[j][k];
+    }
+    return same;
+}
+
 // d += A B of 16 rows (tokens), 8 columns and 16 k.  A lane holds of A the rows
 // lane / 4 and lane / 4 + 8, of B the column lane / 4, of d those rows and the
 // columns 2 (lane % 4) and the next; of k each lane % 4 has four.
@@ -247,20 +265,13 @@ __global__ void __launch_bounds__(kThreads, kShrinkCtas) small_shrink_kernel(con
         float red[2][kWarps][kGroup][kRows + 2];
     } scratch;
     auto &red = scratch.red;
-    // ids and the pools may have been written by the work ahead on the stream,
-    // which may have let this launch start early: none of it is read before the
-    // wait.  (Reading them ahead of it, while the projection's last launch ends,
-    // took 1.0 us less of 12.3 for q, k, v of 4096 columns with adapters of rank 16
-    // and the heads after them at 1 token, and 1.7 of 26 at 32 tokens.)
-    pdl_wait();
-    pdl_launch_dependents();
-    const int groups = find_groups(p, grp, scratch.f);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int kw = warp * kWarpCols + 8 * (lane & 3);
     const int t0 = lane >> 2, t1 = t0 + 8;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     constexpr int kSteps = kWarpCols / 32;
-    const int blocks = p.row0[p.nproj], units = groups * blocks * p.slices;
+    const int blocks = p.row0[p.nproj];
+    int groups, units;
     // the next unit from `unit` on that has something to do; its place
     int g, j, r0, slice, rank;
     auto find = [&](int unit) {
@@ -288,8 +299,25 @@ __global__ void __launch_bounds__(kThreads, kShrinkCtas) small_shrink_kernel(con
             w[s][1] = in && row + 8 < rank ? ld_early_v4(a + (int64_t)8 * p.n_in + 32 * s) : zero;
         }
     };
-    int unit = find(blockIdx.x);
-    if (unit < units) load();
+    // The work ahead on the stream may have let this launch start while it still
+    // writes ids, ranks or the pools.  The groups are found from what is there, and
+    // again after the wait for that work where ids or ranks have changed; nothing
+    // else is read before it.  (100 tokens, 16 adapters of rank 32, 5120 to 2 x 17408
+    // columns, passes one behind the other: 20.9 us; 21.9 with the groups found after
+    // the wait, 19.4 with A read ahead of it, which would be the old A.)
+    int unit;
+#pragma unroll 1
+    for (bool again = false;; again = true) {
+        groups = find_groups(p, grp, scratch.f);
+        units = groups * blocks * p.slices;
+        unit = find(blockIdx.x);
+        if (!again) {
+            pdl_wait();
+            pdl_launch_dependents();
+        }
+        if (unit < units) load();
+        if (again || !__syncthreads_or(!still_so(p, grp, scratch.f, groups))) break;
+    }
     for (int turn = 0; unit < units; turn ^= 1) {
         const int n = grp.size[g], k0 = slice * kSlice + kw;
         const uint16_t *tok = grp.order + grp.start[g];
@@ -347,6 +375,9 @@ __global__ void __launch_bounds__(kThreads, expand_ctas(KS)) small_expand_kernel
     constexpr int kAtOnce = 8;  // partials a thread asks for at once
     // shrink let this launch start after its own wait: what is older is complete
     const int groups = find_groups(p, grp, scratch.f);
+    if (blockIdx.x == 0)
+        for (int t = threadIdx.x; t < p.tokens; t += kThreads)
+            if (__ldcg(p.ids + t) >= p.count) set_status(p.status, LB_ERR_INVALID_ARGUMENT);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane >> 2, q = lane & 3;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     const int chunks = p.chunk0[p.nproj], units = groups * chunks;

@@ -166,3 +166,29 @@ def test_ids_past_the_pool_that_are_written_over_in_time(early_copy, tokens):
     assert t.equal(y[tokens // 2], base[tokens // 2])
     y[tokens // 2] = want[tokens // 2]
     assert t.equal(y, want)
+
+
+@pytest.mark.parametrize("tokens,count", [(2, 5), (17, 64), (100, 16), (368, 5), (1500, 64), (2048, 1000)])
+def test_small_batches_behind_an_early_writer(early_copy, tokens, count):
+    """What the groups of tokens were found from before it was written."""
+    t = torch_()
+    g = gen(67)
+    n_in, outs = 2080, [288, 64]
+    ranks = [(7 * i) % 17 for i in range(count)]
+    pools = [make_pool(g, count, 16, n_in, o, ranks) for o in outs]
+    x, bases = normal(g, tokens, n_in), [normal(g, tokens, o) for o in outs]
+    ids = t.randint(-1, count, (tokens,), generator=g, device="cuda").to(t.int32)
+    ids[0], ids[1] = 1, 0
+    ys = [t.empty_like(b) for b in bases]
+    fields = dict(ids=ids, ranks=pools[1].ranks, a=pools[0].a, b=pools[1].b, x=x, base=bases[1])
+    behind(early_copy, fields, lambda: lb.adapters_forward(x, ids, pools, bases=bases, ys=ys), "forward")
+    # from all tokens without an adapter to all of one, and back
+    for old, new in ((-1, 1), (1, -1)):
+        ids.fill_(new)
+        want = [y.clone() for y in lb.adapters_forward(x, ids, pools, bases=bases)]
+        late = ids.clone()
+        ids.fill_(old)
+        t.cuda.synchronize()
+        early_copy(ids, late)
+        got = lb.adapters_forward(x, ids, pools, bases=bases)
+        assert all(t.equal(a, b) for a, b in zip(got, want))
