@@ -21,27 +21,31 @@
 // groups for itself, once, and takes its units one after the other, the next one's
 // weights asked for before the last is written; in expand a CTA's units are a run,
 // so that v is put together once for many of them.
-// Measured, both launches, operands not in L2: 1 token and three projections of
-// 4096 x 4096, rank 16, 3.9 us; 100 tokens, 16 adapters of rank 32, 5120 to 2 x
-// 17408 columns, 19.1 us, 3.2 TB/s (60 us with fp32 FMAs, a thread a row of B: most
-// of it spent unpacking and on 16-byte pieces of 32 rows at a time; 36 us with the
-// products but a CTA a unit: most of it spent finding groups, one wave of CTAs
-// after the other; 20.5 us with the units dealt out in turn); 128 tokens, 32
-// adapters of rank 128, 4096 x 4096, 19 us, 3.6 TB/s.  What is left is the chain of each unit: partials, split, product, store.
+// Measured, both launches, operands not in L2, one pass behind the other: 1 token
+// and three projections of 4096 x 4096, rank 16, 4.8 us; 100 tokens, 16 adapters of
+// rank 32, 5120 to 2 x 17408 columns, 20.9 us, 2.9 TB/s (60 us with fp32 FMAs, a
+// thread a row of B: most of it spent unpacking and on 16-byte pieces of 32 rows at
+// a time; 36 us with the products but a CTA a unit: most of it spent finding
+// groups, one wave of CTAs after the other; 1.4 us more with the units dealt out in
+// turn); 128 tokens, 32 adapters of rank 128, 4096 x 4096, 22 us, 3.1 TB/s.  What is
+// left is the chain of each unit: partials, split, product, store.
 //
 // For up to 128 + 48 tokens for each adapter of the pool, at most 512, or 24 for
 // each, at most kAdapterSmallTokens (2048); beyond, and for the backward pass, the
 // tcgen05 kernels of lb_adapters_mma.cu, whose tiles hold 128 tokens of one
 // adapter: they pay where an adapter has many tokens.  The rule knows the tokens
 // and the pool's size, which the host has; where the forms cross depends on rank
-// and width too, and on how the tokens are spread, so that it is off by up to 1.7
-// times on either side of its border.  Here and there, tokens spread over the pool: 8 adapters of
-// rank 16, 4096 x 4096, 513 tokens 9.9 and 16.6 us, 1024 tokens 14.6 and 19.7; 64
-// of rank 16, 5120 to 7168 columns, 1024 tokens 34 and 82, 2048 tokens 57 and 83;
-// 32 of rank 128, 4096 x 4096, 768 tokens 38 and 39, 1024 tokens 46 and 40; 16 of
-// rank 32, 5120 to 34816, 513 tokens 44 and 55, 768 tokens 59 and 56; 4 of rank 64,
-// 4096 to 11008, 400 tokens 19.1 and 19.3, 513 tokens 24 and 21; 1 of rank 64, 4096
-// to 28672, 128 tokens 14.1 and 15.6, 200 tokens 20 and 19.
+// and width too, and on how the tokens are spread, so that near its border it takes
+// the slower form by up to 1.6 times.  Here and there (the small form with the
+// groups found behind the wait, up to 3 us more than it takes now), tokens spread
+// over the pool: 8 adapters of rank 16, 4096 x 4096, 256 tokens 9.7 and 18.6 us, 513
+// tokens 13.5 and 19.3, 1024 tokens 19.6 and 23.7, 2048 tokens 32.6 and 29.3; 64 of
+// rank 16, 5120 to 7168 columns, 1024 tokens 41 and 86, 1537 tokens 54 and 87; 32 of
+// rank 128, 4096 x 4096, 768 tokens 43 and 42, 1024 tokens 51 and 44; 16 of rank 32,
+// 5120 to 34816, 513 tokens 49 and 57, 768 tokens 65 and 58; 4 of rank 64, 4096 to
+// 11008, 400 tokens 23 and 22, 513 tokens 28 and 24; 1 of rank 64, 4096 to 28672,
+// 128 tokens 18.3 and 18.8, 200 tokens 24 and 21.  All tokens of one adapter of the
+// 64: 512 tokens 18 and 21, 1536 tokens 41 and 30.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>

@@ -39,13 +39,13 @@
 // older: each of them, and plan, lets the next begin only after its own wait, so
 // that all launches but the last one are complete, whatever came before plan.  In
 // the backward pass wgrad goes before expand, and expand, which needs nothing of
-// it, begins on the SMs that wgrad leaves.  Measured on the device, alone and at
-// full clocks, 8192 tokens of 5120 columns, 8 adapters of rank 64: forward to 5120
-// columns 60 us (plan 4 us past the launch before; shrink 23, 3.7 TB/s; finish 3;
-// expand 30, 5.6 TB/s over the base read and y written), backward from 17408
-// columns, 4 adapters, 192 us (shrink 72 us, 5.1 TB/s; wgrad 74, 5.0 TB/s; expand
-// 30; finish 3 and 10).  333 tokens, 3 adapters of rank 8, 4096 x 4096, backward
-// 25 us: six launches of 3 to 6 us, each a chain of reads that depend on one
+// it, begins on the SMs that wgrad leaves.  Measured on the device, passes one
+// behind the other, 8192 tokens of 5120 columns, 8 adapters of rank 64: forward to
+// 5120 columns 67 us (of it shrink 23, 3.7 TB/s; finish 3; expand 30, 5.6 TB/s over
+// the base read and y written; 63 with plan's counting ahead of its wait), backward
+// from 17408 columns, 4 adapters, 198 us (shrink 72 us, 5.1 TB/s; wgrad 74, 5.0
+// TB/s; expand 30; finish 3 and 10).  333 tokens, 3 adapters of rank 8, 4096 x 4096,
+// backward 26 us: six launches of 3 to 6 us, each a chain of reads that depend on one
 // another.
 #include <algorithm>
 #include <cstdint>
@@ -341,7 +341,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint16_t *src, bool t
 // on, 16 bytes at chunk tid % 8, in the layout of a TMA box.  The rows' addresses
 // are found once, so that a copy is an addition and the copy itself: with a
 // multiplication in each, four warps could not keep up with a weight gradient
-// (the backward pass of 8192 tokens in any order, 276 us; 235 us so).  Rows that are not `there` are not read
+// (the backward pass of 8192 tokens in any order, 276 us; 236 us so).  Rows that are not `there` are not read
 // (`strict`: zeros).
 template <int ROWS>
 struct Copier {
@@ -410,8 +410,8 @@ __device__ __forceinline__ int used_rank(const int32_t *ranks, int rank, int ada
 // each: CTA c has start(c) .. start(c + 1) - 1.
 // Shrink takes 4 or more: sums that a CTA shares cost a read and a write of them.
 // A weight gradient has few K-blocks where there are few tokens, and one each
-// spreads its products: 30 tokens, 2 adapters, 34 us at 4 and 26 us at 1; 148
-// tokens, 4 adapters of rank 64, 43 and 33 us.
+// spreads its products: at 4 instead of 1, 30 tokens of 2 adapters took 8 us more,
+// 148 tokens of 4 adapters of rank 64 10 us more.
 constexpr int kLeastBlocks = 4;
 struct Shares {
     int ctas, base, rem;

@@ -18,7 +18,7 @@
 // of a rotated pair in the same lane (so the rotation needs no exchange, and the
 // norm's sum is a shuffle tree), the head's weights in registers, 16 elements a
 // lane where the sizes allow it, else 8.  For 8192 tokens of 40 + 8 heads of
-// 128: 35 us forward (5.7 TB/s), 61 us backward (4.9 TB/s).  (A CTA a token: 63 us
+// 128: 36 us forward (5.6 TB/s), 62 us backward (4.9 TB/s).  (A CTA a token: 63 us
 // forward; CTAs that stay, with the next tokens in registers, 41 us forward and 86
 // us backward; 8 elements a lane on twice the threads, 67 us backward, 16 on twice
 // the threads 74.)
